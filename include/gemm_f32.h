@@ -76,6 +76,10 @@ extern "C" {
 #define GEMM_F32_ERR_WORKSPACE      10  /* workspace smaller than required            */
 #define GEMM_F32_ERR_INVALID_FORMAT 11  /* 16-bit input format unknown                */
 #define GEMM_F32_ERR_SCRATCH        12  /* partials would exceed the fixed scratch      */
+#define GEMM_F32_ERR_INVALID_TYPE   13  /* a stored type the entry point does not take */
+#define GEMM_F32_ERR_INVALID_ACTIVATION 14 /* activation unknown                       */
+#define GEMM_F32_ERR_INVALID_EPILOGUE 15 /* an epilogue field its mode does not take   */
+#define GEMM_F32_ERR_INVALID_SCALAR 16  /* eps, a coefficient or a step count out of range */
 
 /* Kernel ladder.  Each rung computes the same product; each is tested against
  * the oracle and against the rung below it.
@@ -461,6 +465,141 @@ int gemm_mixed_default_variant(int64_t M, int64_t N, int64_t K);
 int gemm_mixed_op(int op_a, int op_b, int format, int64_t M, int64_t N, int64_t K,
                   const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
                   float *C, int64_t ldc, void *stream);
+
+/* Stored types of the entry points below: the 16-bit formats' numbers, and
+ * binary32. */
+#define GEMM_MIXED_F32 2
+
+/* Activations. */
+#define GEMM_ACT_NONE      0
+#define GEMM_ACT_RELU      1  /* max(z, 0), NaN stays NaN; derivative 0 at 0            */
+#define GEMM_ACT_GELU      2  /* z Phi(z), Phi the normal distribution function         */
+#define GEMM_ACT_GELU_TANH 3  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2         */
+#define GEMM_ACT_SILU      4  /* z / (1 + e^-z)                                         */
+
+/* What a product's entries pass through before they are stored.
+ *   gradient == 0, the layer's forward pass:
+ *     Z = op(A) op(B) + bias          (bias added to every row)
+ *     C = act(Z) + residual
+ *     preact, if not NULL, receives Z rounded to the factors' format
+ *   gradient == 1, the backward pass through an activation that comes before
+ *   the product in the network:
+ *     C = (op(A) op(B) + residual) * act'(Z), Z read from preact
+ *     bias_grad, if not NULL, receives the N column sums of C, added in
+ *     binary32 before C's rounding, in a fixed order
+ * Fields: */
+typedef struct gemm_epilogue {
+    int c_type;           /* type of C and residual: the factors' format or GEMM_MIXED_F32  */
+    int activation;       /* GEMM_ACT_*                                                     */
+    int gradient;         /* 0 or 1                                                         */
+    int bias_type;        /* type of bias: the factors' format or GEMM_MIXED_F32            */
+    const void *bias;     /* N values, or NULL; NULL in gradient mode                       */
+    const void *residual; /* M x N, or NULL; may be C itself (same pointer, leading dimension) */
+    int64_t ld_residual;  /* >= max(1, N) where residual is set                             */
+    void *preact;         /* M x N of the factors' format, or NULL; needed in gradient mode
+                             unless the activation is GEMM_ACT_NONE                         */
+    int64_t ld_preact;    /* >= max(1, N) where preact is used                              */
+    float *bias_grad;     /* N sums, or NULL; NULL in forward mode                          */
+} gemm_epilogue;
+
+/* The 16-bit product with its epilogue: the fully connected layer of the
+ * same deep-learning chapter ("FC Layer = GEMM", "Backward") without a
+ * binary32 product in memory between its steps.
+ *   op_a, op_b, format, M, N, K, A, lda, B, ldb   as for gemm_mixed_op; any
+ *            alignment of 2 bytes and any leading dimension are taken
+ *   C        M x N of epilogue->c_type, element (i, j) at C[i*ldc + j];
+ *            aligned to its type's size, as are bias, residual and preact
+ *   workspace, workspace_bytes   device memory of at least
+ *            gemm_mixed_epilogue_workspace_size() bytes for the same
+ *            arguments (NULL allowed when that is 0), 16-byte aligned, owned
+ *            by the caller until the call has run; contents undefined after
+ *            it.  Two calls that may overlap need a workspace each.
+ * Products and sums are accumulated in binary32 and every stored value is
+ * rounded once.  C must not overlap A, B or preact, nor residual unless it
+ * is residual.  K == 0 leaves a product of zeros to the epilogue; M == 0
+ * writes +0 to bias_grad; N == 0 is a no-op.  Statuses as for gemm_mixed,
+ * with GEMM_F32_ERR_INVALID_TYPE, _ACTIVATION and _EPILOGUE for the
+ * epilogue's fields and GEMM_F32_ERR_WORKSPACE.  Enqueue-only on `stream`;
+ * calls no allocator and may be captured into a graph. */
+int64_t gemm_mixed_epilogue_workspace_size(int op_a, int op_b, int format, int64_t M, int64_t N, int64_t K,
+                                           const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
+                                           const gemm_epilogue *epilogue);   /* bytes; -1 if invalid */
+int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, int64_t N, int64_t K,
+                        const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
+                        void *C, int64_t ldc, const gemm_epilogue *epilogue,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+
+/* The gradient mode without a product, for a gradient dY that is already
+ * there: dZ = dY * act'(Z), and the bias gradient, dZ's column sums.
+ *   format      GEMM_MIXED_BF16 or GEMM_MIXED_F16, of dY, preact and dZ
+ *   dY          M x N, ld_dy >= max(1, N)
+ *   preact      Z, M x N, ld_preact >= max(1, N); may be NULL if the
+ *               activation is GEMM_ACT_NONE
+ *   dZ          M x N, ld_dz >= max(1, N), may be dY itself, or NULL for the
+ *               sums alone
+ *   bias_grad   N binary32 sums (of dZ before its rounding, in a fixed
+ *               order), or NULL; needs the workspace
+ * Rules as for gemm_mixed_epilogue. */
+int64_t activation_grad_workspace_size(int64_t M, int64_t N);   /* bytes; -1 if invalid */
+int activation_grad(int activation, int format, int64_t M, int64_t N, const uint16_t *dY, int64_t ld_dy,
+                    const uint16_t *preact, int64_t ld_preact, uint16_t *dZ, int64_t ld_dz, float *bias_grad,
+                    void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Layer norm over the rows of a rows x cols matrix (cols >= 1).
+ *   mean = <x>, rstd = 1 / sqrt(<(x - mean)^2> + eps), <.> over a row
+ *   y = (x - mean) rstd gamma + beta
+ *   type         of x and y: GEMM_MIXED_BF16, _F16 or _F32
+ *   x, y         element (r, c) at x[r*ldx + c], ldx >= cols; y may be x
+ *   gamma, beta  cols values of param_type (any of the three), or NULL (1, 0)
+ *   eps          >= 0, finite
+ *   mean, rstd   rows binary32 values for the backward pass, or NULL
+ * Statistics are binary32; the variance is the mean of the squared
+ * deviations.  rows == 0 is a no-op.  Statuses, streams and alignment (each
+ * pointer to its type's size) as above. */
+int layer_norm(int type, int64_t rows, int64_t cols, const void *x, int64_t ldx, int param_type, const void *gamma,
+               const void *beta, float eps, void *y, int64_t ldy, float *mean, float *rstd, void *stream);
+
+/* Its backward pass, with xhat = (x - mean) rstd and g = dy gamma:
+ *   dx     = rstd (g - <g> - xhat <g xhat>) + residual_grad
+ *   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
+ *   dy, x, dx      of type, with leading dimensions >= cols; dx may be dy or
+ *                  residual_grad
+ *   mean, rstd     as the forward pass wrote them
+ *   gamma          cols values of param_type, or NULL (1)
+ *   residual_grad  the gradient that reaches x past the layer, of type, or NULL
+ *   dgamma, dbeta  cols binary32 sums, added in a fixed order, or NULL;
+ *                  +0 when rows == 0
+ *   workspace      as for gemm_mixed_epilogue */
+int64_t layer_norm_backward_workspace_size(int type, int64_t rows, int64_t cols);   /* bytes; -1 if invalid */
+int layer_norm_backward(int type, int64_t rows, int64_t cols, const void *dy, int64_t lddy, const void *x,
+                        int64_t ldx, const float *mean, const float *rstd, int param_type, const void *gamma,
+                        const void *residual_grad, int64_t ld_residual, void *dx, int64_t lddx, float *dgamma,
+                        float *dbeta, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Orthogonalisation of `batch` rows x cols matrices by Newton-Schulz
+ * products (the update step of the Muon optimiser).  Per matrix,
+ *   X <- G / (|G|_F + eps), then `steps` times
+ *   X <- a X + (b S + c S^2) X with S = X X^T          (rows <= cols)
+ *   X <- a X + X (b S + c S^2) with S = X^T X          (rows > cols)
+ * so that every singular value s of X goes to a s + b s^3 + c s^5.
+ *   type        of G and out: GEMM_MIXED_BF16, _F16 or _F32
+ *   G           matrix z's element (r, c) at G[z*stride_g + r*ldg + c], ldg >=
+ *               cols, stride_g >= 0
+ *   out         likewise with ldo, stride_o; matrices must not overlap
+ *               (stride_o >= (rows - 1) ldo + cols when batch > 1); may be G
+ *               with the same strides
+ *   steps       0 .. 100
+ *   a, b, c     finite; refused (GEMM_F32_ERR_INVALID_SCALAR) if singular
+ *               values of at most 1 could pass 2^40 within the steps
+ *   eps         >= 0, finite; with eps > 0 a matrix of zeros gives zeros
+ *   workspace   of newton_schulz_workspace_size() bytes, as for
+ *               gemm_mixed_epilogue
+ * A matrix with a NaN or an infinity gives NaN throughout; the other
+ * matrices of the batch do not see it.  Statuses as above. */
+int64_t newton_schulz_workspace_size(int type, int64_t batch, int64_t rows, int64_t cols);   /* bytes; -1 if invalid */
+int newton_schulz(int type, int64_t batch, int64_t rows, int64_t cols, const void *G, int64_t ldg, int64_t stride_g,
+                  int steps, float a, float b, float c, float eps, void *out, int64_t ldo, int64_t stride_o,
+                  void *workspace, int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

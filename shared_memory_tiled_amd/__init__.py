@@ -18,6 +18,10 @@ _BINDING_NAMES = {
     "gemm_mixed", "gemm_mixed_variant", "gemm_mixed_op", "gemm_mixed_num_variants", "gemm_mixed_variant_name",
     "gemm_f32_default_variant", "gemm_mixed_default_variant", "transpose_f32_default_variant",
     "gemm16", "FORMATS",
+    "gemm_mixed_epilogue", "gemm_mixed_epilogue_workspace_size", "epilogue", "activation_grad",
+    "activation_grad_workspace_size", "linear", "linear_grad", "linear_backward", "activation_backward",
+    "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_size",
+    "newton_schulz", "newton_schulz_workspace_size", "NEWTON_SCHULZ_COEFFICIENTS", "ACTIVATIONS", "TYPES",
     "VARIANTS", "load_library", "library_path",
 }
 

@@ -7,6 +7,7 @@
 // (PMPP chapter 5 notes, section 5.4): with K = 0 there are no phases and
 // every output is the initial +0; with M = 0 or N = 0 there is no output.
 #include "gemm_f32.h"
+#include "api_checks.h"
 #include "launch.h"
 
 #include <limits.h>
@@ -58,16 +59,6 @@ constexpr int kNumDiagnostics = (int)(sizeof(kDiagnostics) / sizeof(kDiagnostics
 
 const char* const kRungNames[kNumRungs] = {
     "naive16x16", "tiled32_pad4", "regblock128x128_bk8_padA4", "mfma_auto"};
-
-bool misaligned(const void* ptr) { return ((uintptr_t)ptr & 3u) != 0; }
-
-// (rows - 1) * ld + cols must be addressable with 64-bit element offsets.
-bool extent_fits(int64_t rows, int64_t cols, int64_t ld) {
-    if (rows == 0 || cols == 0) return true;
-    int64_t last;
-    if (__builtin_mul_overflow(rows - 1, ld, &last)) return false;
-    return !__builtin_add_overflow(last, cols, &last);
-}
 
 // op_a / op_b: 0 = the factor as stored, 1 = its transpose (A stored K x M,
 // B stored N x K).
@@ -181,10 +172,15 @@ extern "C" const char* gemm_f32_status_string(int status) {
         case GEMM_F32_ERR_LAUNCH: return "kernel launch rejected by the HIP runtime";
         case GEMM_F32_ERR_DEVICE: return "no usable current HIP device";
         case GEMM_F32_ERR_INVALID_OP: return "invalid op: op_a and op_b must be GEMM_F32_OP_N or GEMM_F32_OP_T";
-        case GEMM_F32_ERR_WORKSPACE: return "workspace smaller than reduce_sum_f32_workspace_size()";
+        case GEMM_F32_ERR_WORKSPACE: return "workspace smaller than the entry point's workspace_size()";
         case GEMM_F32_ERR_INVALID_FORMAT: return "unknown 16-bit format: use GEMM_MIXED_BF16 or GEMM_MIXED_F16";
         case GEMM_F32_ERR_SCRATCH:
             return "partials exceed the library's fixed 1 MiB scratch: use reduce_sum_f32_variant with a workspace";
+        case GEMM_F32_ERR_INVALID_TYPE: return "stored type not taken: the factors' format or GEMM_MIXED_F32 (a 16-bit format or GEMM_MIXED_F32 for the others)";
+        case GEMM_F32_ERR_INVALID_ACTIVATION: return "unknown activation: use GEMM_ACT_*";
+        case GEMM_F32_ERR_INVALID_EPILOGUE:
+            return "epilogue field not taken in this mode: bias goes with gradient 0, bias_grad with gradient 1";
+        case GEMM_F32_ERR_INVALID_SCALAR: return "eps, a coefficient or a step count out of range";
         default: return "unknown status";
     }
 }

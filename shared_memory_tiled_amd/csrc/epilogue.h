@@ -1,0 +1,195 @@
+// epilogue.h -- what happens to an entry of a product before it is stored:
+// bias, activation and residual of a fully connected layer, or the
+// activation's derivative of its backward pass (device code shared by the
+// kernels that end in it; not part of the public interface).
+//
+//   forward    z = v + bias[col];      C = act(z) + residual;  z kept if asked
+//   gradient   d = (v + residual) act'(z);  C = d;  column sums of d if asked
+//
+// v, z, d and the column sums are binary32; C, residual, bias and the kept z
+// are 16-bit or binary32 values, each rounded once, when it is stored (the
+// column sums add d before its rounding).
+#pragma once
+
+#include "launch.h"
+
+namespace gemmf32 {
+
+namespace {
+
+// Types of stored values: 0 bfloat16, 1 binary16, 2 binary32.
+template <int TYPE>
+struct Stored;
+template <>
+struct Stored<0> {
+    using T = __bf16;
+};
+template <>
+struct Stored<1> {
+    using T = _Float16;
+};
+template <>
+struct Stored<2> {
+    using T = float;
+};
+
+// W consecutive stored values as binary32, and back (nearest-even), the first
+// `valid` of them (the rest read as 0 and are not written).  The values need
+// their own alignment only; gfx9 runs global memory in unaligned mode, so the
+// compiler may use one wide access.
+template <int TYPE, int W>
+__device__ __forceinline__ void load_values(const void* base, int64_t index, int valid, float (&v)[W]) {
+    using T = typename Stored<TYPE>::T;
+    const T* p = static_cast<const T*>(base) + index;
+    if (valid >= W) {
+        T raw[W];
+        __builtin_memcpy(raw, p, sizeof(raw));
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = (float)raw[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = e < valid ? (float)p[e] : 0.0f;
+    }
+}
+template <int TYPE, int W>
+__device__ __forceinline__ void store_values(void* base, int64_t index, int valid, const float (&v)[W]) {
+    using T = typename Stored<TYPE>::T;
+    T* p = static_cast<T*>(base) + index;
+    if (valid >= W) {
+        T raw[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) raw[e] = (T)v[e];
+        __builtin_memcpy(p, raw, sizeof(raw));
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e < valid) p[e] = (T)v[e];
+    }
+}
+template <int W>
+__device__ __forceinline__ void load_values(int type, const void* base, int64_t index, int valid, float (&v)[W]) {
+    if (type == 0) load_values<0>(base, index, valid, v);
+    else if (type == 1) load_values<1>(base, index, valid, v);
+    else load_values<2>(base, index, valid, v);
+}
+template <int W>
+__device__ __forceinline__ void store_values(int type, void* base, int64_t index, int valid, const float (&v)[W]) {
+    if (type == 0) store_values<0>(base, index, valid, v);
+    else if (type == 1) store_values<1>(base, index, valid, v);
+    else store_values<2>(base, index, valid, v);
+}
+
+// e^x and 1 / x on the hardware's 1-ulp units: with the argument's scaling
+// by log2 e, e^x is within (2 + |x|) 2^-24 of its value.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// The normal distribution function Phi(z) and its density's exponential
+// e^(-z^2 / 2).  With t = 1 / (1 + 0.28 |z|), e^(z^2 / 2) Phi(-|z|) is t
+// times a polynomial in t: eighth degree, fitted to half the scaled
+// complementary error function in binary64 for the smallest largest relative
+// error, 3.5e-7 evaluated in binary32.  Phi(z) = 1 - Phi(-z) for z > 0, so
+// small tails keep their relative accuracy.
+__device__ __forceinline__ float normal_cdf(float z, float* density) {
+    const float a = __builtin_fabsf(z);
+    const float t = fast_rcp(1.0f + 0.28f * a);
+    float q = 0.02475812f;
+    q = __builtin_fmaf(q, t, -0.09374318f);
+    q = __builtin_fmaf(q, t, 0.09266892f);
+    q = __builtin_fmaf(q, t, -0.00665205f);
+    q = __builtin_fmaf(q, t, 0.07287117f);
+    q = __builtin_fmaf(q, t, 0.0836053f);
+    q = __builtin_fmaf(q, t, 0.10308819f);
+    q = __builtin_fmaf(q, t, 0.11169959f);
+    q = __builtin_fmaf(q, t, 0.11170386f);
+    const float g = fast_exp(-0.5f * z * z);
+    const float tail = g * (t * q);
+    *density = g;
+    return z > 0.0f ? 1.0f - tail : tail;
+}
+
+// Activations (GEMM_ACT_*) and their derivatives.  NaN stays NaN.
+//   gelu_tanh: (1 + tanh u) / 2 = 1 / (1 + e^(-2 u)), u = c (z + 0.044715 z^3),
+//   c = sqrt(2 / pi).
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+constexpr float kTanhC = 0.79788456080286536f, kTanhCubic = 0.044715f;
+
+__device__ __forceinline__ float activate(int act, float z) {
+    if (act == kActRelu) return z <= 0.0f ? 0.0f : z;
+    if (act == kActGelu) {
+        float g;
+        return z * normal_cdf(z, &g);
+    }
+    if (act == kActGeluTanh) {
+        const float u2 = -2.0f * kTanhC * z * __builtin_fmaf(kTanhCubic * z, z, 1.0f);
+        return z * fast_rcp(1.0f + fast_exp(u2));
+    }
+    if (act == kActSilu) return z * fast_rcp(1.0f + fast_exp(-z));
+    return z;
+}
+
+__device__ __forceinline__ float activate_derivative(int act, float z) {
+    if (act == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    if (act == kActGelu) {
+        float g;
+        const float cdf = normal_cdf(z, &g);
+        return __builtin_fmaf(z * 0.39894228040143268f, g, cdf);
+    }
+    if (act == kActGeluTanh) {
+        const float u2 = -2.0f * kTanhC * z * __builtin_fmaf(kTanhCubic * z, z, 1.0f);
+        const float s = fast_rcp(1.0f + fast_exp(u2));
+        // d u2 / dz = -2 c (1 + 3 0.044715 z^2); s' = -s (1 - s) du2
+        const float du = 2.0f * kTanhC * __builtin_fmaf(3.0f * kTanhCubic * z, z, 1.0f);
+        return __builtin_fmaf(z * du, s * (1.0f - s), s);
+    }
+    if (act == kActSilu) {
+        const float s = fast_rcp(1.0f + fast_exp(-z));
+        return __builtin_fmaf(z, s * (1.0f - s), s);
+    }
+    return 1.0f;
+}
+
+// W consecutive columns from `col` of row `row` (inside C; columns past N are
+// skipped): v holds the product's entries on entry and, in gradient mode, d
+// on return (0 past N).
+template <int W>
+__device__ __forceinline__ void finish_entries(const EpilogueArgs& e, int row, int col, float (&v)[W]) {
+    const int valid = e.N - col;
+    const int64_t ci = (int64_t)row * e.ldc + col, zi = (int64_t)row * e.ldz + col;
+    float r[W];
+    if (e.residual != nullptr) load_values(e.c_type, e.residual, (int64_t)row * e.ldr + col, valid, r);
+    if (e.gradient) {
+        if (e.residual != nullptr) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] += r[i];
+        }
+        if (e.act != kActNone) {
+            float z[W];
+            load_values(e.z_type, e.preact, zi, valid, z);
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] *= activate_derivative(e.act, z[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = i < valid ? v[i] : 0.0f;
+        if (e.C != nullptr) store_values(e.c_type, e.C, ci, valid, v);
+        return;
+    }
+    if (e.bias != nullptr) {
+        float b[W];
+        load_values(e.bias_type, e.bias, col, valid, b);
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] += b[i];
+    }
+    if (e.preact != nullptr) store_values(e.z_type, e.preact, zi, valid, v);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = activate(e.act, v[i]);
+    if (e.residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] += r[i];
+    }
+    store_values(e.c_type, e.C, ci, valid, v);
+}
+
+}  // namespace
+
+}  // namespace gemmf32

@@ -64,6 +64,66 @@ hipError_t launch_wide16_160(const Gemm16Args& p, hipStream_t s, int format, int
 // stored (A k-contiguous, B mn-contiguous) only.
 hipError_t launch_wide16_4stage(const Gemm16Args& p, hipStream_t s, int format, int group_m);
 
+// What follows a 16-bit product before its entries are stored (epilogue.h):
+// pointers and types validated by the entry point.  Types: 0 bfloat16, 1
+// binary16, 2 binary32.
+struct EpilogueArgs {
+    int M, N;
+    int gradient;                  // 0 forward, 1 the backward pass's form
+    int act;                       // GEMM_ACT_*
+    int c_type; void* C; int64_t ldc;                 // C may be null in gradient mode (column sums only)
+    int bias_type; const void* bias;                   // N values or null
+    const void* residual; int64_t ldr;                 // of C's type, or null; may be C
+    int z_type; void* preact; int64_t ldz;             // forward: written if not null; gradient: read
+    float* bias_grad;                                  // gradient: N column sums, or null
+};
+// The product with its epilogue (linear.hip; p.C is not used) and the bytes
+// of workspace the launch needs.
+int64_t linear_workspace(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b);
+hipError_t launch_linear(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_a, int op_b,
+                         void* workspace);
+// The pass over finished sums (in_type 2: `planes` binary32 planes added in
+// order) or over 16-bit gradients (in_type 0, 1); `partials` holds
+// epilogue_pass_workspace(M, N) bytes when bias_grad is set.
+int64_t epilogue_pass_workspace(int M, int N);
+hipError_t launch_epilogue_pass(const EpilogueArgs& e, int in_type, const void* in, int64_t ld, int planes,
+                                int64_t plane_stride, float* partials, hipStream_t s);
+// out[c] = sum over i < count of partials[i n + c], in a fixed order.
+hipError_t launch_column_sums(int count, int n, const float* partials, float* out, hipStream_t s);
+
+// Layer norm (layer_norm.hip), forward and backward.  type: of x, y, dy, dx
+// and the residual's gradient; param_type: of gamma and beta (0, 1, 2).
+struct LayerNormArgs {
+    int64_t rows; int cols;
+    int type, param_type;
+    const void* x; int64_t ldx;
+    const void* gamma; const void* beta;                // cols values or null
+    float eps;
+    void* y; int64_t ldy;                               // forward
+    float* mean; float* rstd;                           // forward: written (or null); backward: read
+    const void* dy; int64_t lddy;                       // backward
+    const void* residual_grad; int64_t ldr;
+    void* dx; int64_t lddx;
+    float* dgamma; float* dbeta;                        // cols sums or null
+};
+hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s);
+int64_t layer_norm_backward_workspace(int type, int64_t rows, int cols);
+hipError_t launch_layer_norm_backward(const LayerNormArgs& a, void* workspace, hipStream_t s);
+
+// Newton-Schulz orthogonalisation (newton_schulz.hip) of `batch` matrices.
+struct NewtonSchulzArgs {
+    int64_t batch; int rows, cols; int type;
+    const void* G; int64_t ldg, stride_g;
+    void* out; int64_t ldo, stride_o;
+    int steps; float a, b, c, eps;
+    const double* bounds;          // steps + 1 bounds on X's singular values (below)
+};
+// bounds[k]: an upper bound on the singular values of X after k steps, from
+// at most 1; false if one passes 2^40.
+bool newton_schulz_bounds(int steps, double a, double b, double c, double* bounds);
+int64_t newton_schulz_workspace(const NewtonSchulzArgs& a);     // -1: too large
+hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, void* workspace, hipStream_t s);
+
 // Sum reduction (reduce.hip): *out = sum of x[0 .. n-1].
 hipError_t launch_reduce(int variant, int64_t n, const float* x, float* out, float* ws, hipStream_t s);
 int64_t reduce_workspace_floats(int variant, int64_t n);

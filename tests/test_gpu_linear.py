@@ -1,0 +1,311 @@
+"""The product with its epilogue and its backward pass against binary64."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import layer_refs as R
+from gpu_support import say
+from shared_memory_tiled_amd import binding
+
+pytestmark = pytest.mark.gpu
+
+
+def normal(seed, *shape, dtype=torch.bfloat16, scale=1.0):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(dtype)
+
+
+def check_forward(M, N, K, dtype, kind, op_b="N", bias=True, residual=True, out_dtype=None, preact=True, seed=0,
+                  op_a="N", strides=False, bias_dtype=None):
+    say(f"linear M={M} N={N} K={K} {dtype} {kind} {op_a}{op_b} bias={bias} res={residual} out={out_dtype} "
+        f"strides={strides}")
+    X, W = normal(seed, M, K, dtype=dtype), normal(seed + 1, K, N, dtype=dtype, scale=max(K, 1) ** -0.5)
+    b = normal(seed + 2, N, dtype=bias_dtype or dtype) if bias else None
+    ot = out_dtype or dtype
+    r = normal(seed + 3, M, N, dtype=ot) if residual else None
+    Y, Z, S = R.linear_ref(X, W, b, kind, r)
+    Xs = X.t().contiguous() if op_a == "T" else X
+    Ws = W.t().contiguous() if op_b == "T" else W
+    out, buf = None, None
+    if strides:
+        Xs, _ = R.padded(Xs, Xs.shape[1] + 3, 1)
+        Ws, _ = R.padded(Ws, Ws.shape[1] + 5, 3)
+        if r is not None:
+            r, _ = R.padded(r, N + 7, 1)
+        out, buf = R.padded(torch.zeros(M, N, dtype=ot, device="cuda"), N + 1, 5, fill=7.0)
+    got = binding.linear(Xs, Ws, bias=b, activation=kind, residual=r, out=out, out_dtype=out_dtype,
+                         return_preact=preact, op_a=op_a, op_b=op_b)
+    y, z = got if preact else (got, None)
+    torch.cuda.synchronize()
+    R.within(y, Y, R.linear_tol(Y, Z, S, K, kind, None if r is None else r, ot), "out")
+    if preact:
+        R.within(z, Z, R.HALF[dtype] * Z.abs() + R.TINY[dtype] + (K + 2) * R.U * S, "preact")
+    if buf is not None:
+        R.untouched(buf, M, N, N + 1, 5)
+
+
+@pytest.mark.parametrize("kind", R.ACTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("op_b", ["N", "T"])
+def test_activations(kind, dtype, op_b):
+    check_forward(70, 200, 136, R.DTYPES[dtype], kind, op_b)
+    check_forward(5, 200, 136, R.DTYPES[dtype], kind, op_b)
+
+
+# one token, decoding batches around the tile heights, odd sizes, sizes below
+# every tile, one-value factors
+SIZES = [(1, 64, 64), (1, 1, 1), (1, 1000, 4096), (2, 129, 8), (3, 7, 5), (8, 256, 8192), (15, 130, 96), (16, 128, 32),
+         (17, 1000, 264), (31, 33, 4096), (32, 512, 1000), (33, 66, 40), (48, 4096, 136), (63, 65, 257), (64, 640, 1024),
+         (65, 320, 1024), (100, 100, 100), (127, 129, 131), (200, 1, 64), (257, 255, 1), (1000, 500, 24),
+         (1000, 1002, 998), (999, 1001, 999), (2048, 200, 4096)]
+
+
+@pytest.mark.parametrize("size", SIZES, ids=str)
+@pytest.mark.parametrize("op_b", ["N", "T"])
+def test_sizes(size, op_b):
+    check_forward(*size, torch.bfloat16, "silu", op_b, seed=11)
+    check_forward(*size, torch.float16, "none", op_b, residual=False, preact=False, out_dtype=torch.float32, seed=12)
+
+
+@pytest.mark.parametrize("size", [(4, 130, 70), (30, 129, 257), (130, 258, 190), (700, 900, 72), (1100, 1300, 264)],
+                         ids=str)
+@pytest.mark.parametrize("op_a,op_b", [("N", "N"), ("N", "T"), ("T", "N"), ("T", "T")])
+def test_strides_and_ops(size, op_a, op_b):
+    check_forward(*size, torch.bfloat16, "gelu", op_b, op_a=op_a, strides=True, seed=21)
+    check_forward(*size, torch.float16, "relu", op_b, op_a=op_a, seed=22, bias_dtype=torch.float32)
+
+
+# every tile family once its count of tiles fits: 256, 192 and 160 tiles, the
+# rows split between 256 and smaller ones, 128 and 64 tiles with K split
+@pytest.mark.parametrize("size", [(2900, 2950, 130), (2300, 2310, 328), (4352, 4352, 64), (2048, 2040, 1032),
+                                  (3000, 3300, 514), (1000, 1100, 2056), (4100, 4090, 70)], ids=str)
+@pytest.mark.parametrize("op_b", ["N", "T"])
+def test_large_tiles(size, op_b):
+    check_forward(*size, torch.bfloat16, "gelu_tanh", op_b, seed=31)
+    check_forward(*size, torch.float16, "silu", op_b, out_dtype=torch.float32, preact=False, seed=32)
+
+
+def test_in_place_residual():
+    for M, N, K in [(3, 200, 64), (50, 1000, 520), (300, 500, 264), (3000, 2900, 72), (33, 35, 37)]:
+        X, W = normal(1, M, K), normal(2, K, N, scale=K ** -0.5)
+        r = normal(3, M, N)
+        Y, Z, S = R.linear_ref(X, W, None, "relu", r)
+        out = r.clone()
+        assert binding.linear(X, W, activation="relu", residual=out, out=out) is out
+        R.within(out, Y, R.linear_tol(Y, Z, S, K, "relu", r, out.dtype), f"in place {M}x{N}x{K}")
+
+
+def test_empty_and_no_inner():
+    b = normal(5, 40)
+    r = normal(6, 30, 40)
+    X, W = torch.empty(30, 0, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 40, dtype=torch.bfloat16, device="cuda")
+    y, z = binding.linear(X, W, bias=b, activation="silu", residual=r, return_preact=True)
+    ref = R.act(b.double(), "silu") + r.double()
+    R.within(y, ref, R.HALF[torch.bfloat16] * ref.abs() + 1e-6, "K = 0")
+    assert torch.equal(z, b.expand(30, 40))
+    assert binding.linear(normal(1, 0, 8), normal(2, 8, 4)).shape == (0, 4)
+    assert binding.linear(normal(1, 4, 8), normal(2, 8, 0)).shape == (4, 0)
+    d, db = binding.linear_grad(normal(1, 0, 8), normal(2, 16, 8), return_bias_grad=True)
+    assert d.shape == (0, 16) and bool((db == 0).all())
+    _, db = binding.activation_backward(normal(1, 0, 8))
+    assert bool((db == 0).all())
+
+
+def test_special_values():
+    """Infinities and NaN stay in their rows and columns; NaN passes every
+    activation; padding full of NaN reaches nothing."""
+    for M, N, K in [(4, 64, 64), (40, 96, 64), (130, 130, 136), (700, 800, 72)]:
+        for kind in R.ACTS:
+            X, W = normal(1, M, K), normal(2, K, N, scale=K ** -0.5)
+            X[1, 3] = float("nan")
+            X[2, 5] = float("inf")
+            y = binding.linear(X, W, activation=kind)
+            assert bool(y[1].isnan().all()), (M, kind)
+            rest = torch.cat([y[:1], y[3:]])
+            assert bool(rest.isfinite().all()), (M, kind)
+            pos = W[5] > 0
+            assert bool((y[2][pos] == float("inf")).all())
+
+
+def test_long_activation_range():
+    """Preactivations from -60 to 60 and the types' extremes."""
+    z = torch.cat([torch.linspace(-60, 60, 4001), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e30, -1e30, 3e38, -3e38])])
+    z = z.to(torch.float32).cuda()
+    X = torch.zeros(z.numel(), 8, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(8, 4, dtype=torch.bfloat16, device="cuda")
+    for kind in R.ACTS:
+        res = None
+        # the bias is the only term: one row of biases per call of 4009 columns
+        y = binding.linear(X[:3], W[:, :1].expand(8, z.numel()).contiguous(), bias=z, activation=kind, residual=res,
+                           out_dtype=torch.float32)
+        ref = R.act(z.double(), kind).float().double()
+        tol = 16 * R.U * ref.abs() + 16 * R.U * torch.exp(-z.double().abs() / 4) + 2.0 ** -126
+        if kind in ("gelu_tanh", "silu"):      # the exponential's argument |x| costs |x| 2^-24 of a small tail
+            x = z.double().abs() if kind == "silu" else 1.6 * (z.double().abs() + 0.044715 * z.double().abs() ** 3)
+            tol = tol + ref.abs() * (x.clamp(max=200) + 4) * 2 * R.U
+        if kind == "gelu":
+            tol = tol + ref.abs() * ((z.double() ** 2).clamp(max=200) + 8) * 2 * R.U
+        R.within(y[0], ref, tol, kind)
+
+
+# ------------------------------------------------------------ backward pass
+
+def grad_tol(D, V, Sv, K, Zd, kind, dtype):
+    """Half a step of D; the binary32 sum's error times |act'| <= 1.13; the
+    derivative's evaluation, within 32 units, times the sum."""
+    return R.HALF[dtype] * D.abs() + R.TINY[dtype] + R.LIPSCHITZ * (K + 2) * R.U * Sv + \
+        (32 * R.U * V.abs() if kind != "none" else 0.0)
+
+
+@pytest.mark.parametrize("kind", R.ACTS)
+@pytest.mark.parametrize("size", [(1, 40, 64), (20, 200, 136), (70, 200, 136), (333, 1000, 72), (999, 1001, 77),
+                                  (2300, 2310, 264), (4100, 4090, 72)], ids=str)
+def test_linear_grad(size, kind):
+    M, N, K = size
+    for dtype, out_dtype, residual in [(torch.bfloat16, None, False), (torch.float16, torch.float32, True)]:
+        say(f"linear_grad {size} {kind} {dtype} residual={residual}")
+        dZ, W, z = normal(1, M, K, dtype=dtype), normal(2, N, K, dtype=dtype, scale=K ** -0.5), normal(3, M, N, dtype=dtype)
+        ot = out_dtype or dtype
+        r = normal(4, M, N, dtype=ot) if residual else None
+        V = dZ.double() @ W.double().t()
+        Sv = dZ.double().abs() @ W.double().abs().t()
+        if residual:
+            V, Sv = V + r.double(), Sv + r.double().abs()
+        D = V * R.act_derivative(z.double(), kind)
+        tol = grad_tol(D, V, Sv, K, z, kind, ot)
+        for op_b in ("T", "N"):
+            Ws = W if op_b == "T" else W.t().contiguous()
+            got, sums = binding.linear_grad(dZ, Ws, preact=z if kind != "none" else None, activation=kind, residual=r,
+                                            out_dtype=out_dtype, return_bias_grad=True, op_b=op_b)
+            R.within(got, D, tol, f"D {op_b}")
+            # the sums add unrounded entries: their errors without the last rounding, and the sum's
+            unrounded = tol - R.HALF[ot] * D.abs()
+            R.within(sums, D.sum(0), unrounded.sum(0) + (M + 8) * R.U * D.abs().sum(0), f"sums {op_b}")
+
+
+@pytest.mark.parametrize("kind", R.ACTS)
+@pytest.mark.parametrize("size", [(1, 1), (1, 1000), (7, 33), (64, 129), (1000, 1001), (5000, 260), (16, 5000)], ids=str)
+def test_activation_backward(size, kind):
+    M, N = size
+    for dtype in (torch.bfloat16, torch.float16):
+        dY, z = normal(1, M, N, dtype=dtype), normal(2, M, N, dtype=dtype)
+        dYp, _ = R.padded(dY, N + 3, 1)
+        zp, _ = R.padded(z, N + 1, 3)
+        D = dY.double() * R.act_derivative(z.double(), kind)
+        dz, db = binding.activation_backward(dYp, zp if kind != "none" else None, kind)
+        R.within(dz, D, R.HALF[dtype] * D.abs() + R.TINY[dtype] + 32 * R.U * dY.double().abs(), "dZ")
+        tol = 32 * R.U * dY.double().abs().sum(0) + (M + 8) * R.U * D.abs().sum(0)
+        R.within(db, D.sum(0), tol, "db")
+        none, db2 = binding.activation_backward(dY, z if kind != "none" else None, kind, return_dz=False)
+        assert none is None and torch.equal(db, db2)
+        inplace = dY.clone()
+        dz2, _ = binding.activation_backward(inplace, z if kind != "none" else None, kind, out=inplace,
+                                             return_bias_grad=False)
+        assert dz2 is inplace and torch.equal(dz2, dz)
+
+
+@pytest.mark.parametrize("size", [(1, 64, 64), (64, 64, 64), (100, 72, 40), (999, 300, 130), (1001, 77, 501),
+                                  (3001, 1000, 520), (2050, 2100, 2200)], ids=str)
+@pytest.mark.parametrize("op_b", ["N", "T"])
+def test_linear_backward(size, op_b):
+    M, N, K = size
+    for dtype, kind in ((torch.bfloat16, "gelu_tanh"), (torch.float16, "silu"), (torch.bfloat16, "none")):
+        for wdt in (None, torch.float32):
+            say(f"linear_backward {size} {op_b} {dtype} {kind} dW {wdt}")
+            X, W = normal(1, M, K, dtype=dtype), normal(2, K, N, dtype=dtype, scale=K ** -0.5)
+            dY, z = normal(3, M, N, dtype=dtype), normal(4, M, N, dtype=dtype)
+            Ws = W.t().contiguous() if op_b == "T" else W
+            dX, dW, db = binding.linear_backward(dY, X, Ws, preact=z if kind != "none" else None, activation=kind,
+                                                 weight_grad_dtype=wdt, op_b=op_b)
+            D = dY.double() * R.act_derivative(z.double(), kind)
+            # dZ's own error: its rounding to dtype (none without an activation) and its evaluation
+            ed = (R.HALF[dtype] * D.abs() + R.TINY[dtype] + 32 * R.U * dY.double().abs()) if kind != "none" else \
+                torch.zeros_like(D)
+            ref = D @ W.double().t()
+            tol = R.HALF[dtype] * ref.abs() + R.TINY[dtype] + (ed + (N + 2) * R.U * D.abs()) @ W.double().abs().t() * 1.01
+            R.within(dX, ref, tol, "dX")
+            refw = X.double().t() @ D
+            ot = wdt or dtype
+            tolw = R.HALF[ot] * refw.abs() + R.TINY[ot] + X.double().abs().t() @ (ed + (M + 2) * R.U * D.abs()) * 1.01
+            if op_b == "T":
+                refw, tolw = refw.t(), tolw.t()
+            R.within(dW, refw, tolw, "dW")
+            tolb = 32 * R.U * dY.double().abs().sum(0) + (M + 8) * R.U * D.abs().sum(0)
+            R.within(db, D.sum(0), tolb, "db")
+
+
+def test_gradient_against_differences():
+    """linear_backward against central differences of a binary64 loss."""
+    M, N, K = 12, 20, 16
+    X, W, dY = normal(1, M, K), normal(2, K, N, scale=0.3), normal(3, M, N)
+    for kind in ("gelu", "gelu_tanh", "silu"):
+        _, z = binding.linear(X, W, activation=kind, return_preact=True)
+        dX, dW, db = binding.linear_backward(dY, X, W, preact=z, activation=kind)
+
+        def loss(x, w, b):
+            return (R.act(x @ w + b, kind) * dY.double()).sum()
+
+        x, w, b = X.double(), W.double(), torch.zeros(N, dtype=torch.float64, device="cuda")
+        h = 1e-5
+        # the gradient is taken at Z rounded to bfloat16: |Z| 2^-8 |act''| of dY, and dZ's and the results' rounding
+        slack = 3 * 2.0 ** -8
+        for t, g, args in ((x, dX, 0), (w, dW, 1), (b, db, 2)):
+            for idx in ([(0, 0), (3, 7), (11, 15)] if t.dim() == 2 and args == 0 else
+                        [(0, 0), (5, 9), (15, 19)] if args == 1 else [(0,), (13,)]):
+                p, m = t.clone(), t.clone()
+                p[idx] += h
+                m[idx] -= h
+                a = [x, w, b]
+                a[args] = p
+                up = loss(*a)
+                a[args] = m
+                num = ((up - loss(*a)) / (2 * h)).item()
+                zabs = (z.double().abs() * R.CURVATURE + R.LIPSCHITZ) * dY.double().abs()
+                scale = (zabs @ w.abs().t())[idx] if args == 0 else (x.abs().t() @ zabs)[idx] if args == 1 else \
+                    zabs.sum(0)[idx]
+                assert abs(g[idx].item() - num) <= slack * scale.item() + 1e-6, (kind, args, idx, g[idx].item(), num)
+
+
+def test_streams_and_graph_replay():
+    """A captured layer, forward and backward, replayed between eager calls on
+    other data gives the eager bits each time; two streams at once do not
+    disturb each other."""
+    for M, N, K in [(3, 512, 1024), (40, 640, 512), (200, 320, 264), (999, 333, 130)]:
+        say(f"graph {M} {N} {K}")
+        X, W, b = normal(1, M, K), normal(2, K, N, scale=K ** -0.5), normal(3, N)
+        dY = normal(4, M, N)
+
+        def layer():
+            y, z = binding.linear(X, W, bias=b, activation="gelu", return_preact=True)
+            return (y, z) + tuple(binding.linear_backward(dY, X, W, preact=z, activation="gelu"))
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            layer()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            captured = layer()
+        for seed in range(3):
+            X.copy_(normal(10 + seed, M, K))
+            dY.copy_(normal(20 + seed, M, N))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            kept = [t.clone() for t in captured]
+            eager = layer()
+            torch.cuda.synchronize()
+            for a, e in zip(kept, eager):
+                assert torch.equal(a, e)
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        outs = []
+        for _ in range(4):
+            outs.append(binding.linear(X, W, bias=b, activation="gelu", stream=s1))
+            outs.append(binding.linear(X, W, bias=b, activation="gelu", stream=s2.cuda_stream))
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o, eager[0])

@@ -1,0 +1,158 @@
+"""Newton-Schulz orthogonalisation against binary64.
+
+The map is not contracting in every direction, so errors are bounded for
+matrices whose small singular values are known: half a step of the entry plus
+the errors of the products, relative to the result's root mean square.
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import layer_refs as R
+from gpu_support import say
+from shared_memory_tiled_amd import binding
+
+pytestmark = pytest.mark.gpu
+
+
+def momentum(seed, *shape, dtype=torch.float32, rank=8):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    strong = torch.randn(*shape[:-1], rank, generator=gen, device="cuda") @ \
+        torch.randn(*shape[:-2], rank, shape[-1], generator=gen, device="cuda")
+    return (1e-3 * (0.1 * strong + torch.randn(*shape, generator=gen, device="cuda"))).to(dtype)
+
+
+def check(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None):
+    """Tolerance, relative to the largest singular value bound 1.3 spread over
+    an entry (the result's root mean square r): a step multiplies a relative
+    error of the factors by at most |a| + 2 |b| + 4 |c| = 21.1 in the worst
+    alignment, but the errors of a product's factors are independent from
+    entry to entry, so they enter as about their root mean square: per step
+    |a| + |b| + |c| = 10.3 of it, five steps' errors meeting at once, and a
+    maximum over 10^7 entries of six of them: 10.3 * sqrt(5) * 6 = 138
+    root-mean-square roundings.  Factors kept to 2^-22 or better (binary32,
+    binary16 results) have a root mean square rounding of 2^-23.8.  A
+    product's binary32 sum of n terms adds its own: each addition rounds the
+    partial sum by at most half a unit in the last place, 2^-23.5 / sqrt(12) =
+    2^-25.3 of it in the root mean square, partial sum i of n terms of random
+    sign has sqrt(i / n) of the final one's size, and the squares add up to
+    n / 2: sqrt(n / 2) 2^-25.3 of the sum, n the longer side.  Factors
+    rounded to 11 bits (bfloat16 results; 2^-12.8 with the diagonals kept
+    apart in binary32) give 138 * 2^-12.8 < 2^-5.6."""
+    step = 2.0 ** -23.8 + math.sqrt(max(G.shape[-2:]) / 2) * 2.0 ** -25.3
+    got = binding.newton_schulz(G, steps=steps, coefficients=coefficients, eps=eps, out=out)
+    torch.cuda.synchronize()
+    ref = R.newton_schulz_ref(G, steps, coefficients, eps)
+    assert bool(ref.isfinite().all())
+    r = ref.square().mean((-1, -2), keepdim=True).sqrt()
+    tol = R.HALF[G.dtype] * ref.abs() + R.TINY[G.dtype] + r * (2.0 ** -5.6 if G.dtype == torch.bfloat16 else 138 * step)
+    R.within(got, ref, tol, f"{tuple(G.shape)} {G.dtype}")
+    rms = ((got.double() - ref).square().mean((-1, -2)).sqrt() / r[..., 0, 0].clamp(min=1e-300)).max().item()
+    say(f"newton_schulz {tuple(G.shape)} {G.dtype} steps={steps}: relative rms error {rms:.2e}")
+    # and in the root mean square: the result's rounding and 10.3 sqrt(5) = 23 roundings of the factors
+    bound = R.HALF[G.dtype] + 23 * (2.0 ** -12.8 if G.dtype == torch.bfloat16 else step)
+    assert rms <= bound, (rms, bound)
+    return got
+
+
+SHAPES = [(1, 1), (1, 7), (9, 1), (2, 2), (16, 16), (17, 33), (63, 64), (64, 65), (100, 30), (31, 200), (128, 128),
+          (130, 257), (300, 129), (500, 500), (257, 1000), (1000, 260), (640, 1300), (1030, 1025)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_shapes(shape, dtype):
+    # binary16 holds 1e-3 values coarsely but exactly; the reference sees the same ones
+    check(momentum(sum(shape), *shape, dtype=R.DTYPES[dtype]))
+
+
+@pytest.mark.parametrize("shape", [(3, 40, 72), (2, 300, 200), (8, 128, 128), (5, 257, 513), (2, 1100, 700), (16, 65, 31),
+                                   (3, 2000, 1000)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_batches(shape, dtype):
+    G = momentum(1, *shape, dtype=R.DTYPES[dtype])
+    got = check(G)
+    one = binding.newton_schulz(G[1].contiguous())
+    r = one.double().square().mean().sqrt()
+    assert (one.double() - got[1].double()).abs().max() <= (2.0 ** -5 if dtype == "bf16" else 2.0 ** -14) * r
+
+
+@pytest.mark.parametrize("shape", [(1800, 2000), (2304, 2304), (4096, 1100), (2700, 2800)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large(shape, dtype):
+    check(momentum(3, *shape, dtype=R.DTYPES[dtype]))
+
+
+def test_strides_and_in_place():
+    for dt in (torch.bfloat16, torch.float32):
+        G = momentum(5, 3, 150, 90, dtype=dt)
+        want = binding.newton_schulz(G)
+        buf = torch.full((3 * 160 * 101 + 64,), 7.0, dtype=dt, device="cuda")
+        view = buf[3:3 + 3 * 160 * 101].view(3, 160, 101)[:, :150, :90]
+        view.copy_(G)
+        src = buf.clone()[3:3 + 3 * 160 * 101].view(3, 160, 101)[:, :150, :90]
+        assert torch.equal(binding.newton_schulz(src), want)
+        got = binding.newton_schulz(view, out=view)
+        assert got is view and torch.equal(view, want)
+        mask = torch.ones_like(buf, dtype=torch.bool)
+        mask[3:3 + 3 * 160 * 101].view(3, 160, 101)[:, :150, :90] = False
+        assert bool((buf[mask] == 7.0).all())
+
+
+def test_steps_and_coefficients():
+    G = momentum(7, 96, 160)
+    for steps in (0, 1, 2, 8):
+        check(G, steps=steps)
+    check(G, steps=12, coefficients=(1.5, -0.5, 0.0))
+    check(G, steps=6, coefficients=(1.875, -1.25, 0.375))
+    check(G * 0, steps=5)
+    check(G * 1e30, steps=5)
+    check(G.float() * 1e-30, steps=5, eps=0.0)
+
+
+def test_orthogonal_result():
+    """After enough steps of a polynomial with a fixed point at 1, the rows
+    are orthonormal to the precision of the factors."""
+    for shape in ((96, 400), (400, 96)):
+        X = binding.newton_schulz(momentum(9, *shape), steps=30, coefficients=(1.875, -1.25, 0.375)).double()
+        S = X @ X.t() if shape[0] < shape[1] else X.t() @ X
+        assert (S - torch.eye(96, dtype=torch.float64, device="cuda")).abs().max() <= 2.0 ** -18
+
+
+def test_nan_stays_in_its_matrix():
+    for dt in (torch.bfloat16, torch.float32):
+        G = momentum(3, 4, 70, 130, dtype=dt)
+        want = binding.newton_schulz(G)
+        G[2, 3, 4] = float("nan")
+        G[1, 69, 129] = float("inf")
+        got = binding.newton_schulz(G)
+        assert bool(got[2].isnan().all()) and bool(got[1].isnan().all())
+        assert torch.equal(got[[0, 3]], want[[0, 3]])
+
+
+def test_streams_and_graph_replay():
+    for shape, dt in (((200, 300), torch.bfloat16), ((2, 520, 260), torch.float32), ((1024, 1024), torch.bfloat16)):
+        G = momentum(1, *shape, dtype=dt)
+        binding.newton_schulz(G)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            captured = binding.newton_schulz(G)
+        for seed in range(3):
+            G.copy_(momentum(10 + seed, *shape, dtype=dt))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            kept = captured.clone()
+            eager = binding.newton_schulz(G)
+            torch.cuda.synchronize()
+            assert torch.equal(kept, eager)
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        a = [binding.newton_schulz(G, stream=s) for s in (s1, s2, s1, s2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, eager) for t in a)
+        assert math.isfinite(eager.float().sum().item())
