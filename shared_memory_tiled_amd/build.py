@@ -28,11 +28,12 @@ FLAGS = ["-O3", f"--offload-arch={ARCH}", "-std=c++17", "-fPIC", "-Wall",
          "-I", INCLUDE, "-I", CSRC]
 
 
-# Per-source extra flags.  mfma16_ksplit.hip: matrix instructions in their
+# Per-source extra flags.  The k-split sources: matrix instructions in their
 # vector-register form -- with the accumulators in AGPRs the register
 # allocator copied every accumulator before each matrix instruction of that
 # kernel.
-EXTRA_FLAGS = {"mfma16_ksplit.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
+EXTRA_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]
+               for src in ("mfma16_ksplit.hip", "newton_schulz_ksplit.hip")}
 
 
 def _compile(src: str, resource_usage: bool) -> str:

@@ -143,6 +143,19 @@ __device__ __forceinline__ void unroll(F&& f) {
     unroll_seq(f, std::make_integer_sequence<int, N>{});
 }
 
+// Block b's tile in an order of tile-row groups of group_m (a group's tiles
+// column by column), each XCD walking a contiguous run of it.
+__device__ __forceinline__ void grouped_tile(int b, int tiles_m, int tiles_n, int group_m, int* tm, int* tn) {
+    const int logical = xcd_contiguous(b, tiles_m * tiles_n);
+    const int group_size = group_m * tiles_n;
+    const int g = logical / group_size;
+    const int first_m = g * group_m;
+    const int gm = min(tiles_m - first_m, group_m);
+    const int in_g = logical - g * group_size;
+    *tm = first_m + in_g % gm;
+    *tn = in_g / gm;
+}
+
 }  // namespace
 
 }  // namespace gemmf32

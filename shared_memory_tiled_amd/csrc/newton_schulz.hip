@@ -7,7 +7,21 @@
 //
 // Each step applies the odd polynomial a s + b s^3 + c s^5 to every singular
 // value s of X and keeps the singular vectors.
+//
+// Three products per step, on binary16 matrix instructions with binary32
+// sums.  Every matrix is kept as two binary16 planes (newton_schulz_product.h;
+// 22 bits).  Binary32 and binary16 results take the products of both planes
+// (three matrix instructions for one: the product of the low planes, 2^-22 of
+// the whole, is left out), whose error is below a binary32 product's at a
+// third of the 16-bit rate instead of a sixteenth.  Bfloat16 results take the
+// product of the high planes alone, X itself and the diagonals of A and B
+// still in 22 and 24 bits: measured against binary64 their error, 5e-4 to
+// 7e-4 of an entry's root mean square, is a third of the result's own
+// rounding (1.7e-3), where products of bfloat16 factors give 1.4e-2 and more.
+// Scales are powers of two from bounds on the singular values, so no plane
+// overflows.
 #include "epilogue.h"
+#include "newton_schulz_product.h"
 
 namespace gemmf32 {
 
@@ -16,60 +30,137 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kNormBlocks = 256;
 
-// Partial sums of squares in binary64 (no overflow or underflow for any
-// binary32 input), one per block and matrix.
+// The sum of squares in binary64 (no overflow or underflow for any binary32
+// input): block b of matrix blockIdx.y takes rows b, b + 256, ...
 template <int TYPE>
 __global__ __launch_bounds__(kThreads)
-void square_sum_kernel(NewtonSchulzArgs a, double* partials) {
+void ns_square_sum_kernel(NewtonSchulzArgs a, double* partials) {
     __shared__ double slots[kThreads];
     const int64_t base = (int64_t)blockIdx.y * a.stride_g;
     double s = 0.0;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x)
-        for (int c = threadIdx.x; c < a.cols; c += kThreads) {
-            float v[1];
-            load_values<TYPE>(a.G, base + r * a.ldg + c, 1, v);
-            s += (double)v[0] * v[0];
+    for (int64_t r = blockIdx.x; r < a.rows; r += kNormBlocks)
+        for (int c = 8 * threadIdx.x; c < a.cols; c += 8 * kThreads) {
+            float v[8];
+            load_values<TYPE>(a.G, base + r * a.ldg + c, a.cols - c, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += (double)v[e] * v[e];
         }
     slots[threadIdx.x] = s;
     for (int h = kThreads / 2; h > 0; h >>= 1) {
         __syncthreads();
         if ((int)threadIdx.x < h) slots[threadIdx.x] += slots[threadIdx.x + h];
     }
-    if (threadIdx.x == 0) partials[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = slots[0];
+    if (threadIdx.x == 0) partials[(int64_t)blockIdx.y * kNormBlocks + blockIdx.x] = slots[0];
 }
 
+// X_0's planes, padding included.  A norm that is no number or infinite
+// makes every entry NaN.
 template <int TYPE>
 __global__ __launch_bounds__(kThreads)
-void scale_kernel(NewtonSchulzArgs a, int64_t z, const double* partials, float* x) {
-    double s = 0.0;
-    for (int i = 0; i < kNormBlocks; ++i) s += partials[i];
-    const float scale = (float)(1.0 / (sqrt(s) + (double)a.eps));
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= a.cols) return;
-    float v[1];
-    load_values<TYPE>(a.G, z * a.stride_g + (int64_t)blockIdx.y * a.ldg + c, 1, v);
-    x[(int64_t)blockIdx.y * a.cols + c] = v[0] * scale;
+void ns_split_kernel(NewtonSchulzArgs a, const double* partials, float x_scale, uint16_t* x, int rp, int cp,
+                     int64_t stride) {
+    __shared__ double slots[kThreads];
+    slots[threadIdx.x] = partials[(int64_t)blockIdx.y * kNormBlocks + threadIdx.x];
+    static_assert(kThreads == kNormBlocks, "one partial per thread");
+    for (int h = kThreads / 2; h > 0; h >>= 1) {
+        __syncthreads();
+        if ((int)threadIdx.x < h) slots[threadIdx.x] += slots[threadIdx.x + h];
+    }
+    __syncthreads();
+    const double norm = sqrt(slots[0]);
+    const double scale = __builtin_isfinite(norm) ? (double)x_scale / (norm + (double)a.eps) : __builtin_nan("");
+    const int64_t base = (int64_t)blockIdx.y * a.stride_g;
+    const int chunks = cp / 8;
+    const int64_t total = (int64_t)rp * chunks;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+        const int r = (int)(i / chunks), c = 8 * (int)(i % chunks);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (r < a.rows && c < a.cols) {
+            load_values<TYPE>(a.G, base + (int64_t)r * a.ldg + c, a.cols - c, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < a.cols ? (float)(v[e] * scale) : 0.0f;
+        }
+        store_planes<8, true>(x + (int64_t)blockIdx.y * stride, (int64_t)r * cp + c, (int64_t)rp * cp, v);
+    }
 }
 
-// out = s u + t v over n values.
+// No step: the planes' values into the result.
 __global__ __launch_bounds__(kThreads)
-void combine_kernel(int64_t n, float s, const float* u, float t, const float* v, float* out) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i < n) out[i] = s * u[i] + t * v[i];
-}
-
-__global__ __launch_bounds__(kThreads)
-void write_kernel(NewtonSchulzArgs a, int64_t z, const float* x) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
+void ns_write_kernel(NewtonSchulzArgs a, float unscale, const uint16_t* x, int rp, int cp, int64_t stride) {
+    const int c = 8 * (blockIdx.x * kThreads + threadIdx.x);
     if (c >= a.cols) return;
-    float v[1] = {x[(int64_t)blockIdx.y * a.cols + c]};
-    store_values(a.type, a.out, z * a.stride_o + (int64_t)blockIdx.y * a.ldo + c, 1, v);
+    const int64_t z = blockIdx.z;
+    for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+        float v[8];
+        PlaneRun<8, true> run;
+        run.load(x + z * stride, r * cp + c, (int64_t)rp * cp);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = run.value(e) * unscale;
+        store_values(a.type, a.out, z * a.stride_o + r * a.ldo + c, a.cols - c, v);
+    }
 }
 
-hipError_t product(int op_a, int op_b, int M, int N, int K, const float* A, int64_t lda, const float* B, int64_t ldb,
-                   float* C, hipStream_t s) {
-    const GemmArgs p{M, N, K, A, lda, B, ldb, C, N};
-    return launch_mfma(p, s, mfma_pick_config(M, N, K), op_a, op_b);
+// Workspace: partial norms, X's planes twice, S's and T's planes, d and e.
+struct Layout {
+    int rp, cp, mp;
+    int64_t x_stride, s_stride;               // elements per matrix
+    int64_t x0, x1, s, t, d, e, bytes;        // byte offsets
+};
+int pad64(int n) { return (n + 63) / 64 * 64; }
+Layout layout(const NewtonSchulzArgs& a) {
+    Layout l;
+    l.rp = pad64(a.rows);
+    l.cp = pad64(a.cols);
+    l.mp = l.rp < l.cp ? l.rp : l.cp;
+    l.x_stride = 2 * (int64_t)l.rp * l.cp;
+    l.s_stride = 2 * (int64_t)l.mp * l.mp;
+    l.x0 = 8 * (int64_t)kNormBlocks * a.batch;
+    l.x1 = l.x0 + 2 * l.x_stride * a.batch;
+    l.s = l.x1 + 2 * l.x_stride * a.batch;
+    l.t = l.s + 2 * l.s_stride * a.batch;
+    l.d = l.t + 2 * l.s_stride * a.batch;
+    l.e = l.d + 4 * (int64_t)l.mp * a.batch;
+    l.bytes = l.e + 4 * (int64_t)l.mp * a.batch;
+    return l;
+}
+
+// The largest power of two that keeps values up to `bound` at most 2^15.
+float plane_scale(double bound) { return (float)ldexp(1.0, 15 - (int)ceil(log2(fmax(bound, 1e-30)))); }
+
+// The tiles a product runs on: those of the smallest estimated time, in us
+// from the following measurements (MI355X, each kernel alone).
+//   Large tiles: every round of 256 blocks takes the K loop, `slow` per 64-deep
+//   phase once all CUs are busy (the clock drops; `fast` up to half of them),
+//   and `fixed` for start and epilogue by stage.  4096^2, one term: Gram 87 /
+//   71 / 83 us on 256 / 192 / 160 tiles (136, 253, 351 of them), update 118 /
+//   143 / 178.
+//   64 tiles, K split over the waves: 3.3 + 0.0037 K per round.  1024^2, one
+//   term: Gram 7.0 against 19.3 us on 160 tiles; 4096^2 310 against 71.
+int pick_tile(const NsProduct& p) {
+    static const struct { int tile; double fast, slow, fixed[3]; } kWide[] = {
+        {256, 1.03, 1.45, {14.6, 22.0, 21.5}}, {192, 0.72, 0.89, {11.3, 14.8, 13.0}}, {160, 0.62, 0.73, {10.4, 14.5, 10.5}}};
+    const double k = (double)p.K * p.terms;
+    const int64_t t64 = (int64_t)(p.M / 64) * (p.N / 64) * p.batch;
+    int best = 64;
+    double best_time = (double)((t64 + 255) / 256) * (3.3 + 0.0037 * k);
+    const int stage = p.stage < kUpdate ? p.stage : kUpdate;
+    for (const auto& w : kWide) {
+        const int64_t tm = ceil_div(p.M, w.tile), tn = ceil_div(p.N, w.tile);
+        const int64_t tiles = (stage < kUpdate ? tm * (tm + 1) / 2 : tm * tn) * p.batch;
+        const double busy = fmin(1.0, fmax(0.0, (double)tiles / 128.0 - 1.0));
+        const double phase = w.fast + (w.slow - w.fast) * busy;
+        const double time = (double)((tiles + 255) / 256) * (phase * k / 64.0 + w.fixed[stage]);
+        if (time < best_time) {
+            best_time = time;
+            best = w.tile;
+        }
+    }
+    return best;
+}
+
+hipError_t launch_product(const NsProduct& p, int op_a, hipStream_t s) {
+    const int tile = pick_tile(p);
+    return tile == 64 ? launch_ns_ksplit(p, op_a, s) : launch_ns_wide(p, tile, op_a, s);
 }
 
 }  // namespace
@@ -100,52 +191,138 @@ bool newton_schulz_bounds(int steps, double a, double b, double c, double* bound
 }
 
 int64_t newton_schulz_workspace(const NewtonSchulzArgs& a) {
-    const int64_t m = a.rows < a.cols ? a.rows : a.cols;
-    return 8 * kNormBlocks * a.batch + 4 * (2 * (int64_t)a.rows * a.cols + 2 * m * m);
+    // both planes of a matrix, with a tile's overhang, within 2^31 bytes
+    const Layout l = layout(a);
+    if (4 * ((int64_t)l.rp + 256) * (l.cp + 256) >= (1ll << 31) || a.batch > 65535) return -1;
+    return l.bytes;
 }
 
 hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, void* workspace, hipStream_t s) {
-    double* const partials = static_cast<double*>(workspace);
-    float* const x = reinterpret_cast<float*>(partials + kNormBlocks * a.batch);
-    const int64_t mn = (int64_t)a.rows * a.cols;
-    const int m = a.rows < a.cols ? a.rows : a.cols, n = a.rows < a.cols ? a.cols : a.rows;
-    const bool wide = a.rows <= a.cols;
-    float* const y = x + mn;
-    float* const A = y + mn;
-    float* const B = A + (int64_t)m * m;
-    if (a.batch > 65535 || a.rows > 65535) return hipErrorInvalidValue;
-    const dim3 ngrid(kNormBlocks, (unsigned)a.batch);
-    if (a.type == 0) hipLaunchKernelGGL(square_sum_kernel<0>, ngrid, dim3(kThreads), 0, s, a, partials);
-    else if (a.type == 1) hipLaunchKernelGGL(square_sum_kernel<1>, ngrid, dim3(kThreads), 0, s, a, partials);
-    else hipLaunchKernelGGL(square_sum_kernel<2>, ngrid, dim3(kThreads), 0, s, a, partials);
-    hipError_t e = hipGetLastError();
-    const dim3 rgrid(ceil_div(a.cols, kThreads), a.rows);
-    auto blocks = [](int64_t n_) { return dim3((unsigned)((n_ + kThreads - 1) / kThreads)); };
-    for (int64_t z = 0; z < a.batch && e == hipSuccess; ++z) {
-        const double* pz = partials + kNormBlocks * z;
-        if (a.type == 0) hipLaunchKernelGGL(scale_kernel<0>, rgrid, dim3(kThreads), 0, s, a, z, pz, x);
-        else if (a.type == 1) hipLaunchKernelGGL(scale_kernel<1>, rgrid, dim3(kThreads), 0, s, a, z, pz, x);
-        else hipLaunchKernelGGL(scale_kernel<2>, rgrid, dim3(kThreads), 0, s, a, z, pz, x);
-        e = hipGetLastError();
-        const int ld = a.cols;
-        for (int k = 0; k < a.steps && e == hipSuccess; ++k) {
-            e = wide ? product(0, 1, m, m, n, x, ld, x, ld, A, s) : product(1, 0, m, m, n, x, ld, x, ld, A, s);
-            if (e == hipSuccess) e = product(0, 0, m, m, m, A, m, A, m, B, s);
-            if (e != hipSuccess) return e;
-            hipLaunchKernelGGL(combine_kernel, blocks((int64_t)m * m), dim3(kThreads), 0, s, (int64_t)m * m, a.b, A,
-                               a.c, B, B);
-            e = hipGetLastError();
-            if (e == hipSuccess)
-                e = wide ? product(0, 0, m, n, m, B, m, x, ld, y, s) : product(0, 0, n, m, m, x, ld, B, m, y, s);
-            if (e != hipSuccess) return e;
-            hipLaunchKernelGGL(combine_kernel, blocks(mn), dim3(kThreads), 0, s, mn, a.a, x, 1.0f, y, x);
-            e = hipGetLastError();
-        }
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(write_kernel, rgrid, dim3(kThreads), 0, s, a, z, x);
-        e = hipGetLastError();
+    const Layout l = layout(a);
+    char* const ws = static_cast<char*>(workspace);
+    double* const partials = reinterpret_cast<double*>(ws);
+    uint16_t* x = reinterpret_cast<uint16_t*>(ws + l.x0);
+    uint16_t* x_next = reinterpret_cast<uint16_t*>(ws + l.x1);
+    uint16_t* const S = reinterpret_cast<uint16_t*>(ws + l.s);
+    uint16_t* const T = reinterpret_cast<uint16_t*>(ws + l.t);
+    float* const d = reinterpret_cast<float*>(ws + l.d);
+    float* const e = reinterpret_cast<float*>(ws + l.e);
+    const unsigned batch = (unsigned)a.batch;
+    const dim3 block(kThreads), ngrid(kNormBlocks, batch);
+    const int64_t chunks = (int64_t)l.rp * l.cp / 8 / kThreads;          // cp is a multiple of 64
+    const dim3 sgrid((unsigned)(chunks < 1 ? 1 : chunks > 2048 ? 2048 : chunks), batch);
+    float sx = plane_scale(a.bounds[0]);
+    if (a.type == 0) {
+        hipLaunchKernelGGL(ns_square_sum_kernel<0>, ngrid, block, 0, s, a, partials);
+        hipLaunchKernelGGL(ns_split_kernel<0>, sgrid, block, 0, s, a, partials, sx, x, l.rp, l.cp, l.x_stride);
+    } else if (a.type == 1) {
+        hipLaunchKernelGGL(ns_square_sum_kernel<1>, ngrid, block, 0, s, a, partials);
+        hipLaunchKernelGGL(ns_split_kernel<1>, sgrid, block, 0, s, a, partials, sx, x, l.rp, l.cp, l.x_stride);
+    } else {
+        hipLaunchKernelGGL(ns_square_sum_kernel<2>, ngrid, block, 0, s, a, partials);
+        hipLaunchKernelGGL(ns_split_kernel<2>, sgrid, block, 0, s, a, partials, sx, x, l.rp, l.cp, l.x_stride);
     }
-    return e;
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    if (a.steps == 0) {
+        hipLaunchKernelGGL(ns_write_kernel, dim3(ceil_div(a.cols, 8 * kThreads), a.rows < 1024 ? a.rows : 1024, batch),
+                           block, 0, s, a, 1.0f / sx, x, l.rp, l.cp, l.x_stride);
+        return hipGetLastError();
+    }
+    const bool wide = a.rows <= a.cols;
+    const int64_t x_plane = l.x_stride / 2, s_plane = l.s_stride / 2;
+    const int terms = a.type == 0 ? 1 : 3;
+    for (int k = 0; k < a.steps; ++k) {
+        const double bx = a.bounds[k], ba = bx * bx, bt = (fabs((double)a.b) + fabs((double)a.c) * ba) * ba * 1.01;
+        const float ss = plane_scale(ba), st = plane_scale(bt);
+        const float sx_next = plane_scale(a.bounds[k + 1]);
+        NsProduct g{};
+        g.batch = (int)a.batch;
+        g.terms = terms;
+        g.a = a.a;
+        g.b = a.b;
+        g.c = a.c;
+        g.diag_n = l.mp;
+        g.rows = a.rows;
+        g.cols = a.cols;
+        // S, d
+        g.stage = kGram;
+        g.M = g.N = l.mp;
+        g.K = wide ? l.cp : l.rp;
+        g.A = g.B = x;
+        g.lda = g.ldb = l.cp;
+        g.plane_a = g.plane_b = x_plane;
+        g.stride_a = g.stride_b = l.x_stride;
+        g.unscale = 1.0f / sx / sx;
+        g.diag_out = d;
+        g.out = S;
+        g.ldo = l.mp;
+        g.plane_o = s_plane;
+        g.stride_o = l.s_stride;
+        g.out_scale = ss;
+        if ((err = launch_product(g, wide ? 0 : 1, s)) != hipSuccess) return err;
+        // T, e
+        g.stage = kPoly;
+        g.K = l.mp;
+        g.A = g.B = S;
+        g.lda = g.ldb = l.mp;
+        g.plane_a = g.plane_b = s_plane;
+        g.stride_a = g.stride_b = l.s_stride;
+        g.unscale = 1.0f / ss / ss;
+        g.in = S;
+        g.ldi = l.mp;
+        g.plane_i = s_plane;
+        g.stride_i = l.s_stride;
+        g.in_unscale = 1.0f / ss;
+        g.diag_in = d;
+        g.diag_out = e;
+        g.out = T;
+        g.out_scale = st;
+        if ((err = launch_product(g, 0, s)) != hipSuccess) return err;
+        // X
+        g.stage = wide ? kUpdate : kUpdateColumns;
+        g.M = l.rp;
+        g.N = l.cp;
+        g.K = l.mp;
+        if (wide) {
+            g.B = x;
+            g.ldb = l.cp;
+            g.plane_b = x_plane;
+            g.stride_b = l.x_stride;
+            g.A = T;
+        } else {
+            g.A = x;
+            g.lda = l.cp;
+            g.plane_a = x_plane;
+            g.stride_a = l.x_stride;
+            g.B = T;
+        }
+        g.unscale = 1.0f / st / sx;
+        g.in = x;
+        g.ldi = l.cp;
+        g.plane_i = x_plane;
+        g.stride_i = l.x_stride;
+        g.in_unscale = 1.0f / sx;
+        g.diag_in = e;
+        g.diag_out = nullptr;
+        g.out = x_next;
+        g.ldo = l.cp;
+        g.plane_o = x_plane;
+        g.stride_o = l.x_stride;
+        g.out_scale = sx_next;
+        if (k == a.steps - 1) {
+            g.final_out = a.out;
+            g.final_type = a.type;
+            g.final_ld = a.ldo;
+            g.final_stride = a.stride_o;
+        }
+        if ((err = launch_product(g, 0, s)) != hipSuccess) return err;
+        uint16_t* const swap = x;
+        x = x_next;
+        x_next = swap;
+        sx = sx_next;
+    }
+    return hipSuccess;
 }
 
 }  // namespace gemmf32

@@ -1,0 +1,145 @@
+// newton_schulz_product.h -- one product of a Newton-Schulz step: its
+// description and what happens to its entries (shared by the kernels on large
+// and on small tiles; not part of the public interface).
+//
+// Matrices are kept as two planes of binary16 values, high and low, whose sum
+// times a power of two is the entry (22 bits; `plane` elements apart).  Sizes
+// are padded to multiples of 64 with zeros, which the steps keep.  The two
+// symmetric matrices are kept without their diagonal, which is a binary32
+// vector of its own: near the end it is the large part of them, and the
+// off-diagonal entries' rounding matters the less.
+//
+//   kGram    D + S = X X^T (or X^T X)           S: zero diagonal
+//   kPoly    E + T = b (D + S) + c (D + S)^2, the product being S S:
+//            (D + S)^2 = S S + (d_i + d_j) S_ij + d_i^2 on the diagonal
+//   kUpdate, kUpdateColumns   X <- (a + e) X + T X, e of the row;
+//            X <- X (a + e) + X T, e of the column
+#pragma once
+
+#include "mfma16_common.h"
+
+namespace gemmf32 {
+
+enum { kGram = 0, kPoly = 1, kUpdate = 2, kUpdateColumns = 3 };
+
+struct NsProduct {
+    int M, N, K, batch;                       // padded sizes of the product
+    int stage;                                // kGram, kPoly, kUpdate, kUpdateColumns
+    int terms;                                // 1: high planes only, 3: see WideCore
+    const uint16_t* A; int64_t lda, plane_a, stride_a;      // factors (stride: from matrix to matrix)
+    const uint16_t* B; int64_t ldb, plane_b, stride_b;
+    float unscale;                            // product of the factors' scales
+    const uint16_t* in; int64_t ldi, plane_i, stride_i;     // kPoly: S; updates: X
+    float in_unscale;
+    const float* diag_in; float* diag_out;    // one vector of diag_n per matrix
+    int diag_n;
+    float a, b, c;
+    uint16_t* out; int64_t ldo, plane_o, stride_o;          // planes, or (final_out) the caller's matrix
+    float out_scale;
+    void* final_out; int final_type; int64_t final_ld, final_stride;
+    int rows, cols;                           // of final_out
+};
+
+// Tiles of 256, 192 or 160 (newton_schulz.hip) and of 64 with K split over
+// the waves (newton_schulz_ksplit.hip).  op_a: kGram of X^T X (the stage
+// says the rest of how the factors are stored).
+hipError_t launch_ns_wide(const NsProduct& p, int bt, int op_a, hipStream_t s);
+hipError_t launch_ns_ksplit(const NsProduct& p, int op_a, hipStream_t s);
+
+#ifdef __HIPCC__
+namespace {
+
+typedef _Float16 half_t;
+
+// W consecutive plane values as loaded, and their value over the scale.
+template <int W, bool LOW>
+struct PlaneRun {
+    half_t h[W], l[LOW ? W : 1];
+    __device__ __forceinline__ void load(const uint16_t* base, int64_t index, int64_t plane) {
+        __builtin_memcpy(h, base + index, sizeof(h));
+        if constexpr (LOW) __builtin_memcpy(l, base + plane + index, sizeof(l));
+    }
+    __device__ __forceinline__ float value(int e) const { return LOW ? (float)h[e] + (float)l[e] : (float)h[e]; }
+};
+// The plane, or both planes, of W scaled values.
+template <int W, bool LOW>
+__device__ __forceinline__ void store_planes(uint16_t* base, int64_t index, int64_t plane, const float (&v)[W]) {
+    half_t h[W], l[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        h[e] = (half_t)v[e];
+        l[e] = (half_t)(v[e] - (float)h[e]);
+    }
+    __builtin_memcpy(base + index, h, sizeof(h));
+    if constexpr (LOW) __builtin_memcpy(base + plane + index, l, sizeof(l));
+}
+
+// What a run of W columns reads: the plane values of S or X at its place and
+// the diagonal's entries of its row and columns.  S and T have a low plane
+// with TERMS = 3 only (without it S's rounding meets T's own, of the same
+// 11 bits).
+template <int STAGE, int TERMS, int W>
+struct NsRun {
+    static constexpr bool LOW = STAGE >= kUpdate || TERMS == 3;      // of the matrix read and of the one stored
+    PlaneRun<W, LOW> in;
+    float row_diag, col_diag[STAGE == kUpdate ? 1 : W];
+    __device__ __forceinline__ void load(const NsProduct& p, int z, int row, int col) {
+        if constexpr (STAGE == kGram) return;
+        in.load(p.in + (int64_t)z * p.stride_i, (int64_t)row * p.ldi + col, p.plane_i);
+        const float* const d = p.diag_in + (int64_t)z * p.diag_n;
+        if constexpr (STAGE != kUpdate) __builtin_memcpy(col_diag, d + col, sizeof(col_diag));
+        if constexpr (STAGE != kUpdateColumns) row_diag = d[row];
+    }
+    // v: the accumulated sums on entry; on return the scaled values that are
+    // stored (kGram, kPoly: for the mirrored store).
+    __device__ __forceinline__ void finish(const NsProduct& p, int z, int row, int col, float (&v)[W]) const {
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] *= p.unscale;
+        if constexpr (STAGE >= kUpdate) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float diag = STAGE == kUpdate ? row_diag : col_diag[STAGE == kUpdate ? 0 : e];
+                v[e] = __builtin_fmaf(p.a + diag, in.value(e) * p.in_unscale, v[e]);
+            }
+            if (p.final_out != nullptr) {
+                if (row < p.rows && col < p.cols)
+                    store_values(p.final_type, p.final_out,
+                                 (int64_t)z * p.final_stride + (int64_t)row * p.final_ld + col, p.cols - col, v);
+                return;
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] *= p.out_scale;
+        } else {
+            const int diag = row - col;                  // the run's entry on the diagonal, if any
+            if constexpr (STAGE == kPoly) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    const float s = in.value(e) * p.in_unscale;
+                    const float lin = diag == e ? row_diag : s;
+                    const float mix = diag == e ? row_diag * row_diag : (row_diag + col_diag[e]) * s;
+                    v[e] = __builtin_fmaf(p.c, v[e] + mix, p.b * lin);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                if (diag == e) {
+                    p.diag_out[(int64_t)z * p.diag_n + row] = v[e];
+                    v[e] = 0.0f;
+                }
+                v[e] *= p.out_scale;
+            }
+        }
+        store_planes<W, LOW>(p.out + (int64_t)z * p.stride_o, (int64_t)row * p.ldo + col, p.plane_o, v);
+    }
+};
+
+// The factors of matrix z.
+__device__ __forceinline__ Gemm16Args ns_factors(const NsProduct& p, int z) {
+    return Gemm16Args{p.M, p.N, p.K, p.A + (int64_t)z * p.stride_a, p.lda, p.B + (int64_t)z * p.stride_b, p.ldb,
+                      nullptr, 0};
+}
+
+}  // namespace
+#endif
+
+}  // namespace gemmf32
