@@ -129,22 +129,24 @@ float plane_scale(double bound) { return (float)ldexp(1.0, 15 - (int)ceil(log2(f
 
 // The tiles a product runs on: those of the smallest estimated time, in us
 // from the following measurements (MI355X, each kernel alone).
-//   Large tiles: every round of 256 blocks takes the K loop, `slow` per 64-deep
-//   phase once all CUs are busy (the clock drops; `fast` up to half of them),
-//   and `fixed` for start and epilogue by stage.  4096^2, one term: Gram 87 /
-//   71 / 83 us on 256 / 192 / 160 tiles (136, 253, 351 of them), update 118 /
-//   143 / 178.
-//   64 tiles, K split over the waves: 3.3 + 0.0037 K per round.  1024^2, one
-//   term: Gram 7.0 against 19.3 us on 160 tiles; 4096^2 310 against 71.
+//   A round of 256 blocks takes the K loop, `slow` per 64-deep phase once all
+//   CUs are busy (the clock drops, and the copies of the small tiles share
+//   the L2; `fast` up to half of them), and `fixed` for start and epilogue by
+//   stage.  4096^2, one term: Gram 86 / 70 / 82 / 129 us on 256 / 192 / 160 /
+//   128 tiles (136, 253, 351 and 528 of them), update 116 / 141 / 177 / 206;
+//   2048^2: update 61 / 42 / 38 / 32.
+//   64 tiles: 3.3 + 0.0037 K per round (1024^2: Gram 6.9 against 17 us on 128
+//   tiles; 4096^2 311 against 70).
 int pick_tile(const NsProduct& p) {
-    static const struct { int tile; double fast, slow, fixed[3]; } kWide[] = {
-        {256, 1.03, 1.45, {14.6, 22.0, 21.5}}, {192, 0.72, 0.89, {11.3, 14.8, 13.0}}, {160, 0.62, 0.73, {10.4, 14.5, 10.5}}};
+    static const struct { int tile; double fast, slow, fixed[3]; } kTiles[] = {
+        {256, 1.03, 1.45, {14.6, 22.0, 21.5}}, {192, 0.72, 0.89, {11.3, 14.8, 13.0}},
+        {160, 0.62, 0.73, {10.4, 14.5, 10.5}}, {128, 0.31, 0.50, {13.5, 15.5, 13.0}}};
     const double k = (double)p.K * p.terms;
     const int64_t t64 = (int64_t)(p.M / 64) * (p.N / 64) * p.batch;
     int best = 64;
     double best_time = (double)((t64 + 255) / 256) * (3.3 + 0.0037 * k);
     const int stage = p.stage < kUpdate ? p.stage : kUpdate;
-    for (const auto& w : kWide) {
+    for (const auto& w : kTiles) {
         const int64_t tm = ceil_div(p.M, w.tile), tn = ceil_div(p.N, w.tile);
         const int64_t tiles = (stage < kUpdate ? tm * (tm + 1) / 2 : tm * tn) * p.batch;
         const double busy = fmin(1.0, fmax(0.0, (double)tiles / 128.0 - 1.0));
@@ -160,7 +162,9 @@ int pick_tile(const NsProduct& p) {
 
 hipError_t launch_product(const NsProduct& p, int op_a, hipStream_t s) {
     const int tile = pick_tile(p);
-    return tile == 64 ? launch_ns_ksplit(p, op_a, s) : launch_ns_wide(p, tile, op_a, s);
+    if (tile == 64) return launch_ns_ksplit(p, op_a, s);
+    if (tile == 128) return launch_ns_ksplit128(p, op_a, s);
+    return launch_ns_wide(p, tile, op_a, s);
 }
 
 }  // namespace

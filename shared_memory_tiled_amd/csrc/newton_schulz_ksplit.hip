@@ -39,13 +39,15 @@ void ns_ksplit_kernel(NsProduct p, int tiles_m, int tiles_n) {
 template <int TERMS>
 void launch(const NsProduct& p, int op_a, unsigned blocks, int tm, int tn, hipStream_t s) {
     const dim3 g(blocks), b(256);
+    // S and T are symmetric: read mn-contiguous, in runs of 128 bytes instead
+    // of 64.
     if (p.stage == kGram && op_a)
         hipLaunchKernelGGL((ns_ksplit_kernel<false, false, TERMS, kGram>), g, b, 0, s, p, tm, tn);
     else if (p.stage == kGram) hipLaunchKernelGGL((ns_ksplit_kernel<true, true, TERMS, kGram>), g, b, 0, s, p, tm, tn);
-    else if (p.stage == kPoly) hipLaunchKernelGGL((ns_ksplit_kernel<true, true, TERMS, kPoly>), g, b, 0, s, p, tm, tn);
+    else if (p.stage == kPoly) hipLaunchKernelGGL((ns_ksplit_kernel<false, false, TERMS, kPoly>), g, b, 0, s, p, tm, tn);
     else if (p.stage == kUpdateColumns)
-        hipLaunchKernelGGL((ns_ksplit_kernel<true, true, TERMS, kUpdateColumns>), g, b, 0, s, p, tm, tn);
-    else hipLaunchKernelGGL((ns_ksplit_kernel<true, false, TERMS, kUpdate>), g, b, 0, s, p, tm, tn);
+        hipLaunchKernelGGL((ns_ksplit_kernel<true, false, TERMS, kUpdateColumns>), g, b, 0, s, p, tm, tn);
+    else hipLaunchKernelGGL((ns_ksplit_kernel<false, false, TERMS, kUpdate>), g, b, 0, s, p, tm, tn);
 }
 
 }  // namespace

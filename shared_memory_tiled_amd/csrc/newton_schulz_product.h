@@ -40,10 +40,11 @@ struct NsProduct {
     int rows, cols;                           // of final_out
 };
 
-// Tiles of 256, 192 or 160 (newton_schulz.hip) and of 64 with K split over
-// the waves (newton_schulz_ksplit.hip).  op_a: kGram of X^T X (the stage
+// Tiles of 256, 192 or 160 (newton_schulz_wide.hip), and of 128 or 64 with K
+// split over the waves (newton_schulz_ksplit128.hip, newton_schulz_ksplit.hip).  op_a: kGram of X^T X (the stage
 // says the rest of how the factors are stored).
 hipError_t launch_ns_wide(const NsProduct& p, int bt, int op_a, hipStream_t s);
+hipError_t launch_ns_ksplit128(const NsProduct& p, int op_a, hipStream_t s);
 hipError_t launch_ns_ksplit(const NsProduct& p, int op_a, hipStream_t s);
 
 #ifdef __HIPCC__
@@ -132,6 +133,15 @@ struct NsRun {
         store_planes<W, LOW>(p.out + (int64_t)z * p.stride_o, (int64_t)row * p.ldo + col, p.plane_o, v);
     }
 };
+
+// Tile t of a lower triangle of tiles, row by row.
+__device__ __forceinline__ void triangle_tile(int t, int* tm, int* tn) {
+    int m = (int)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while ((m + 1) * (m + 2) / 2 <= t) ++m;
+    while (m * (m + 1) / 2 > t) --m;
+    *tm = m;
+    *tn = t - m * (m + 1) / 2;
+}
 
 // The factors of matrix z.
 __device__ __forceinline__ Gemm16Args ns_factors(const NsProduct& p, int z) {

@@ -31,11 +31,8 @@ void ns_wide_kernel(NsProduct p, int tiles_m, int tiles_n, int tiles) {
     const int logical = xcd_contiguous((int)blockIdx.x, (int)gridDim.x);
     const int z = logical / tiles, t = logical - z * tiles;
     int tm, tn;
-    if constexpr (SYMMETRIC) {                    // tile t of the lower triangle, row by row
-        tm = (int)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-        while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
-        while (tm * (tm + 1) / 2 > t) --tm;
-        tn = t - tm * (tm + 1) / 2;
+    if constexpr (SYMMETRIC) {
+        triangle_tile(t, &tm, &tn);
     } else {
         const int group_size = kGroupM * tiles_n;
         const int g = t / group_size, first = g * kGroupM, gm = min(tiles_m - first, kGroupM), in_g = t - g * group_size;
