@@ -13,6 +13,8 @@
 
 #include "launch.h"
 
+#include <type_traits>
+
 namespace gemmf32 {
 
 namespace {
@@ -114,80 +116,172 @@ __device__ __forceinline__ float normal_cdf(float z, float* density) {
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 constexpr float kTanhC = 0.79788456080286536f, kTanhCubic = 0.044715f;
 
-__device__ __forceinline__ float activate(int act, float z) {
-    if (act == kActRelu) return z <= 0.0f ? 0.0f : z;
-    if (act == kActGelu) {
+template <int ACT>
+__device__ __forceinline__ float activate_one(float z) {
+    if constexpr (ACT == kActRelu) return z <= 0.0f ? 0.0f : z;
+    if constexpr (ACT == kActGelu) {
         float g;
         return z * normal_cdf(z, &g);
     }
-    if (act == kActGeluTanh) {
+    if constexpr (ACT == kActGeluTanh) {
         const float u2 = -2.0f * kTanhC * z * __builtin_fmaf(kTanhCubic * z, z, 1.0f);
         return z * fast_rcp(1.0f + fast_exp(u2));
     }
-    if (act == kActSilu) return z * fast_rcp(1.0f + fast_exp(-z));
+    if constexpr (ACT == kActSilu) return z * fast_rcp(1.0f + fast_exp(-z));
     return z;
 }
 
-__device__ __forceinline__ float activate_derivative(int act, float z) {
-    if (act == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    if (act == kActGelu) {
+template <int ACT>
+__device__ __forceinline__ float activate_derivative_one(float z) {
+    if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    if constexpr (ACT == kActGelu) {
         float g;
         const float cdf = normal_cdf(z, &g);
         return __builtin_fmaf(z * 0.39894228040143268f, g, cdf);
     }
-    if (act == kActGeluTanh) {
+    if constexpr (ACT == kActGeluTanh) {
         const float u2 = -2.0f * kTanhC * z * __builtin_fmaf(kTanhCubic * z, z, 1.0f);
         const float s = fast_rcp(1.0f + fast_exp(u2));
         // d u2 / dz = -2 c (1 + 3 0.044715 z^2); s' = -s (1 - s) du2
         const float du = 2.0f * kTanhC * __builtin_fmaf(3.0f * kTanhCubic * z, z, 1.0f);
         return __builtin_fmaf(z * du, s * (1.0f - s), s);
     }
-    if (act == kActSilu) {
+    if constexpr (ACT == kActSilu) {
         const float s = fast_rcp(1.0f + fast_exp(-z));
         return __builtin_fmaf(z, s * (1.0f - s), s);
     }
     return 1.0f;
 }
 
-// W consecutive columns from `col` of row `row` (inside C; columns past N are
-// skipped): v holds the product's entries on entry and, in gradient mode, d
-// on return (0 past N).
+// v = act(v), or v *= act'(z): one branch for the run, not one per value.
 template <int W>
-__device__ __forceinline__ void finish_entries(const EpilogueArgs& e, int row, int col, float (&v)[W]) {
-    const int valid = e.N - col;
-    const int64_t ci = (int64_t)row * e.ldc + col, zi = (int64_t)row * e.ldz + col;
-    float r[W];
-    if (e.residual != nullptr) load_values(e.c_type, e.residual, (int64_t)row * e.ldr + col, valid, r);
-    if (e.gradient) {
-        if (e.residual != nullptr) {
+__device__ __forceinline__ void activate(int act, float (&v)[W]) {
+    auto each = [&](auto a) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] += r[i];
+        for (int i = 0; i < W; ++i) v[i] = activate_one<decltype(a)::value>(v[i]);
+    };
+    if (act == kActRelu) each(std::integral_constant<int, kActRelu>{});
+    else if (act == kActGelu) each(std::integral_constant<int, kActGelu>{});
+    else if (act == kActGeluTanh) each(std::integral_constant<int, kActGeluTanh>{});
+    else if (act == kActSilu) each(std::integral_constant<int, kActSilu>{});
+}
+template <int W>
+__device__ __forceinline__ void times_derivative(int act, const float (&z)[W], float (&v)[W]) {
+    auto each = [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] *= activate_derivative_one<decltype(a)::value>(z[i]);
+    };
+    if (act == kActRelu) each(std::integral_constant<int, kActRelu>{});
+    else if (act == kActGelu) each(std::integral_constant<int, kActGelu>{});
+    else if (act == kActGeluTanh) each(std::integral_constant<int, kActGeluTanh>{});
+    else if (act == kActSilu) each(std::integral_constant<int, kActSilu>{});
+}
+
+// W stored values as loaded, of a type known at run time only.
+template <int W>
+struct RawRun {
+    unsigned w[W];
+    __device__ __forceinline__ void load(int type, const void* base, int64_t index, int valid) {
+        if (type == 2) {
+            const float* p = static_cast<const float*>(base) + index;
+            if (valid >= W) {
+                __builtin_memcpy(w, p, 4 * W);
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e) w[e] = e < valid ? __builtin_bit_cast(unsigned, p[e]) : 0u;
+            }
+        } else {
+            const uint16_t* p = static_cast<const uint16_t*>(base) + index;
+            if (valid >= W) {
+                __builtin_memcpy(w, p, 2 * W);
+            } else {
+#pragma unroll
+                for (int e = 0; e < W / 2; ++e)
+                    w[e] = (2 * e < valid ? (unsigned)p[2 * e] : 0u) |
+                           (2 * e + 1 < valid ? (unsigned)p[2 * e + 1] << 16 : 0u);
+            }
         }
-        if (e.act != kActNone) {
-            float z[W];
-            load_values(e.z_type, e.preact, zi, valid, z);
+    }
+    __device__ __forceinline__ void values(int type, float (&v)[W]) const {
+        if (type == 2) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] *= activate_derivative(e.act, z[i]);
+            for (int e = 0; e < W; ++e) v[e] = __builtin_bit_cast(float, w[e]);
+        } else if (type == 0) {
+#pragma unroll
+            for (int e = 0; e < W / 2; ++e) {
+                v[2 * e] = __builtin_bit_cast(float, w[e] << 16);
+                v[2 * e + 1] = __builtin_bit_cast(float, w[e] & 0xFFFF0000u);
+            }
+        } else {
+            _Float16 h[W];
+            __builtin_memcpy(h, w, 2 * W);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = (float)h[e];
         }
-#pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = i < valid ? v[i] : 0.0f;
-        if (e.C != nullptr) store_values(e.c_type, e.C, ci, valid, v);
-        return;
     }
-    if (e.bias != nullptr) {
-        float b[W];
-        load_values(e.bias_type, e.bias, col, valid, b);
+};
+
+// W consecutive columns from `col` of a row inside C (columns past N are
+// skipped): what the epilogue reads there, loaded ahead of its use, and the
+// epilogue.  GRADIENT: the mode, EpilogueArgs::gradient.
+template <int W, bool GRADIENT>
+struct EpilogueRun {
+    RawRun<W> residual;
+    unsigned preact[GRADIENT ? W / 2 : 1];
+    __device__ __forceinline__ void load(const EpilogueArgs& e, int row, int col) {
+        if (e.residual != nullptr) residual.load(e.c_type, e.residual, (int64_t)row * e.ldr + col, e.N - col);
+        if constexpr (GRADIENT) {
+            if (e.act != kActNone) {
+                RawRun<W> z;
+                z.load(e.z_type, e.preact, (int64_t)row * e.ldz + col, e.N - col);
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] += b[i];
+                for (int i = 0; i < W / 2; ++i) preact[i] = z.w[i];
+            }
+        }
     }
-    if (e.preact != nullptr) store_values(e.z_type, e.preact, zi, valid, v);
+    // v: the product's entries on entry; d on return in gradient mode (0 past
+    // N).  bias: the columns' (forward mode; zeros without one).
+    __device__ __forceinline__ void finish(const EpilogueArgs& e, int row, int col, const float (&bias)[W],
+                                           float (&v)[W]) const {
+        const int valid = e.N - col;
+        float r[W];
+        if (e.residual != nullptr) residual.values(e.c_type, r);
+        if constexpr (GRADIENT) {
+            if (e.residual != nullptr) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = activate(e.act, v[i]);
-    if (e.residual != nullptr) {
+                for (int i = 0; i < W; ++i) v[i] += r[i];
+            }
+            if (e.act != kActNone) {
+                RawRun<W> raw;
+                float z[W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] += r[i];
+                for (int i = 0; i < W / 2; ++i) raw.w[i] = preact[i];
+                raw.values(e.z_type, z);
+                times_derivative(e.act, z, v);
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = i < valid ? v[i] : 0.0f;
+            if (e.C != nullptr) store_values(e.c_type, e.C, (int64_t)row * e.ldc + col, valid, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] += bias[i];
+            if (e.preact != nullptr) store_values(e.z_type, e.preact, (int64_t)row * e.ldz + col, valid, v);
+            activate(e.act, v);
+            if (e.residual != nullptr) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[i] += r[i];
+            }
+            store_values(e.c_type, e.C, (int64_t)row * e.ldc + col, valid, v);
+        }
     }
-    store_values(e.c_type, e.C, ci, valid, v);
+};
+
+// The bias of W columns from `col` (zeros without one).
+template <int W>
+__device__ __forceinline__ void load_bias(const EpilogueArgs& e, int col, float (&b)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) b[i] = 0.0f;
+    if (e.bias != nullptr && col < e.N) load_values(e.bias_type, e.bias, col, e.N - col, b);
 }
 
 }  // namespace

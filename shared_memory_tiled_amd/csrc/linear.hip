@@ -8,13 +8,24 @@
 // "FC Layer = GEMM", "Backward"); what follows the product there is done
 // here before the entry leaves the chip.
 //
+// The product runs on the tiles of least estimated time (pick_tile, below),
+// on the few-row kernel up to 64 rows, or, split by rows, on 256 x 256 tiles
+// and smaller ones for the rest.  Factors those kernels do not take (an odd
+// width, leading dimension or K, a base of 2-byte alignment) are first copied
+// into the workspace with padded rows: two passes over a factor cost less
+// than the element-wise kernels would (999 x 1001 x 77 ..).  What is left
+// (factors of 2 GiB and more, K = 0) runs the library's product into a
+// binary32 matrix in the workspace and the epilogue as a pass over it.
+//
 // epilogue_kernel is the pass over finished sums: it adds the planes of a
 // product whose K was split over blocks (or reads a matrix of 16-bit
 // gradients), applies the epilogue and leaves column sums of its block of
 // rows, which column_sum_kernel adds in row order (deterministic).
 #include "epilogue.h"
+#include "linear_kernels.h"
 
 #include <limits.h>
+#include <math.h>
 
 namespace gemmf32 {
 
@@ -23,9 +34,9 @@ namespace {
 // Column tile of 128 (32 threads of 4 columns), 8 rows at a time,
 // `rows_per_block` rows per block.  IN: 0, 1 a matrix of 16-bit values of
 // that format, 2 `planes` binary32 planes of plane_stride floats, added in
-// order.
+// order, eight loads in flight.
 constexpr int kPassCols = 128;
-template <int IN>
+template <int IN, bool GRADIENT>
 __global__ __launch_bounds__(256)
 void epilogue_kernel(EpilogueArgs e, const void* in, int64_t ld, int planes, int64_t plane_stride,
                      int rows_per_block, float* partials) {
@@ -35,36 +46,49 @@ void epilogue_kernel(EpilogueArgs e, const void* in, int64_t ld, int planes, int
     const int last = min(e.M, first + rows_per_block);
     float sums[4] = {0.f, 0.f, 0.f, 0.f};
     if (col < e.N) {
+        float bias[4];
+        if constexpr (!GRADIENT) load_bias(e, col, bias);
         for (int row = first + tr; row < last; row += 8) {
+            EpilogueRun<4, GRADIENT> run;
+            run.load(e, row, col);
             float v[4] = {0.f, 0.f, 0.f, 0.f};
+            const int64_t at = (int64_t)row * ld + col;
             if constexpr (IN == 2) {
-                for (int s = 0; s < planes; ++s) {
-                    float w[4];
-                    load_values<2>(in, s * plane_stride + (int64_t)row * ld + col, e.N - col, w);
+                for (int s = 0; s < planes; s += 8) {
+                    float w[8][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] += w[i];
+                    for (int u = 0; u < 8; ++u)
+                        if (s + u < planes) load_values<2>(in, (s + u) * plane_stride + at, e.N - col, w[u]);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (s + u < planes) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] += w[u][i];
+                        }
                 }
             } else {
-                load_values<IN>(in, (int64_t)row * ld + col, e.N - col, v);
+                load_values<IN>(in, at, e.N - col, v);
             }
-            finish_entries(e, row, col, v);
-            if (e.gradient) {
+            run.finish(e, row, col, bias, v);
+            if constexpr (GRADIENT) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sums[i] += v[i];
             }
         }
     }
-    if (partials == nullptr) return;                     // the same for every thread
-    __shared__ float part[8][kPassCols];
+    if constexpr (GRADIENT) {
+        if (partials == nullptr) return;                     // the same for every thread
+        __shared__ float part[8][kPassCols];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[tr][4 * tc + i] = sums[i];
-    __syncthreads();
-    const int c = blockIdx.x * kPassCols + threadIdx.x;
-    if (threadIdx.x < kPassCols && c < e.N) {
-        float s = 0.f;
+        for (int i = 0; i < 4; ++i) part[tr][4 * tc + i] = sums[i];
+        __syncthreads();
+        const int c = blockIdx.x * kPassCols + threadIdx.x;
+        if (threadIdx.x < kPassCols && c < e.N) {
+            float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
-        partials[(int64_t)blockIdx.y * e.N + c] = s;
+            for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
+            partials[(int64_t)blockIdx.y * e.N + c] = s;
+        }
     }
 }
 
@@ -117,31 +141,264 @@ hipError_t launch_epilogue_pass(const EpilogueArgs& e, int in_type, const void* 
     if (gy > 65535) return hipErrorInvalidValue;
     const dim3 grid(ceil_div(e.N, kPassCols), (unsigned)gy);
     float* const part = e.bias_grad != nullptr ? partials : nullptr;
-    if (in_type == 0)
-        hipLaunchKernelGGL(epilogue_kernel<0>, grid, dim3(256), 0, s, e, in, ld, planes, plane_stride, rpb, part);
-    else if (in_type == 1)
-        hipLaunchKernelGGL(epilogue_kernel<1>, grid, dim3(256), 0, s, e, in, ld, planes, plane_stride, rpb, part);
-    else
-        hipLaunchKernelGGL(epilogue_kernel<2>, grid, dim3(256), 0, s, e, in, ld, planes, plane_stride, rpb, part);
+    auto launch = [&](auto in_c) {
+        constexpr int IN = decltype(in_c)::value;
+        if (e.gradient)
+            hipLaunchKernelGGL((epilogue_kernel<IN, true>), grid, dim3(256), 0, s, e, in, ld, planes, plane_stride, rpb, part);
+        else
+            hipLaunchKernelGGL((epilogue_kernel<IN, false>), grid, dim3(256), 0, s, e, in, ld, planes, plane_stride, rpb, part);
+    };
+    if (in_type == 0) launch(std::integral_constant<int, 0>{});
+    else if (in_type == 1) launch(std::integral_constant<int, 1>{});
+    else launch(std::integral_constant<int, 2>{});
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || part == nullptr) return err;
     return launch_column_sums((int)gy, e.N, part, e.bias_grad, s);
 }
 
-int64_t linear_workspace(const Gemm16Args& p, const EpilogueArgs& e, int, int) {
-    return align256(4 * (int64_t)p.M * p.N) + (e.bias_grad ? epilogue_pass_workspace(p.M, p.N) : 0);
+namespace {
+
+// ------------------------------------------------------- choice of kernel
+
+enum { kRows = 0, kTiles = 1, kGeneral = 2 };
+struct Plan {
+    int kind;
+    // kTiles: `tile` for the first `rows` rows of op(A) (all of them unless
+    // split), rest_tile for the others
+    int tile, rows, rest_tile;
+    int splits;                               // kRows: blocks along K
+    bool pack_a, pack_b;                      // factors copied into the workspace
+    int K;                                    // as the product runs it (padded if packed)
+    int64_t lda, ldb;                         // of the copies, where packed
+    int64_t a_bytes, b_bytes, main_bytes, part_rows;   // workspace: copies, planes, column sums
+};
+
+int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// Estimated time of an M x N x K product on `tile` x `tile` tiles, in us
+// (MI355X, each kernel alone).  A round of 256 blocks takes the K loop,
+// `slow` per 64-deep phase once all CUs are busy (`fast` up to half of them:
+// the clock drops, and the small tiles' copies share the L2), and `fixed` for
+// start and epilogue.  128 tiles copy k-contiguous factors in runs of 64
+// bytes: 0.09 more for each.
+double tile_time(int tile, int M, int N, int K, int k_contiguous) {
+    const double tiles = (double)ceil_div(M, tile) * ceil_div(N, tile);
+    const double rounds = ceil(tiles / 256.0);
+    if (tile == 64) return rounds * (3.3 + 0.0037 * K);
+    static const struct { int tile; double fast, slow, fixed; } kCost[] = {
+        {256, 1.03, 1.45, 16.0}, {192, 0.72, 0.89, 12.0}, {160, 0.62, 0.73, 11.0}, {128, 0.31, 0.42, 12.0}};
+    for (const auto& c : kCost)
+        if (c.tile == tile) {
+            const double busy = fmin(1.0, fmax(0.0, tiles / 128.0 - 1.0));
+            const double slow = c.slow + (tile == 128 ? 0.09 * k_contiguous : 0.0);
+            return rounds * ((c.fast + (slow - c.fast) * busy) * ceil_div(K, 64) + c.fixed);
+        }
+    return 1e30;
+}
+
+int pick_tile(int M, int N, int K, bool split_k, int k_contiguous, double* time) {
+    int best = 256;
+    *time = 1e30;
+    for (const int tile : {256, 192, 160, 128, 64}) {
+        if (tile <= 128 && !split_k) continue;
+        const double t = tile_time(tile, M, N, K, k_contiguous);
+        if (t < *time) {
+            *time = t;
+            best = tile;
+        }
+    }
+    return best;
+}
+
+Plan make_plan(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
+    Plan q{};
+    q.K = p.K;
+    q.lda = p.lda;
+    q.ldb = p.ldb;
+    if (p.M <= kLinearRowsMax && !op_a && p.K > 0 && p.K < (1 << 30)) {
+        q.kind = kRows;
+        q.splits = linear_rows_splits(p.M, p.N, p.K);
+        if (q.splits > 1 || e.gradient) q.main_bytes = align256(4 * (int64_t)q.splits * p.M * p.N);
+        q.part_rows = e.bias_grad ? 1 : 0;
+        return q;
+    }
+    // The tile kernels copy 4 bytes at a time at least: even leading
+    // dimensions, widths of mn-contiguous factors, and K where a factor is
+    // k-contiguous; the split-K ones 16 bytes along K.
+    const bool both_mn = op_a && !op_b;
+    const bool pad_k = !both_mn && p.K % 2 != 0;
+    q.pack_a = pad_k || (reinterpret_cast<uintptr_t>(p.A) & 3) != 0 || p.lda % 2 != 0 || (op_a && p.M % 2 != 0);
+    q.pack_b = pad_k || (reinterpret_cast<uintptr_t>(p.B) & 3) != 0 || p.ldb % 2 != 0 || (!op_b && p.N % 2 != 0);
+    if (pad_k) q.K = (int)(pad8(p.K) > INT_MAX ? 0 : pad8(p.K));
+    const int64_t a_rows = op_a ? q.K : p.M, b_rows = op_b ? p.N : q.K;
+    if (q.pack_a) q.lda = pad8(op_a ? p.M : q.K);
+    if (q.pack_b) q.ldb = pad8(op_b ? q.K : p.N);
+    q.kind = kTiles;
+    if (q.K == 0 || 2 * (a_rows + 256) * q.lda >= (1ll << 31) || 2 * (b_rows + 256) * q.ldb >= (1ll << 31)) {
+        q.kind = kGeneral;
+        q.pack_a = q.pack_b = false;
+        q.main_bytes = align256(4 * (int64_t)p.M * p.N);
+        q.part_rows = e.bias_grad ? 1 : 0;
+        return q;
+    }
+    if (q.pack_a) q.a_bytes = align256(2 * a_rows * q.lda);
+    if (q.pack_b) q.b_bytes = align256(2 * b_rows * q.ldb);
+    const bool split_k = both_mn || q.K % 8 == 0;
+    const int kc = (op_a ? 0 : 1) + (op_b ? 1 : 0);
+    double time;
+    q.tile = pick_tile(p.M, p.N, q.K, split_k, kc, &time);
+    q.rows = p.M;
+    q.rest_tile = q.tile;
+    // All rounds of 256 x 256 tiles but the last, the rows of that one on
+    // smaller tiles.
+    const int64_t tn = ceil_div(p.N, 256), tiles = ceil_div(p.M, 256) * tn, full = tiles / 256;
+    const int64_t rows = full > 0 ? 256 * (256 * full / tn) : 0;
+    if (rows > 0 && rows < p.M) {
+        double rest;
+        const int rest_tile = pick_tile(p.M - (int)rows, p.N, q.K, split_k, kc, &rest);
+        const double top = tile_time(256, (int)rows, p.N, q.K, kc);
+        if (top + rest < time) {
+            q.tile = 256;
+            q.rows = (int)rows;
+            q.rest_tile = rest_tile;
+        }
+    }
+    if (e.bias_grad)
+        q.part_rows = ceil_div(q.rows, q.tile) + (q.rows < p.M ? ceil_div(p.M - q.rows, q.rest_tile) : 0);
+    return q;
+}
+
+int64_t sums_bytes(const Plan& q, const EpilogueArgs& e) {
+    if (!e.bias_grad) return 0;
+    return q.kind == kTiles ? align256(4 * q.part_rows * e.N) : epilogue_pass_workspace(e.M, e.N);
+}
+
+// rows x cols 16-bit values (leading dimension ld_in, any alignment) into
+// out_rows x ld_out ones, zeros around them; block row y < blocks_a is the
+// first factor's.
+struct PackArgs {
+    const uint16_t* in; int64_t ld_in;
+    uint16_t* out; int64_t ld_out;
+    int rows, cols, out_rows;
+};
+__global__ __launch_bounds__(256)
+void pack_kernel(PackArgs a, PackArgs b, int blocks_a) {
+    const bool second = (int)blockIdx.y >= blocks_a;
+    const PackArgs& m = second ? b : a;
+    const int64_t first = (second ? blockIdx.y - blocks_a : blockIdx.y), step = second ? gridDim.y - blocks_a : blocks_a;
+    const int chunks = (int)(m.ld_out / 8);
+    const int64_t total = (int64_t)m.out_rows * chunks;
+    for (int64_t i = first * 256 + threadIdx.x; i < total; i += step * 256) {
+        const int r = (int)(i / chunks), c = 8 * (int)(i - (int64_t)r * chunks);
+        uint16_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (r < m.rows && c < m.cols) {
+            const uint16_t* q = m.in + (int64_t)r * m.ld_in + c;
+            if (c + 8 <= m.cols) {
+                __builtin_memcpy(v, q, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < m.cols) v[e] = q[e];
+            }
+        }
+        __builtin_memcpy(m.out + (int64_t)r * m.ld_out + c, v, 16);
+    }
+}
+
+hipError_t launch_tiles(int tile, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_a,
+                        int op_b, float* partials) {
+    switch (tile) {
+        case 256: return launch_linear_wide256(p, e, s, format, op_a, op_b, partials);
+        case 192: return launch_linear_wide192(p, e, s, format, op_a, op_b, partials);
+        case 160: return launch_linear_wide160(p, e, s, format, op_a, op_b, partials);
+        case 128: return launch_linear_ksplit128(p, e, s, format, op_a, op_b, partials);
+        default: return launch_linear_ksplit(p, e, s, format, op_a, op_b, partials);
+    }
+}
+
+// The epilogue of the rows from `row` on.
+EpilogueArgs rows_from(const EpilogueArgs& e, int row) {
+    EpilogueArgs r = e;
+    const int64_t size = e.c_type == 2 ? 4 : 2;
+    r.M = e.M - row;
+    r.C = static_cast<char*>(e.C) + size * row * e.ldc;
+    if (e.residual) r.residual = static_cast<const char*>(e.residual) + size * row * e.ldr;
+    if (e.preact) r.preact = static_cast<char*>(e.preact) + 2 * row * e.ldz;
+    return r;
+}
+
+}  // namespace
+
+int64_t linear_workspace(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
+    const Plan q = make_plan(p, e, op_a, op_b);
+    return q.a_bytes + q.b_bytes + q.main_bytes + sums_bytes(q, e);
 }
 
 hipError_t launch_linear(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_a, int op_b,
                          void* workspace) {
-    Gemm16Args q = p;
-    q.C = static_cast<float*>(workspace);
-    q.ldc = p.N;
-    const hipError_t err = (op_a || op_b) ? launch_mixed_op(q, s, format, op_a, op_b)
-                                          : launch_mixed(q, s, format, mixed_pick_config(q.M, q.N, q.K));
-    if (err != hipSuccess) return err;
-    float* const partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(4 * (int64_t)p.M * p.N));
-    return launch_epilogue_pass(e, 2, q.C, q.ldc, 1, 0, partials, s);
+    const Plan q = make_plan(p, e, op_a, op_b);
+    char* const ws = static_cast<char*>(workspace);
+    uint16_t* const a_copy = reinterpret_cast<uint16_t*>(ws);
+    uint16_t* const b_copy = reinterpret_cast<uint16_t*>(ws + q.a_bytes);
+    float* const main = reinterpret_cast<float*>(ws + q.a_bytes + q.b_bytes);
+    float* const partials = reinterpret_cast<float*>(ws + q.a_bytes + q.b_bytes + q.main_bytes);
+    hipError_t err;
+    if (q.kind == kRows) {
+        const bool planes = q.splits > 1 || e.gradient;
+        err = launch_linear_rows(p, e, s, format, op_b, q.splits, planes ? main : nullptr);
+        if (err != hipSuccess || !planes) return err;
+        return launch_epilogue_pass(e, 2, main, p.N, q.splits, (int64_t)p.M * p.N, partials, s);
+    }
+    if (q.kind == kGeneral) {
+        Gemm16Args r = p;
+        r.C = main;
+        r.ldc = p.N;
+        err = (op_a || op_b) ? launch_mixed_op(r, s, format, op_a, op_b)
+                             : launch_mixed(r, s, format, mixed_pick_config(r.M, r.N, r.K));
+        if (err != hipSuccess) return err;
+        return launch_epilogue_pass(e, 2, main, p.N, 1, 0, partials, s);
+    }
+    Gemm16Args r = p;
+    r.K = q.K;
+    if (q.pack_a || q.pack_b) {
+        const PackArgs a{p.A, p.lda, a_copy, q.lda, op_a ? p.K : p.M, op_a ? p.M : p.K, op_a ? q.K : p.M};
+        const PackArgs b{p.B, p.ldb, b_copy, q.ldb, op_b ? p.N : p.K, op_b ? p.K : p.N, op_b ? p.N : q.K};
+        auto blocks = [](const PackArgs& m) {
+            const int64_t n = ((int64_t)m.out_rows * (m.ld_out / 8) + 255) / 256;
+            return (int)(n > 1024 ? 1024 : n);
+        };
+        const int ba = q.pack_a ? blocks(a) : 0, bb = q.pack_b ? blocks(b) : 0;
+        hipLaunchKernelGGL(pack_kernel, dim3(1, (unsigned)(ba + bb)), dim3(256), 0, s, a, b, ba);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+        if (q.pack_a) {
+            r.A = a_copy;
+            r.lda = q.lda;
+        }
+        if (q.pack_b) {
+            r.B = b_copy;
+            r.ldb = q.ldb;
+        }
+    }
+    // An odd width of an mn-contiguous factor (then packed, zeros beside it)
+    // goes to the product as the even one above: its copies' range ends on a
+    // dword.  The epilogue keeps to e.M and e.N.
+    if (op_a) r.M = p.M + p.M % 2;
+    if (!op_b) r.N = p.N + p.N % 2;
+    float* const part = e.bias_grad ? partials : nullptr;
+    const bool split = q.rows < p.M;
+    Gemm16Args top = r;
+    EpilogueArgs te = e;
+    if (split) top.M = te.M = q.rows;
+    err = launch_tiles(q.tile, top, te, s, format, op_a, op_b, part);
+    if (err == hipSuccess && split) {
+        Gemm16Args rest = r;
+        rest.M = r.M - q.rows;
+        rest.A = r.A + (op_a ? (int64_t)q.rows : (int64_t)q.rows * r.lda);
+        err = launch_tiles(q.rest_tile, rest, rows_from(e, q.rows), s, format, op_a, op_b,
+                           part ? part + (int64_t)ceil_div(q.rows, q.tile) * p.N : nullptr);
+    }
+    if (err != hipSuccess || part == nullptr) return err;
+    return launch_column_sums((int)q.part_rows, p.N, part, e.bias_grad, s);
 }
 
 }  // namespace gemmf32

@@ -1,0 +1,146 @@
+// linear_wide_kernel.h -- the product with its epilogue on the scheduled 256,
+// 192 and 160 tiles (WideCore), instantiated per tile size in
+// linear_wide*.hip (device code; not part of the public interface).
+//
+// The K loop is mfma16_wide.hip's; then the accumulators go through LDS as
+// runs of 8 consecutive columns (staged_tile.h), the bias from LDS, residual
+// and pre-activation from memory a few runs ahead, so that a 16-bit result is
+// written in rows of 256 bytes and nothing passes through memory in binary32.
+// The column sums of the gradient mode stay in registers per lane (a lane's
+// runs repeat their columns every kSets), then are added over the wave's rows
+// and the block's two row halves through LDS, in a fixed order.
+#pragma once
+
+#include "epilogue.h"
+#include "linear_kernels.h"
+#include "mfma16_wide_core.h"
+#include "staged_tile.h"
+
+namespace gemmf32 {
+
+namespace {
+
+template <int FMT, bool KCA, bool KCB, int BT, bool GRADIENT>
+__global__ __launch_bounds__(256)
+void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, int group_m, float* partials) {
+    using Core = WideCore<FMT, KCA, KCB, BT>;
+    using Staged = StagedTile<Core::FM, Core::FN>;
+    using Run = EpilogueRun<8, GRADIENT>;
+    constexpr int PATCHES = 4 * Staged::PATCH * 4;                 // bytes; then BT floats
+    static_assert(PATCHES + 4 * BT <= Core::LDS_BYTES, "patches and bias");
+    constexpr int kSets = Staged::CHUNKS == 16 ? 1 : Staged::CHUNKS == 12 ? 3 : 5;
+    static_assert(64 * kSets % Staged::CHUNKS == 0, "columns repeat");
+    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    int tm, tn;
+    grouped_tile((int)blockIdx.x, tiles_m, tiles_n, group_m, &tm, &tn);
+    const int m0 = tm * BT, n0 = tn * BT;
+    float bias[1] = {0.0f};
+    if constexpr (!GRADIENT)
+        if ((int)threadIdx.x < BT) load_bias(e, n0 + (int)threadIdx.x, bias);
+    floatx4 acc[Core::FM][Core::FN];
+    Core::run(p, m0, n0, lds, acc);
+    GEMM16_PIN_ACCUMULATORS(acc, Core::FM, Core::FN);
+    __syncthreads();
+
+    float* const shared = reinterpret_cast<float*>(lds + PATCHES);
+    if constexpr (!GRADIENT) {
+        if ((int)threadIdx.x < BT) shared[threadIdx.x] = bias[0];
+        __syncthreads();
+    }
+    float* const patch = reinterpret_cast<float*>(lds) + wave * Staged::PATCH;
+    const int row0 = m0 + wave / 2 * Core::WM, wcol = wave % 2 * Core::WN, col0 = n0 + wcol;
+    float sums[GRADIENT ? kSets : 1][8];
+    if constexpr (GRADIENT) {
+#pragma unroll
+        for (int i = 0; i < kSets; ++i)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sums[i][c] = 0.0f;
+    }
+    Staged::template rows<false, Run>(
+        acc, patch, lane,
+        [&](int row, int col) __attribute__((always_inline)) {
+            Run run;
+            if (row0 + row < e.M && col0 + col < e.N) run.load(e, row0 + row, col0 + col);
+            return run;
+        },
+        [&](int it, int row, int col, float (&v)[8], const Run& run) __attribute__((always_inline)) {
+            if (row0 + row >= e.M || col0 + col >= e.N) return;
+            float b[8];
+            if constexpr (!GRADIENT) {
+                const floatx4 lo = *reinterpret_cast<const floatx4*>(shared + wcol + col);
+                const floatx4 hi = *reinterpret_cast<const floatx4*>(shared + wcol + col + 4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    b[c] = lo[c];
+                    b[4 + c] = hi[c];
+                }
+            }
+            run.finish(e, row0 + row, col0 + col, b, v);
+            if constexpr (GRADIENT) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) sums[it % kSets][c] += v[c];
+            }
+        },
+        [](int, int) {});
+    if constexpr (GRADIENT) {
+        if (partials == nullptr) return;                            // the same for every thread
+        // set i of lane l: columns 8 c .. of slot (64 i + l) / CHUNKS, c the rest
+        constexpr int SLOTS = 64 * kSets / Staged::CHUNKS;
+        static_assert(SLOTS <= 32, "slots fit in the patch");
+        wave_lds_fence();
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            const int id = 64 * i + lane, slot = id / Staged::CHUNKS, c = id - slot * Staged::CHUNKS;
+            floatx4* q = reinterpret_cast<floatx4*>(patch + slot * Staged::PITCH + 8 * c);
+            q[0] = floatx4{sums[i][0], sums[i][1], sums[i][2], sums[i][3]};
+            q[1] = floatx4{sums[i][4], sums[i][5], sums[i][6], sums[i][7]};
+        }
+        wave_lds_fence();
+        for (int c = lane; c < Core::WN; c += 64) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) s += patch[i * Staged::PITCH + c];
+            if (wave >= 2) shared[wcol + c] = s;                    // the lower rows' half
+            else patch[c] = s;
+        }
+        __syncthreads();
+        if (wave < 2)
+            for (int c = lane; c < Core::WN; c += 64)
+                if (col0 + c < e.N) partials[(int64_t)tm * e.N + col0 + c] = patch[c] + shared[wcol + c];
+    }
+}
+
+template <int FMT, bool KCA, bool KCB, int BT>
+void launch_linear_wide_ops(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int tm, int tn, int group_m,
+                            float* partials) {
+    const dim3 g((unsigned)(tm * tn)), b(256);
+    if (e.gradient)
+        hipLaunchKernelGGL((linear_wide_kernel<FMT, KCA, KCB, BT, true>), g, b, 0, s, p, e, tm, tn, group_m, partials);
+    else
+        hipLaunchKernelGGL((linear_wide_kernel<FMT, KCA, KCB, BT, false>), g, b, 0, s, p, e, tm, tn, group_m, partials);
+}
+
+template <int BT>
+hipError_t launch_linear_wide(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_a, int op_b,
+                              float* partials) {
+    constexpr int kGroupM = 4;                                     // as mfma16_wide.hip's launches
+    const int tm = ceil_div(p.M, BT), tn = ceil_div(p.N, BT);
+    if ((int64_t)tm * tn > 0x7FFFFFFFll / 256) return hipErrorInvalidValue;
+    switch (4 * (format ? 1 : 0) + 2 * (op_a ? 1 : 0) + (op_b ? 1 : 0)) {
+        case 0: launch_linear_wide_ops<0, true, false, BT>(p, e, s, tm, tn, kGroupM, partials); break;
+        case 1: launch_linear_wide_ops<0, true, true, BT>(p, e, s, tm, tn, kGroupM, partials); break;
+        case 2: launch_linear_wide_ops<0, false, false, BT>(p, e, s, tm, tn, kGroupM, partials); break;
+        case 3: launch_linear_wide_ops<0, false, true, BT>(p, e, s, tm, tn, kGroupM, partials); break;
+        case 4: launch_linear_wide_ops<1, true, false, BT>(p, e, s, tm, tn, kGroupM, partials); break;
+        case 5: launch_linear_wide_ops<1, true, true, BT>(p, e, s, tm, tn, kGroupM, partials); break;
+        case 6: launch_linear_wide_ops<1, false, false, BT>(p, e, s, tm, tn, kGroupM, partials); break;
+        default: launch_linear_wide_ops<1, false, true, BT>(p, e, s, tm, tn, kGroupM, partials); break;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace gemmf32
