@@ -6,9 +6,9 @@
 // runs of 8 consecutive columns (staged_tile.h), the bias from LDS, residual
 // and pre-activation from memory a few runs ahead, so that a 16-bit result is
 // written in rows of 256 bytes and nothing passes through memory in binary32.
-// The column sums of the gradient mode stay in registers per lane (a lane's
-// runs repeat their columns every kSets), then are added over the wave's rows
-// and the block's two row halves through LDS, in a fixed order.
+// The column sums of the gradient mode are taken column by column from what
+// each group of 32 rows leaves in LDS, then added over the block's two row
+// halves, in a fixed order.
 #pragma once
 
 #include "epilogue.h"
@@ -28,8 +28,6 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
     using Run = EpilogueRun<8, GRADIENT>;
     constexpr int PATCHES = 4 * Staged::PATCH * 4;                 // bytes; then BT floats
     static_assert(PATCHES + 4 * BT <= Core::LDS_BYTES, "patches and bias");
-    constexpr int kSets = Staged::CHUNKS == 16 ? 1 : Staged::CHUNKS == 12 ? 3 : 5;
-    static_assert(64 * kSets % Staged::CHUNKS == 0, "columns repeat");
     __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -51,22 +49,22 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
     }
     float* const patch = reinterpret_cast<float*>(lds) + wave * Staged::PATCH;
     const int row0 = m0 + wave / 2 * Core::WM, wcol = wave % 2 * Core::WN, col0 = n0 + wcol;
-    float sums[GRADIENT ? kSets : 1][8];
-    if constexpr (GRADIENT) {
-#pragma unroll
-        for (int i = 0; i < kSets; ++i)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) sums[i][c] = 0.0f;
-    }
-    Staged::template rows<false, Run>(
+    float sums[2] = {0.0f, 0.0f};                  // of columns lane, lane + 64 of the wave's
+    Staged::template rows<GRADIENT, Run>(
         acc, patch, lane,
         [&](int row, int col) __attribute__((always_inline)) {
             Run run;
             if (row0 + row < e.M && col0 + col < e.N) run.load(e, row0 + row, col0 + col);
             return run;
         },
-        [&](int it, int row, int col, float (&v)[8], const Run& run) __attribute__((always_inline)) {
-            if (row0 + row >= e.M || col0 + col >= e.N) return;
+        [&](int row, int col, float (&v)[8], const Run& run) __attribute__((always_inline)) {
+            if (row0 + row >= e.M || col0 + col >= e.N) {
+                if constexpr (GRADIENT) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] = 0.0f;        // for the column sums
+                }
+                return;
+            }
             float b[8];
             if constexpr (!GRADIENT) {
                 const floatx4 lo = *reinterpret_cast<const floatx4*>(shared + wcol + col);
@@ -78,37 +76,35 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
                 }
             }
             run.finish(e, row0 + row, col0 + col, b, v);
-            if constexpr (GRADIENT) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) sums[it % kSets][c] += v[c];
-            }
         },
-        [](int, int) {});
+        [&](int, int rows) __attribute__((always_inline)) {
+            if constexpr (GRADIENT) {
+                if (partials == nullptr) return;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = lane + 64 * h;
+                    if (c < Core::WN) {
+#pragma unroll 8
+                        for (int r = 0; r < rows; ++r) sums[h] += patch[r * Staged::PITCH + c];
+                    }
+                }
+            }
+        });
     if constexpr (GRADIENT) {
         if (partials == nullptr) return;                            // the same for every thread
-        // set i of lane l: columns 8 c .. of slot (64 i + l) / CHUNKS, c the rest
-        constexpr int SLOTS = 64 * kSets / Staged::CHUNKS;
-        static_assert(SLOTS <= 32, "slots fit in the patch");
-        wave_lds_fence();
-#pragma unroll
-        for (int i = 0; i < kSets; ++i) {
-            const int id = 64 * i + lane, slot = id / Staged::CHUNKS, c = id - slot * Staged::CHUNKS;
-            floatx4* q = reinterpret_cast<floatx4*>(patch + slot * Staged::PITCH + 8 * c);
-            q[0] = floatx4{sums[i][0], sums[i][1], sums[i][2], sums[i][3]};
-            q[1] = floatx4{sums[i][4], sums[i][5], sums[i][6], sums[i][7]};
-        }
-        wave_lds_fence();
-        for (int c = lane; c < Core::WN; c += 64) {
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < SLOTS; ++i) s += patch[i * Staged::PITCH + c];
-            if (wave >= 2) shared[wcol + c] = s;                    // the lower rows' half
-            else patch[c] = s;
+        if (wave >= 2) {                                            // the lower rows' half
+            shared[wcol + lane] = sums[0];
+            if (lane + 64 < Core::WN) shared[wcol + lane + 64] = sums[1];
         }
         __syncthreads();
-        if (wave < 2)
-            for (int c = lane; c < Core::WN; c += 64)
-                if (col0 + c < e.N) partials[(int64_t)tm * e.N + col0 + c] = patch[c] + shared[wcol + c];
+        if (wave < 2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = lane + 64 * h;
+                if (c < Core::WN && col0 + c < e.N)
+                    partials[(int64_t)tm * e.N + col0 + c] = sums[h] + shared[wcol + c];
+            }
+        }
     }
 }
 

@@ -55,7 +55,7 @@ void ns_wide_kernel(NsProduct p, int tiles_m, int tiles_n, int tiles) {
             if (row0 + row < p.M && col0 + col < p.N) run.load(p, z, row0 + row, col0 + col);
             return run;
         },
-        [&](int, int row, int col, float (&v)[8], const Run& run) __attribute__((always_inline)) {
+        [&](int row, int col, float (&v)[8], const Run& run) __attribute__((always_inline)) {
             if (row0 + row < p.M && col0 + col < p.N) run.finish(p, z, row0 + row, col0 + col, v);
         },
         [&](int first, int rows) __attribute__((always_inline)) {

@@ -10,9 +10,11 @@
 // per lane, so that every global access of the epilogue is 16 bytes or more
 // and a row of a 256 tile's wave is one run of 256 bytes of 16-bit values.
 //
-// What the epilogue reads from memory is loaded DEPTH runs ahead: with one
-// wave per SIMD nothing else hides the latency (a run loaded where it is
-// used cost a memory round trip each: 30 us of a 256 x 256 tile's 43).
+// What the epilogue reads from memory is loaded two runs ahead: with one wave
+// per SIMD nothing else hides the latency.  A group's runs are a rolled loop:
+// unrolled, a tile's epilogue is over 30 KB of code that each wave executes
+// once, and the instruction fetches set its time (256 x 256 tiles, bias only:
+// 26 us of fixed time per block unrolled).
 #pragma once
 
 #include "mfma16_common.h"
@@ -44,12 +46,10 @@ struct StagedTile {
     static constexpr int ITERS = CHUNKS / 2;              // runs of a lane in a full group
     static constexpr int LAST_ITERS = FM % 2 ? (CHUNKS + 3) / 4 : ITERS;
     static constexpr int RUNS = (GROUPS - 1) * ITERS + LAST_ITERS;
-    static constexpr int DEPTH = 8;
     static_assert(CHUNKS % 2 == 0, "whole runs in a full group");
 
-    // Run t of a lane: its `it` within the group (the same it has the same
-    // column in every group), row and column in the wave's span; false past
-    // the last row.
+    // Run t of a lane: its number within the group, row and column in the
+    // wave's span; false past the last row.
     __device__ static __forceinline__ bool run_at(int t, int lane, int* it, int* row, int* col) {
         const int g = t / ITERS;
         *it = t - g * ITERS;
@@ -60,23 +60,24 @@ struct StagedTile {
         return *row < 16 * FM;
     }
 
-    // For every run t: pre = load(row, col) ahead of time, then
-    // use(it, row, col, v, pre) with v[8] the columns col .. col + 7; what it
-    // leaves in v is written back to the patch if WRITE_BACK, and done(row0,
-    // rows) runs after the `rows` rows of a group from row0 (patch row 0).
+    // For every run: pre = load(row, col) two runs ahead, then use(row, col, v,
+    // pre) with v[8] the columns col .. col + 7; what it leaves in v is
+    // written back to the patch if WRITE_BACK, and done(row0, rows) runs after
+    // the `rows` rows of a group from row0 (patch row 0).
     template <bool WRITE_BACK, typename Pre, typename L, typename F, typename G>
     __device__ static __forceinline__ void rows(const floatx4 (&acc)[FM][FN], float* patch, int lane, L&& load, F&& use,
                                                 G&& done) {
         float* const wr = patch + 4 * (lane >> 4) * PITCH + (lane & 15);
-        Pre ahead[DEPTH];
-        auto fetch = [&](auto tc) __attribute__((always_inline)) {
-            constexpr int t = decltype(tc)::value;
+        auto fetch = [&](Pre& pre, int t) __attribute__((always_inline)) {
             int it, row, col;
-            if (run_at(t, lane, &it, &row, &col)) ahead[t % DEPTH] = load(row, col);
+            if (run_at(t, lane, &it, &row, &col)) pre = load(row, col);
         };
-        unroll<(DEPTH < RUNS ? DEPTH : RUNS)>([&](auto tc) __attribute__((always_inline)) { fetch(tc); });
+        Pre now, next, after;
+        fetch(now, 0);
+        fetch(next, 1);
         unroll<GROUPS>([&](auto gc) __attribute__((always_inline)) {
             constexpr int g = decltype(gc)::value;
+            constexpr int last = g == GROUPS - 1 ? LAST_ITERS : ITERS;
             wave_lds_fence();
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -88,23 +89,25 @@ struct StagedTile {
                             wr[(16 * b + r) * PITCH + 16 * j] = acc[2 * g + b < FM ? 2 * g + b : 0][j][r];
                 }
             wave_lds_fence();
-            unroll<(g == GROUPS - 1 ? LAST_ITERS : ITERS)>([&](auto ic) __attribute__((always_inline)) {
-                constexpr int t = g * ITERS + decltype(ic)::value;
+#pragma unroll 1
+            for (int i = 0; i < last; ++i) {
+                const int t = g * ITERS + i;
                 int it, row, col;
                 const bool inside = run_at(t, lane, &it, &row, &col);
-                Pre pre = ahead[t % DEPTH];
+                if (t + 2 < RUNS) fetch(after, t + 2);
                 if (inside) {
                     floatx4* q = reinterpret_cast<floatx4*>(patch + (row - 32 * g) * PITCH + col);
                     const floatx4 lo = q[0], hi = q[1];
                     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                    use(it, row, col, v, pre);
+                    use(row, col, v, now);
                     if constexpr (WRITE_BACK) {
                         q[0] = floatx4{v[0], v[1], v[2], v[3]};
                         q[1] = floatx4{v[4], v[5], v[6], v[7]};
                     }
                 }
-                if constexpr (t + DEPTH < RUNS) fetch(std::integral_constant<int, t + DEPTH>{});
-            });
+                now = next;
+                next = after;
+            }
             if constexpr (WRITE_BACK) wave_lds_fence();
             done(32 * g, 2 * g + 1 < FM ? 32 : 16);
         });
