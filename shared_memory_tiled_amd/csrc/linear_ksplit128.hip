@@ -1,5 +1,6 @@
 // linear_ksplit128.hip -- the product with its epilogue on 128 x 128 tiles
-// whose four waves split K (Ksplit128Core): runs of 4 columns.
+// whose four waves split K (Ksplit128Core): runs of 4 columns, a round of
+// what the epilogue reads loaded ahead of the exchange.
 #include "epilogue.h"
 #include "linear_kernels.h"
 #include "mfma16_ksplit128_core.h"
@@ -25,21 +26,26 @@ void linear_ksplit128_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tile
     GEMM16_PIN_ACCUMULATORS(acc, 8, 8);
     float bias[4];
     if constexpr (!GRADIENT) load_bias(e, col, bias);
-    using Run = EpilogueRun<4, GRADIENT>;
-    float sums[4] = {0.f, 0.f, 0.f, 0.f};
-    Core::template exchange_rolled<Run>(
-        acc, lds,
-        [&](Run& run, int r, int) __attribute__((always_inline)) {
-            if (m0 + r < e.M && col < e.N) run.load(e, m0 + r, col);
-        },
-        [&](int r, int, floatx4 sum, float*, const Run& run) __attribute__((always_inline)) {
-            if (m0 + r >= e.M || col >= e.N) return;
-            float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-            run.finish(e, m0 + r, col, bias, v);
-            if constexpr (GRADIENT) {
+    EpilogueRun<4, GRADIENT> run[8];
+    auto load = [&](int a, int it) __attribute__((always_inline)) {
+        const int row = m0 + 16 * (4 * a + w) + 2 * it + (lane >> 5);
+        if (row < e.M && col < e.N) run[it].load(e, row, col);
+    };
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sums[c] += v[c];
+    for (int it = 0; it < 8; ++it) load(0, it);
+    float sums[4] = {0.f, 0.f, 0.f, 0.f};
+    Core::exchange(
+        acc, lds,
+        [&](int a, int it, int r, int, floatx4 sum, float*) __attribute__((always_inline)) {
+            float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+            if (m0 + r < e.M && col < e.N) {
+                run[it].finish(e, m0 + r, col, bias, v);
+                if constexpr (GRADIENT) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sums[c] += v[c];
+                }
             }
+            if (a == 0) load(1, it);
         },
         [](int) {});
     if constexpr (GRADIENT) {

@@ -4,8 +4,10 @@
 //
 // The K loop is mfma16_wide.hip's; then the accumulators go through LDS as
 // runs of 8 consecutive columns (staged_tile.h), the bias from LDS, residual
-// and pre-activation from memory a few runs ahead, so that a 16-bit result is
-// written in rows of 256 bytes and nothing passes through memory in binary32.
+// and pre-activation from memory a group of rows ahead, so that a 16-bit
+// result is written in rows of 256 bytes and nothing passes through memory in
+// binary32.  (A binary32 residual in gradient mode is loaded where it is used:
+// slots for it would not fit.)
 // The column sums of the gradient mode are taken column by column from what
 // each group of 32 rows leaves in LDS, then added over the block's two row
 // halves, in a fixed order.
@@ -26,9 +28,14 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
     using Core = WideCore<FMT, KCA, KCB, BT>;
     using Staged = StagedTile<Core::FM, Core::FN>;
     using Run = EpilogueRun<8, GRADIENT>;
-    constexpr int PATCHES = 4 * Staged::PATCH * 4;                 // bytes; then BT floats
-    static_assert(PATCHES + 4 * BT <= Core::LDS_BYTES, "patches and bias");
-    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
+    // After the K loop: each wave's patch and slots, then BT floats.  Slots:
+    // the residual (forward: 16 or 32 bytes a run) or, in gradient mode, a
+    // 16-bit residual and the pre-activation.
+    constexpr int NV = 2;
+    constexpr int PATCHES = 4 * Staged::PATCH * 4, SLOTS = 4 * Staged::slot_bytes(NV);
+    constexpr int BYTES = PATCHES + SLOTS + 4 * BT > Core::LDS_BYTES ? PATCHES + SLOTS + 4 * BT : Core::LDS_BYTES;
+    static_assert(BYTES <= 163840, "LDS");
+    __shared__ __attribute__((aligned(16))) unsigned char lds[BYTES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int tm, tn;
@@ -42,7 +49,7 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
     GEMM16_PIN_ACCUMULATORS(acc, Core::FM, Core::FN);
     __syncthreads();
 
-    float* const shared = reinterpret_cast<float*>(lds + PATCHES);
+    float* const shared = reinterpret_cast<float*>(lds + PATCHES + SLOTS);
     if constexpr (!GRADIENT) {
         if ((int)threadIdx.x < BT) shared[threadIdx.x] = bias[0];
         __syncthreads();
@@ -50,14 +57,25 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
     float* const patch = reinterpret_cast<float*>(lds) + wave * Staged::PATCH;
     const int row0 = m0 + wave / 2 * Core::WM, wcol = wave % 2 * Core::WN, col0 = n0 + wcol;
     float sums[2] = {0.0f, 0.0f};                  // of columns lane, lane + 64 of the wave's
-    Staged::template rows<GRADIENT, Run>(
-        acc, patch, lane,
-        [&](int row, int col) __attribute__((always_inline)) {
-            Run run;
-            if (row0 + row < e.M && col0 + col < e.N) run.load(e, row0 + row, col0 + col);
-            return run;
+    u32x4* const slots = reinterpret_cast<u32x4*>(lds + PATCHES) + wave * (Staged::slot_bytes(NV) / 16);
+    const bool residual = e.residual != nullptr, wide = e.c_type == 2;
+    const bool late = GRADIENT && residual && wide;
+    const bool z = GRADIENT && e.act != kActNone;
+    Staged::template rows<GRADIENT, NV>(
+        acc, patch, slots, lane, (residual && !late) || z,
+        // whole runs; a run across column N is loaded where it is used
+        [&](int row, int col, u32x4 (&pre)[NV]) __attribute__((always_inline)) {
+            if (row0 + row >= e.M || col0 + col + 8 > e.N) return;
+            const int64_t at = (int64_t)(row0 + row) * e.ldr + col0 + col;
+            if (residual && !late) {
+                if (!GRADIENT && wide) __builtin_memcpy(pre, static_cast<const float*>(e.residual) + at, 32);
+                else __builtin_memcpy(pre, static_cast<const uint16_t*>(e.residual) + at, 16);
+            }
+            if (z)
+                __builtin_memcpy(&pre[1], static_cast<const uint16_t*>(e.preact) +
+                                              (int64_t)(row0 + row) * e.ldz + col0 + col, 16);
         },
-        [&](int row, int col, float (&v)[8], const Run& run) __attribute__((always_inline)) {
+        [&](int row, int col, float (&v)[8], const u32x4 (&pre)[NV]) __attribute__((always_inline)) {
             if (row0 + row >= e.M || col0 + col >= e.N) {
                 if constexpr (GRADIENT) {
 #pragma unroll
@@ -65,6 +83,11 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
                 }
                 return;
             }
+            Run run;
+            __builtin_memcpy(run.residual.w, pre, GRADIENT ? 16 : 32);
+            if constexpr (GRADIENT) __builtin_memcpy(run.preact, &pre[1], 16);
+            if (col0 + col + 8 > e.N) run.load(e, row0 + row, col0 + col);
+            else if (late) run.residual.load(2, e.residual, (int64_t)(row0 + row) * e.ldr + col0 + col, 8);
             float b[8];
             if constexpr (!GRADIENT) {
                 const floatx4 lo = *reinterpret_cast<const floatx4*>(shared + wcol + col);

@@ -306,60 +306,6 @@ struct Ksplit128Core {
             done(a);
         });
     }
-
-    // exchange() for a long `use`, in one rolled loop over both rounds
-    // (unrolled, its code is fetched once per use and the fetches set the
-    // time): pre = load(row, column) two runs ahead, then use(row, column, sum,
-    // slot, pre).
-    template <typename Pre, typename L, typename F, typename G>
-    __device__ static __forceinline__ void exchange_rolled(const floatx4 (&acc)[8][8], unsigned char* lds, L&& load,
-                                                           F&& use, G&& done) {
-        const int lane = threadIdx.x & 63;
-        const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        unsigned char* const wl = lds + w * WAVE_BYTES;
-        const int b16 = (lane >> 4) & 1;
-        float* const wbase_even = reinterpret_cast<float*>(wl) + 512 * (lane >> 4) + (lane & 15) + 16 * b16;
-        float* const wbase_odd = reinterpret_cast<float*>(wl) + 512 * (lane >> 4) + (lane & 15) - 16 * b16;
-        const int colq = 4 * (lane & 31);
-        float* const rbase = reinterpret_cast<float*>(lds) + 2048 * w + 128 * (lane >> 5);
-        auto row_of = [&](int t) __attribute__((always_inline)) {
-            return 16 * (4 * (t >> 3) + w) + 2 * (t & 7) + (lane >> 5);
-        };
-        Pre now, next, after;
-        load(now, row_of(0), colq);
-        load(next, row_of(1), colq);
-#pragma unroll 1
-        for (int t = 0; t < 16; ++t) {
-            const int a = t >> 3, it = t & 7;
-            if (it == 0) {
-                if (a == 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // round 0 is read
-                unroll<2>([&](auto ac) __attribute__((always_inline)) {
-                    constexpr int A_ = decltype(ac)::value;
-                    if (a == A_) {
-                        unroll<4>([&](auto vc) __attribute__((always_inline)) {
-                            constexpr int v = decltype(vc)::value;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    ((j & 1) ? wbase_odd : wbase_even)[2048 * v + 128 * r + 16 * j] =
-                                        acc[4 * A_ + v][j][r];
-                        });
-                    }
-                });
-                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            }
-            if (t + 2 < 16) load(after, row_of(t + 2), colq);
-            float* const q = rbase + 256 * it + (colq ^ (16 * ((it >> 1) & 1)));
-            floatx4 sum = *reinterpret_cast<const floatx4*>(q);
-#pragma unroll
-            for (int u = 1; u < 4; ++u) sum += *reinterpret_cast<const floatx4*>(q + (WAVE_BYTES / 4) * u);
-            use(row_of(t), colq, sum, q, now);
-            now = next;
-            next = after;
-            if (it == 7) done(a);
-        }
-    }
 };
 
 }  // namespace

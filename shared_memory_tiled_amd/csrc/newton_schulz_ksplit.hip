@@ -25,14 +25,22 @@ void ns_ksplit_kernel(NsProduct p, int tiles_m, int tiles_n) {
     const int z = logical / (tiles_m * tiles_n), t = logical - z * (tiles_m * tiles_n);
     const int m0 = 64 * (t % tiles_m), n0 = 64 * (t / tiles_m);
     Core::run(ns_factors(p, z), m0, n0, lds, p.plane_a, p.plane_b);
+    const int col = n0 + Core::sum_col(lane);
+    const float* const d = STAGE == kGram ? nullptr : p.diag_in + (int64_t)z * p.diag_n;
+    float col_diag[4], row_diag[4];
+    if constexpr (STAGE == kPoly || STAGE == kUpdateColumns) __builtin_memcpy(col_diag, d + col, sizeof(col_diag));
     NsRun<STAGE, TERMS, 4> run[4];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) run[it].load(p, z, m0 + Core::sum_row(w, lane, it), n0 + Core::sum_col(lane));
+    for (int it = 0; it < 4; ++it) {
+        const int row = m0 + Core::sum_row(w, lane, it);
+        if constexpr (STAGE == kPoly || STAGE == kUpdate) row_diag[it] = d[row];
+        run[it].load(p, z, row, col);
+    }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const floatx4 s = Core::sum4(lds, w, lane, it);
         float v[4] = {s[0], s[1], s[2], s[3]};
-        run[it].finish(p, z, m0 + Core::sum_row(w, lane, it), n0 + Core::sum_col(lane), v);
+        run[it].finish(p, z, m0 + Core::sum_row(w, lane, it), col, row_diag[it], col_diag, v);
     }
 }
 

@@ -35,15 +35,28 @@ void ns_ksplit128_kernel(NsProduct p, int tiles_m, int tiles) {
     floatx4 acc[8][8];
     Core::run(ns_factors(p, z), m0, n0, lds, acc, p.plane_a, p.plane_b);
     GEMM16_PIN_ACCUMULATORS(acc, 8, 8);
+    // What the epilogue reads, a round ahead of its use.
+    const int col = n0 + 4 * (lane & 31);
+    const float* const d = STAGE == kGram ? nullptr : p.diag_in + (int64_t)z * p.diag_n;
+    float col_diag[4], row_diag[8];
+    if constexpr (STAGE == kPoly || STAGE == kUpdateColumns)
+        if (col < p.N) __builtin_memcpy(col_diag, d + col, sizeof(col_diag));
+    Run run[8];
+    auto load = [&](int a, int it) __attribute__((always_inline)) {
+        const int row = m0 + 16 * (4 * a + w) + 2 * it + (lane >> 5);
+        if (row >= p.M || col >= p.N) return;
+        if constexpr (STAGE == kPoly || STAGE == kUpdate) row_diag[it] = d[row];
+        run[it].load(p, z, row, col);
+    };
+#pragma unroll
+    for (int it = 0; it < 8; ++it) load(0, it);
     const bool mirror = SYMMETRIC && tm != tn;
-    Core::template exchange_rolled<Run>(
+    Core::exchange(
         acc, lds,
-        [&](Run& run, int r, int c) __attribute__((always_inline)) {
-            if (m0 + r < p.M && n0 + c < p.N) run.load(p, z, m0 + r, n0 + c);
-        },
-        [&](int r, int c, floatx4 sum, float* slot, const Run& run) __attribute__((always_inline)) {
+        [&](int a, int it, int r, int, floatx4 sum, float* slot) __attribute__((always_inline)) {
             float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-            if (m0 + r < p.M && n0 + c < p.N) run.finish(p, z, m0 + r, n0 + c, v);
+            if (m0 + r < p.M && col < p.N) run[it].finish(p, z, m0 + r, col, row_diag[it], col_diag, v);
+            if (a == 0) load(1, it);
             if constexpr (SYMMETRIC) *reinterpret_cast<floatx4*>(slot) = floatx4{v[0], v[1], v[2], v[3]};
         },
         // The transposed store: two lanes on the 16 entries of a row of the

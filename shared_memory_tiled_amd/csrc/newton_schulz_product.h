@@ -75,31 +75,29 @@ __device__ __forceinline__ void store_planes(uint16_t* base, int64_t index, int6
     if constexpr (LOW) __builtin_memcpy(base + plane + index, l, sizeof(l));
 }
 
-// What a run of W columns reads: the plane values of S or X at its place and
-// the diagonal's entries of its row and columns.  S and T have a low plane
-// with TERMS = 3 only (without it S's rounding meets T's own, of the same
-// 11 bits).
+// A run of W columns: what it reads of S or X, and the epilogue.  S and T
+// have a low plane with TERMS = 3 only (without it S's rounding meets T's
+// own, of the same 11 bits).
 template <int STAGE, int TERMS, int W>
 struct NsRun {
     static constexpr bool LOW = STAGE >= kUpdate || TERMS == 3;      // of the matrix read and of the one stored
     PlaneRun<W, LOW> in;
-    float row_diag, col_diag[STAGE == kUpdate ? 1 : W];
     __device__ __forceinline__ void load(const NsProduct& p, int z, int row, int col) {
         if constexpr (STAGE == kGram) return;
         in.load(p.in + (int64_t)z * p.stride_i, (int64_t)row * p.ldi + col, p.plane_i);
-        const float* const d = p.diag_in + (int64_t)z * p.diag_n;
-        if constexpr (STAGE != kUpdate) __builtin_memcpy(col_diag, d + col, sizeof(col_diag));
-        if constexpr (STAGE != kUpdateColumns) row_diag = d[row];
     }
     // v: the accumulated sums on entry; on return the scaled values that are
-    // stored (kGram, kPoly: for the mirrored store).
-    __device__ __forceinline__ void finish(const NsProduct& p, int z, int row, int col, float (&v)[W]) const {
+    // stored (kGram, kPoly: for the mirrored store).  row_diag, col_diag: the
+    // diagonal's entries of the row and the columns, where the stage reads
+    // them (kPoly both, kUpdate the row's, kUpdateColumns the columns').
+    __device__ __forceinline__ void finish(const NsProduct& p, int z, int row, int col, float row_diag,
+                                           const float* col_diag, float (&v)[W]) const {
 #pragma unroll
         for (int e = 0; e < W; ++e) v[e] *= p.unscale;
         if constexpr (STAGE >= kUpdate) {
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const float diag = STAGE == kUpdate ? row_diag : col_diag[STAGE == kUpdate ? 0 : e];
+                const float diag = STAGE == kUpdate ? row_diag : col_diag[e];
                 v[e] = __builtin_fmaf(p.a + diag, in.value(e) * p.in_unscale, v[e]);
             }
             if (p.final_out != nullptr) {

@@ -24,8 +24,14 @@ void ns_wide_kernel(NsProduct p, int tiles_m, int tiles_n, int tiles) {
     using Staged = StagedTile<Core::FM, Core::FN>;
     using Run = NsRun<STAGE, TERMS, 8>;
     constexpr bool SYMMETRIC = STAGE < kUpdate;
-    static_assert(4 * Staged::PATCH * 4 <= Core::LDS_BYTES, "patches");
-    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
+    // After the K loop: each wave's patch and slots, then the diagonal's
+    // entries of the block's rows and columns.
+    constexpr int NV = STAGE == kGram ? 0 : Run::LOW ? 2 : 1;
+    constexpr int PATCHES = 4 * Staged::PATCH * 4, SLOTS = 4 * Staged::slot_bytes(NV);
+    constexpr int EPILOGUE_BYTES = PATCHES + SLOTS + 2 * 4 * BT;
+    constexpr int BYTES = EPILOGUE_BYTES > Core::LDS_BYTES ? EPILOGUE_BYTES : Core::LDS_BYTES;
+    static_assert(BYTES <= 163840, "LDS");
+    __shared__ __attribute__((aligned(16))) unsigned char lds[BYTES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int logical = xcd_contiguous((int)blockIdx.x, (int)gridDim.x);
@@ -46,17 +52,35 @@ void ns_wide_kernel(NsProduct p, int tiles_m, int tiles_n, int tiles) {
     __syncthreads();
 
     float* const patch = reinterpret_cast<float*>(lds) + wave * Staged::PATCH;
-    const int row0 = m0 + wave / 2 * Core::WM, col0 = n0 + wave % 2 * Core::WN;
+    u32x4* const slots = reinterpret_cast<u32x4*>(lds + PATCHES) + wave * (Staged::slot_bytes(NV) / 16);
+    float* const row_diags = reinterpret_cast<float*>(lds + PATCHES + SLOTS);
+    float* const col_diags = row_diags + BT;
+    const int tid = threadIdx.x, wrow = wave / 2 * Core::WM, wcol = wave % 2 * Core::WN;
+    const int row0 = m0 + wrow, col0 = n0 + wcol;
+    if constexpr (STAGE != kGram) {
+        const float* const d = p.diag_in + (int64_t)z * p.diag_n;
+        if (tid < BT) {
+            if constexpr (STAGE != kUpdateColumns) row_diags[tid] = m0 + tid < p.M ? d[m0 + tid] : 0.0f;
+            if constexpr (STAGE != kUpdate) col_diags[tid] = n0 + tid < p.N ? d[n0 + tid] : 0.0f;
+        }
+        __syncthreads();
+    }
     const bool mirror = SYMMETRIC && tm != tn;
-    Staged::template rows<SYMMETRIC, Run>(
-        acc, patch, lane,
-        [&](int row, int col) __attribute__((always_inline)) {
+    Staged::template rows<SYMMETRIC, NV>(
+        acc, patch, slots, lane, true,
+        [&](int row, int col, auto& pre) __attribute__((always_inline)) {
+            if (row0 + row >= p.M || col0 + col >= p.N) return;
             Run run;
-            if (row0 + row < p.M && col0 + col < p.N) run.load(p, z, row0 + row, col0 + col);
-            return run;
+            run.load(p, z, row0 + row, col0 + col);
+            if constexpr (NV > 0) __builtin_memcpy(&pre[0], run.in.h, 16);
+            if constexpr (NV > 1) __builtin_memcpy(&pre[1], run.in.l, 16);
         },
-        [&](int row, int col, float (&v)[8], const Run& run) __attribute__((always_inline)) {
-            if (row0 + row < p.M && col0 + col < p.N) run.finish(p, z, row0 + row, col0 + col, v);
+        [&](int row, int col, float (&v)[8], const auto& pre) __attribute__((always_inline)) {
+            if (row0 + row >= p.M || col0 + col >= p.N) return;
+            Run run;
+            if constexpr (NV > 0) __builtin_memcpy(run.in.h, &pre[0], 16);
+            if constexpr (NV > 1) __builtin_memcpy(run.in.l, &pre[1], 16);
+            run.finish(p, z, row0 + row, col0 + col, row_diags[wrow + row], col_diags + wcol + col, v);
         },
         [&](int first, int rows) __attribute__((always_inline)) {
             if (!mirror) return;

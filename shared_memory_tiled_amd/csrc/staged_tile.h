@@ -10,11 +10,13 @@
 // per lane, so that every global access of the epilogue is 16 bytes or more
 // and a row of a 256 tile's wave is one run of 256 bytes of 16-bit values.
 //
-// What the epilogue reads from memory is loaded two runs ahead: with one wave
-// per SIMD nothing else hides the latency.  A group's runs are a rolled loop:
-// unrolled, a tile's epilogue is over 30 KB of code that each wave executes
-// once, and the instruction fetches set its time (256 x 256 tiles, bias only:
-// 26 us of fixed time per block unrolled).
+// What the epilogue reads from memory (a residual, a pre-activation, the
+// other term of a sum) comes a group ahead: loaded into registers while the
+// group before is worked on, then put into the lane's own slots of LDS, so
+// that the loop over a group's runs can stay rolled.  With one wave per SIMD
+// nothing else hides the latency, and the counter that a load is waited for
+// with counts the stores too: a load per run, even two runs ahead, made each
+// run wait for the stores before it (26 us of a 256 x 256 tile's 30).
 #pragma once
 
 #include "mfma16_common.h"
@@ -60,24 +62,37 @@ struct StagedTile {
         return *row < 16 * FM;
     }
 
-    // For every run: pre = load(row, col) two runs ahead, then use(row, col, v,
-    // pre) with v[8] the columns col .. col + 7; what it leaves in v is
-    // written back to the patch if WRITE_BACK, and done(row0, rows) runs after
-    // the `rows` rows of a group from row0 (patch row 0).
-    template <bool WRITE_BACK, typename Pre, typename L, typename F, typename G>
-    __device__ static __forceinline__ void rows(const floatx4 (&acc)[FM][FN], float* patch, int lane, L&& load, F&& use,
-                                                G&& done) {
+    // Bytes of a wave's slots for NV vectors of 16 bytes per run.
+    static constexpr int slot_bytes(int nv) { return ITERS * 64 * 16 * nv; }
+
+    // For every run: use(row, col, v, pre) with v[8] the columns col .. col +
+    // 7 and pre[NV] what load(row, col, pre) brought (only if `loads`, the
+    // same for every lane); what use leaves in v is written back to the patch
+    // if WRITE_BACK, and done(row0, rows) runs after the `rows` rows of a group
+    // from row0 (patch row 0).  Both see runs inside the wave's span only.
+    template <bool WRITE_BACK, int NV, typename L, typename F, typename G>
+    __device__ static __forceinline__ void rows(const floatx4 (&acc)[FM][FN], float* patch, u32x4* slots, int lane,
+                                                bool loads, L&& load, F&& use, G&& done) {
         float* const wr = patch + 4 * (lane >> 4) * PITCH + (lane & 15);
-        auto fetch = [&](Pre& pre, int t) __attribute__((always_inline)) {
-            int it, row, col;
-            if (run_at(t, lane, &it, &row, &col)) pre = load(row, col);
+        constexpr int V = NV > 0 ? NV : 1;
+        u32x4 ahead[ITERS][V];
+        auto fetch = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < ITERS; ++i) {
+                int it, row, col;
+                if (run_at(g * ITERS + i, lane, &it, &row, &col)) load(row, col, ahead[i]);
+            }
         };
-        Pre now, next, after;
-        fetch(now, 0);
-        fetch(next, 1);
+        if (NV > 0 && loads) fetch(0);
         unroll<GROUPS>([&](auto gc) __attribute__((always_inline)) {
             constexpr int g = decltype(gc)::value;
-            constexpr int last = g == GROUPS - 1 ? LAST_ITERS : ITERS;
+            if (NV > 0 && loads) {
+#pragma unroll
+                for (int i = 0; i < ITERS; ++i)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) slots[(i * V + k) * 64 + lane] = ahead[i][k];
+                if (g + 1 < GROUPS) fetch(g + 1);
+            }
             wave_lds_fence();
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -90,23 +105,23 @@ struct StagedTile {
                 }
             wave_lds_fence();
 #pragma unroll 1
-            for (int i = 0; i < last; ++i) {
-                const int t = g * ITERS + i;
+            for (int i = 0; i < (g == GROUPS - 1 ? LAST_ITERS : ITERS); ++i) {
                 int it, row, col;
-                const bool inside = run_at(t, lane, &it, &row, &col);
-                if (t + 2 < RUNS) fetch(after, t + 2);
-                if (inside) {
+                if (run_at(g * ITERS + i, lane, &it, &row, &col)) {
+                    u32x4 pre[V];
+                    if (NV > 0 && loads) {
+#pragma unroll
+                        for (int k = 0; k < V; ++k) pre[k] = slots[(i * V + k) * 64 + lane];
+                    }
                     floatx4* q = reinterpret_cast<floatx4*>(patch + (row - 32 * g) * PITCH + col);
                     const floatx4 lo = q[0], hi = q[1];
                     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                    use(row, col, v, now);
+                    use(row, col, v, pre);
                     if constexpr (WRITE_BACK) {
                         q[0] = floatx4{v[0], v[1], v[2], v[3]};
                         q[1] = floatx4{v[4], v[5], v[6], v[7]};
                     }
                 }
-                now = next;
-                next = after;
             }
             if constexpr (WRITE_BACK) wave_lds_fence();
             done(32 * g, 2 * g + 1 < FM ? 32 : 16);
