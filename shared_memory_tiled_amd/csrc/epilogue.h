@@ -244,6 +244,45 @@ struct EpilogueRun {
     __device__ __forceinline__ void finish(const EpilogueArgs& e, int row, int col, const float (&bias)[W],
                                            float (&v)[W]) const {
         const int valid = e.N - col;
+        apply(
+            e, bias, v,
+            [&](const float (&z)[W]) __attribute__((always_inline)) {
+                store_values(e.z_type, e.preact, (int64_t)row * e.ldz + col, valid, z);
+            },
+            [&](const float (&c)[W]) __attribute__((always_inline)) {
+                store_values(e.c_type, e.C, (int64_t)row * e.ldc + col, valid, c);
+            });
+        if constexpr (GRADIENT) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = i < valid ? v[i] : 0.0f;
+        }
+    }
+    // The epilogue of whole runs at given places: C's at c_base + c_at
+    // elements, the kept pre-activation's at z_base + z_at.
+    __device__ __forceinline__ void finish_at(const EpilogueArgs& e, char* c_base, uint32_t c_at, char* z_base,
+                                              uint32_t z_at, const float (&bias)[W], float (&v)[W]) const {
+        apply(
+            e, bias, v,
+            [&](const float (&z)[W]) __attribute__((always_inline)) {
+                if (e.z_type == 0) store_whole<0>(z_base, 2 * z_at, z);
+                else store_whole<1>(z_base, 2 * z_at, z);
+            },
+            [&](const float (&c)[W]) __attribute__((always_inline)) {
+                if (e.c_type == 0) store_whole<0>(c_base, 2 * c_at, c);
+                else if (e.c_type == 1) store_whole<1>(c_base, 2 * c_at, c);
+                else store_whole<2>(c_base, 4 * c_at, c);
+            });
+    }
+    template <int TYPE>
+    __device__ static __forceinline__ void store_whole(char* base, uint32_t byte, const float (&v)[W]) {
+        typename Stored<TYPE>::T raw[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) raw[i] = (typename Stored<TYPE>::T)v[i];
+        __builtin_memcpy(base + byte, raw, sizeof(raw));
+    }
+    template <typename SZ, typename SC>
+    __device__ __forceinline__ void apply(const EpilogueArgs& e, const float (&bias)[W], float (&v)[W], SZ&& store_z,
+                                          SC&& store_c) const {
         float r[W];
         if (e.residual != nullptr) residual.values(e.c_type, r);
         if constexpr (GRADIENT) {
@@ -259,19 +298,17 @@ struct EpilogueRun {
                 raw.values(e.z_type, z);
                 times_derivative(e.act, z, v);
             }
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = i < valid ? v[i] : 0.0f;
-            if (e.C != nullptr) store_values(e.c_type, e.C, (int64_t)row * e.ldc + col, valid, v);
+            if (e.C != nullptr) store_c(v);
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i) v[i] += bias[i];
-            if (e.preact != nullptr) store_values(e.z_type, e.preact, (int64_t)row * e.ldz + col, valid, v);
+            if (e.preact != nullptr) store_z(v);
             activate(e.act, v);
             if (e.residual != nullptr) {
 #pragma unroll
                 for (int i = 0; i < W; ++i) v[i] += r[i];
             }
-            store_values(e.c_type, e.C, (int64_t)row * e.ldc + col, valid, v);
+            store_c(v);
         }
     }
 };

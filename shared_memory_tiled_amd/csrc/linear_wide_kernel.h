@@ -6,8 +6,8 @@
 // runs of 8 consecutive columns (staged_tile.h), the bias from LDS, residual
 // and pre-activation from memory a group of rows ahead, so that a 16-bit
 // result is written in rows of 256 bytes and nothing passes through memory in
-// binary32.  (A binary32 residual in gradient mode is loaded where it is used:
-// slots for it would not fit.)
+// binary32.  Tiles across column N with N no multiple of 8, and binary32
+// residuals, take a second loop that loads where it uses.
 // The column sums of the gradient mode are taken column by column from what
 // each group of 32 rows leaves in LDS, then added over the block's two row
 // halves, in a fixed order.
@@ -28,10 +28,9 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
     using Core = WideCore<FMT, KCA, KCB, BT>;
     using Staged = StagedTile<Core::FM, Core::FN>;
     using Run = EpilogueRun<8, GRADIENT>;
-    // After the K loop: each wave's patch and slots, then BT floats.  Slots:
-    // the residual (forward: 16 or 32 bytes a run) or, in gradient mode, a
-    // 16-bit residual and the pre-activation.
-    constexpr int NV = 2;
+    // After the K loop: each wave's patch and slots, then BT floats.  Slots: a
+    // 16-bit residual and, in gradient mode, the pre-activation.
+    constexpr int NV = GRADIENT ? 2 : 1;
     constexpr int PATCHES = 4 * Staged::PATCH * 4, SLOTS = 4 * Staged::slot_bytes(NV);
     constexpr int BYTES = PATCHES + SLOTS + 4 * BT > Core::LDS_BYTES ? PATCHES + SLOTS + 4 * BT : Core::LDS_BYTES;
     static_assert(BYTES <= 163840, "LDS");
@@ -58,61 +57,77 @@ void linear_wide_kernel(Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, 
     const int row0 = m0 + wave / 2 * Core::WM, wcol = wave % 2 * Core::WN, col0 = n0 + wcol;
     float sums[2] = {0.0f, 0.0f};                  // of columns lane, lane + 64 of the wave's
     u32x4* const slots = reinterpret_cast<u32x4*>(lds + PATCHES) + wave * (Staged::slot_bytes(NV) / 16);
-    const bool residual = e.residual != nullptr, wide = e.c_type == 2;
-    const bool late = GRADIENT && residual && wide;
-    const bool z = GRADIENT && e.act != kActNone;
-    Staged::template rows<GRADIENT, NV>(
-        acc, patch, slots, lane, (residual && !late) || z,
-        // whole runs; a run across column N is loaded where it is used
-        [&](int row, int col, u32x4 (&pre)[NV]) __attribute__((always_inline)) {
-            if (row0 + row >= e.M || col0 + col + 8 > e.N) return;
-            const int64_t at = (int64_t)(row0 + row) * e.ldr + col0 + col;
-            if (residual && !late) {
-                if (!GRADIENT && wide) __builtin_memcpy(pre, static_cast<const float*>(e.residual) + at, 32);
-                else __builtin_memcpy(pre, static_cast<const uint16_t*>(e.residual) + at, 16);
-            }
-            if (z)
-                __builtin_memcpy(&pre[1], static_cast<const uint16_t*>(e.preact) +
-                                              (int64_t)(row0 + row) * e.ldz + col0 + col, 16);
-        },
-        [&](int row, int col, float (&v)[8], const u32x4 (&pre)[NV]) __attribute__((always_inline)) {
-            if (row0 + row >= e.M || col0 + col >= e.N) {
-                if constexpr (GRADIENT) {
+    const bool residual = e.residual != nullptr, z = GRADIENT && e.act != kActNone;
+    auto bias_of = [&](int col, float (&b)[8]) __attribute__((always_inline)) {
+        if constexpr (!GRADIENT) {
+            const floatx4 lo = *reinterpret_cast<const floatx4*>(shared + wcol + col);
+            const floatx4 hi = *reinterpret_cast<const floatx4*>(shared + wcol + col + 4);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = 0.0f;        // for the column sums
-                }
-                return;
+            for (int c = 0; c < 4; ++c) {
+                b[c] = lo[c];
+                b[4 + c] = hi[c];
             }
-            Run run;
-            __builtin_memcpy(run.residual.w, pre, GRADIENT ? 16 : 32);
-            if constexpr (GRADIENT) __builtin_memcpy(run.preact, &pre[1], 16);
-            if (col0 + col + 8 > e.N) run.load(e, row0 + row, col0 + col);
-            else if (late) run.residual.load(2, e.residual, (int64_t)(row0 + row) * e.ldr + col0 + col, 8);
-            float b[8];
-            if constexpr (!GRADIENT) {
-                const floatx4 lo = *reinterpret_cast<const floatx4*>(shared + wcol + col);
-                const floatx4 hi = *reinterpret_cast<const floatx4*>(shared + wcol + col + 4);
+        }
+    };
+    auto outside = [&](int row, int col, float (&v)[8]) __attribute__((always_inline)) -> bool {
+        if (row0 + row < e.M && col0 + col < e.N) return false;
+        if constexpr (GRADIENT) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    b[c] = lo[c];
-                    b[4 + c] = hi[c];
-                }
-            }
-            run.finish(e, row0 + row, col0 + col, b, v);
-        },
-        [&](int, int rows) __attribute__((always_inline)) {
-            if constexpr (GRADIENT) {
-                if (partials == nullptr) return;
+            for (int c = 0; c < 8; ++c) v[c] = 0.0f;                // for the column sums
+        }
+        return true;
+    };
+    auto column_sums = [&](int, int rows) __attribute__((always_inline)) {
+        if constexpr (GRADIENT) {
+            if (partials == nullptr) return;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = lane + 64 * h;
-                    if (c < Core::WN) {
+            for (int h = 0; h < 2; ++h) {
+                const int c = lane + 64 * h;
+                if (c < Core::WN) {
 #pragma unroll 8
-                        for (int r = 0; r < rows; ++r) sums[h] += patch[r * Staged::PITCH + c];
-                    }
+                    for (int r = 0; r < rows; ++r) sums[h] += patch[r * Staged::PITCH + c];
                 }
             }
-        });
+        }
+    };
+    // Places within a wave's span as 32-bit offsets from its corner.
+    constexpr int64_t kMaxLd = 1 << 22;
+    if ((n0 + BT <= e.N || e.N % 8 == 0) && !(residual && e.c_type == 2) && e.ldc < kMaxLd &&
+        (!residual || e.ldr < kMaxLd) && (e.preact == nullptr || e.ldz < kMaxLd)) {
+        char* const c_base = static_cast<char*>(e.C) + (e.c_type == 2 ? 4 : 2) * ((int64_t)row0 * e.ldc + col0);
+        char* const z_base = static_cast<char*>(e.preact) + 2 * ((int64_t)row0 * e.ldz + col0);
+        const char* const r_base = static_cast<const char*>(e.residual) + 2 * ((int64_t)row0 * e.ldr + col0);
+        const unsigned ldc = (unsigned)e.ldc, ldz = (unsigned)e.ldz, ldr = (unsigned)e.ldr;
+        Staged::template rows<GRADIENT, NV>(
+            acc, patch, slots, lane, residual || z,
+            [&](int row, int col, u32x4 (&pre)[NV]) __attribute__((always_inline)) {
+                if (row0 + row >= e.M || col0 + col >= e.N) return;
+                if (residual) __builtin_memcpy(&pre[0], r_base + 2 * (__umul24(row, ldr) + col), 16);
+                if (z) __builtin_memcpy(&pre[NV - 1], z_base + 2 * (__umul24(row, ldz) + col), 16);
+            },
+            [&](int row, int col, float (&v)[8], const u32x4 (&pre)[NV]) __attribute__((always_inline)) {
+                if (outside(row, col, v)) return;
+                float b[8];
+                bias_of(col, b);
+                Run run;
+                __builtin_memcpy(run.residual.w, &pre[0], 16);
+                if constexpr (GRADIENT) __builtin_memcpy(run.preact, &pre[NV - 1], 16);
+                run.finish_at(e, c_base, __umul24(row, ldc) + col, z_base, __umul24(row, ldz) + col, b, v);
+            },
+            column_sums);
+    } else {
+        Staged::template rows<GRADIENT, 0>(
+            acc, patch, slots, lane, false, [](int, int, u32x4 (&)[1]) {},
+            [&](int row, int col, float (&v)[8], const u32x4 (&)[1]) __attribute__((always_inline)) {
+                if (outside(row, col, v)) return;
+                float b[8];
+                bias_of(col, b);
+                Run run;
+                run.load(e, row0 + row, col0 + col);
+                run.finish(e, row0 + row, col0 + col, b, v);
+            },
+            column_sums);
+    }
     if constexpr (GRADIENT) {
         if (partials == nullptr) return;                            // the same for every thread
         if (wave >= 2) {                                            // the lower rows' half

@@ -15,8 +15,11 @@
 // group before is worked on, then put into the lane's own slots of LDS, so
 // that the loop over a group's runs can stay rolled.  With one wave per SIMD
 // nothing else hides the latency, and the counter that a load is waited for
-// with counts the stores too: a load per run, even two runs ahead, made each
-// run wait for the stores before it (26 us of a 256 x 256 tile's 30).
+// with counts the stores too: a load in the loop makes each run wait for the
+// stores before it (20 us of a 256 x 256 tile's epilogue; so do loads that are
+// never reached, which is why edges have a loop of their own).  One vector per
+// run is loaded for the whole tile before the first store, two a group at a
+// time.
 #pragma once
 
 #include "mfma16_common.h"
@@ -75,12 +78,13 @@ struct StagedTile {
                                                 bool loads, L&& load, F&& use, G&& done) {
         float* const wr = patch + 4 * (lane >> 4) * PITCH + (lane & 15);
         constexpr int V = NV > 0 ? NV : 1;
-        u32x4 ahead[ITERS][V];
-        auto fetch = [&](int g) __attribute__((always_inline)) {
+        constexpr int HELD = NV == 1 ? RUNS : ITERS;          // runs held in registers
+        u32x4 ahead[HELD][V];
+        auto fetch = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < ITERS; ++i) {
+            for (int i = 0; i < HELD; ++i) {
                 int it, row, col;
-                if (run_at(g * ITERS + i, lane, &it, &row, &col)) load(row, col, ahead[i]);
+                if (t0 + i < RUNS && run_at(t0 + i, lane, &it, &row, &col)) load(row, col, ahead[i]);
             }
         };
         if (NV > 0 && loads) fetch(0);
@@ -90,8 +94,9 @@ struct StagedTile {
 #pragma unroll
                 for (int i = 0; i < ITERS; ++i)
 #pragma unroll
-                    for (int k = 0; k < V; ++k) slots[(i * V + k) * 64 + lane] = ahead[i][k];
-                if (g + 1 < GROUPS) fetch(g + 1);
+                    for (int k = 0; k < V; ++k)
+                        if (g * ITERS + i < RUNS) slots[(i * V + k) * 64 + lane] = ahead[NV == 1 ? g * ITERS + i : i][k];
+                if (NV != 1 && g + 1 < GROUPS) fetch((g + 1) * ITERS);
             }
             wave_lds_fence();
 #pragma unroll
