@@ -179,18 +179,20 @@ int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 // (MI355X, each kernel alone).  A round of 256 blocks takes the K loop,
 // `slow` per 64-deep phase once all CUs are busy (`fast` up to half of them:
 // the clock drops, and the small tiles' copies share the L2), and `fixed` for
-// start and epilogue.  128 tiles copy k-contiguous factors in runs of 64
-// bytes: 0.09 more for each.
+// start and epilogue (with a kept pre-activation; the activation adds the
+// same everywhere).  128 tiles copy k-contiguous factors in runs of 64 bytes:
+// 0.06 more for each.  4096^3: 106 / 135 / 165 / 160 / 262 us on 256 / 192 /
+// 160 / 128 / 64 tiles; 1000 x 2000 x 1000: 41 / 26 / 22 / 21 / 17.
 double tile_time(int tile, int M, int N, int K, int k_contiguous) {
     const double tiles = (double)ceil_div(M, tile) * ceil_div(N, tile);
     const double rounds = ceil(tiles / 256.0);
-    if (tile == 64) return rounds * (3.3 + 0.0037 * K);
+    if (tile == 64) return rounds * (4.4 + 0.0037 * K);
     static const struct { int tile; double fast, slow, fixed; } kCost[] = {
-        {256, 1.03, 1.45, 16.0}, {192, 0.72, 0.89, 12.0}, {160, 0.62, 0.73, 11.0}, {128, 0.31, 0.42, 12.0}};
+        {256, 1.00, 1.38, 20.0}, {192, 0.70, 0.86, 13.0}, {160, 0.62, 0.70, 10.8}, {128, 0.31, 0.36, 16.0}};
     for (const auto& c : kCost)
         if (c.tile == tile) {
             const double busy = fmin(1.0, fmax(0.0, tiles / 128.0 - 1.0));
-            const double slow = c.slow + (tile == 128 ? 0.09 * k_contiguous : 0.0);
+            const double slow = c.slow + (tile == 128 ? 0.06 * k_contiguous : 0.0);
             return rounds * ((c.fast + (slow - c.fast) * busy) * ceil_div(K, 64) + c.fixed);
         }
     return 1e30;

@@ -80,7 +80,7 @@ void ns_split_kernel(NewtonSchulzArgs a, const double* partials, float x_scale, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = c + e < a.cols ? (float)(v[e] * scale) : 0.0f;
         }
-        store_planes<8, true>(x + (int64_t)blockIdx.y * stride, (int64_t)r * cp + c, (int64_t)rp * cp, v);
+        store_planes<8, true>(x + (int64_t)blockIdx.y * stride, plane_index(r, cp, c), (int64_t)rp * cp, v);
     }
 }
 
@@ -93,7 +93,7 @@ void ns_write_kernel(NewtonSchulzArgs a, float unscale, const uint16_t* x, int r
     for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
         float v[8];
         PlaneRun<8, true> run;
-        run.load(x + z * stride, r * cp + c, (int64_t)rp * cp);
+        run.load(x + z * stride, plane_index((int)r, cp, c), (int64_t)rp * cp);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = run.value(e) * unscale;
         store_values(a.type, a.out, z * a.stride_o + r * a.ldo + c, a.cols - c, v);
@@ -132,15 +132,15 @@ float plane_scale(double bound) { return (float)ldexp(1.0, 15 - (int)ceil(log2(f
 //   A round of 256 blocks takes the K loop, `slow` per 64-deep phase once all
 //   CUs are busy (the clock drops, and the copies of the small tiles share
 //   the L2; `fast` up to half of them), and `fixed` for start and epilogue by
-//   stage.  4096^2, one term: Gram 86 / 70 / 82 / 129 us on 256 / 192 / 160 /
-//   128 tiles (136, 253, 351 and 528 of them), update 116 / 141 / 177 / 206;
-//   2048^2: update 61 / 42 / 38 / 32.
-//   64 tiles: 3.3 + 0.0037 K per round (1024^2: Gram 6.9 against 17 us on 128
-//   tiles; 4096^2 311 against 70).
+//   stage.  4096^2, one term: Gram 84 / 67 / 81 / 124 us on 256 / 192 / 160 /
+//   128 tiles (136, 253, 351 and 528 of them), update 114 / 141 / 176 / 207;
+//   2048^2: update 53 / 38 / 34 / 31.
+//   64 tiles: 3.3 + 0.0037 K per round (1024^2: Gram 6.7 against 15.3 us on
+//   128 tiles; 4096^2 302 against 67).
 int pick_tile(const NsProduct& p) {
     static const struct { int tile; double fast, slow, fixed[3]; } kTiles[] = {
-        {256, 1.03, 1.45, {14.6, 22.0, 21.5}}, {192, 0.72, 0.89, {11.3, 14.8, 13.0}},
-        {160, 0.62, 0.73, {10.4, 14.5, 10.5}}, {128, 0.31, 0.50, {13.5, 15.5, 13.0}}};
+        {256, 1.03, 1.50, {14.0, 23.0, 18.0}}, {192, 0.72, 0.90, {9.2, 14.0, 11.4}},
+        {160, 0.62, 0.75, {7.3, 10.6, 8.7}}, {128, 0.37, 0.52, {9.7, 13.7, 12.5}}};
     const double k = (double)p.K * p.terms;
     const int64_t t64 = (int64_t)(p.M / 64) * (p.N / 64) * p.batch;
     int best = 64;

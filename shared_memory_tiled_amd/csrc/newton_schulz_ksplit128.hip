@@ -74,7 +74,7 @@ void ns_ksplit128_kernel(NsProduct p, int tiles_m, int tiles) {
                 float v[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) v[r] = rows[128 * (q + r) + (c ^ (16 * (((q + r) >> 2) & 1)))];
-                store_planes<8, Run::LOW>(p.out + (int64_t)z * p.stride_o, (int64_t)(n0 + c) * p.ldo + row0, p.plane_o, v);
+                store_planes<8, Run::LOW>(p.out + (int64_t)z * p.stride_o, plane_index(n0 + c, p.ldo, row0), p.plane_o, v);
             }
         });
 }

@@ -52,27 +52,39 @@ namespace {
 
 typedef _Float16 half_t;
 
+// Element `index` of a plane whose base is the same for every lane: planes
+// are below 2^31 bytes (newton_schulz_workspace), so the place is a 32-bit
+// offset; rows and leading dimensions are below 2^24.
+template <typename T>
+__device__ __forceinline__ T* plane_at(T* base, uint32_t index) {
+    using C = std::conditional_t<std::is_const_v<T>, const char, char>;
+    return reinterpret_cast<T*>(reinterpret_cast<C*>(base) + 2 * index);
+}
+__device__ __forceinline__ uint32_t plane_index(int row, int64_t ld, int col) {
+    return __umul24((unsigned)row, (unsigned)ld) + (unsigned)col;
+}
+
 // W consecutive plane values as loaded, and their value over the scale.
 template <int W, bool LOW>
 struct PlaneRun {
     half_t h[W], l[LOW ? W : 1];
-    __device__ __forceinline__ void load(const uint16_t* base, int64_t index, int64_t plane) {
-        __builtin_memcpy(h, base + index, sizeof(h));
-        if constexpr (LOW) __builtin_memcpy(l, base + plane + index, sizeof(l));
+    __device__ __forceinline__ void load(const uint16_t* base, uint32_t index, int64_t plane) {
+        __builtin_memcpy(h, plane_at(base, index), sizeof(h));
+        if constexpr (LOW) __builtin_memcpy(l, plane_at(base + plane, index), sizeof(l));
     }
     __device__ __forceinline__ float value(int e) const { return LOW ? (float)h[e] + (float)l[e] : (float)h[e]; }
 };
 // The plane, or both planes, of W scaled values.
 template <int W, bool LOW>
-__device__ __forceinline__ void store_planes(uint16_t* base, int64_t index, int64_t plane, const float (&v)[W]) {
+__device__ __forceinline__ void store_planes(uint16_t* base, uint32_t index, int64_t plane, const float (&v)[W]) {
     half_t h[W], l[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) {
         h[e] = (half_t)v[e];
         l[e] = (half_t)(v[e] - (float)h[e]);
     }
-    __builtin_memcpy(base + index, h, sizeof(h));
-    if constexpr (LOW) __builtin_memcpy(base + plane + index, l, sizeof(l));
+    __builtin_memcpy(plane_at(base, index), h, sizeof(h));
+    if constexpr (LOW) __builtin_memcpy(plane_at(base + plane, index), l, sizeof(l));
 }
 
 // A run of W columns: what it reads of S or X, and the epilogue.  S and T
@@ -84,7 +96,7 @@ struct NsRun {
     PlaneRun<W, LOW> in;
     __device__ __forceinline__ void load(const NsProduct& p, int z, int row, int col) {
         if constexpr (STAGE == kGram) return;
-        in.load(p.in + (int64_t)z * p.stride_i, (int64_t)row * p.ldi + col, p.plane_i);
+        in.load(p.in + (int64_t)z * p.stride_i, plane_index(row, p.ldi, col), p.plane_i);
     }
     // v: the accumulated sums on entry; on return the scaled values that are
     // stored (kGram, kPoly: for the mirrored store).  row_diag, col_diag: the
@@ -110,25 +122,30 @@ struct NsRun {
             for (int e = 0; e < W; ++e) v[e] *= p.out_scale;
         } else {
             const int diag = row - col;                  // the run's entry on the diagonal, if any
+            float on_diag = 0.0f;
+            const bool has_diag = (unsigned)diag < (unsigned)W;
+            if (has_diag) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) on_diag = diag == e ? v[e] : on_diag;
+            }
             if constexpr (STAGE == kPoly) {
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
                     const float s = in.value(e) * p.in_unscale;
-                    const float lin = diag == e ? row_diag : s;
-                    const float mix = diag == e ? row_diag * row_diag : (row_diag + col_diag[e]) * s;
-                    v[e] = __builtin_fmaf(p.c, v[e] + mix, p.b * lin);
+                    v[e] = __builtin_fmaf(p.c, __builtin_fmaf(row_diag + col_diag[e], s, v[e]), p.b * s);
                 }
             }
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                if (diag == e) {
-                    p.diag_out[(int64_t)z * p.diag_n + row] = v[e];
-                    v[e] = 0.0f;
-                }
-                v[e] *= p.out_scale;
+            for (int e = 0; e < W; ++e) v[e] *= p.out_scale;
+            if (has_diag) {
+                if constexpr (STAGE == kPoly)
+                    on_diag = __builtin_fmaf(p.c, __builtin_fmaf(row_diag, row_diag, on_diag), p.b * row_diag);
+                p.diag_out[(int64_t)z * p.diag_n + row] = on_diag;
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] = diag == e ? 0.0f : v[e];
             }
         }
-        store_planes<W, LOW>(p.out + (int64_t)z * p.stride_o, (int64_t)row * p.ldo + col, p.plane_o, v);
+        store_planes<W, LOW>(p.out + (int64_t)z * p.stride_o, plane_index(row, p.ldo, col), p.plane_o, v);
     }
 };
 

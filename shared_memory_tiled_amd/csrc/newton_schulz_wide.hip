@@ -93,7 +93,7 @@ void ns_wide_kernel(NsProduct p, int tiles_m, int tiles_n, int tiles) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) v[r] = patch[(q + r) * Staged::PITCH + c];
                 store_planes<8, Run::LOW>(p.out + (int64_t)z * p.stride_o,
-                                          (int64_t)(col0 + c) * p.ldo + row0 + first + q, p.plane_o, v);
+                                          plane_index(col0 + c, p.ldo, row0 + first + q), p.plane_o, v);
             }
         });
 }
