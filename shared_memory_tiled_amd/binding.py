@@ -11,6 +11,7 @@ built, or a call returns a nonzero status, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -521,97 +522,116 @@ def newton_schulz_workspace_size(type_, batch, rows, cols) -> int:
     return int(load_library().newton_schulz_workspace_size(int(type_), batch, rows, cols))
 
 
-class _Launch:
-    """Makes the tensors' device current and, if a stream is given, that
-    stream torch's current one, so that outputs and workspaces allocated
-    inside belong to the stream the kernels run on; ``handle`` is that
-    stream.  All tensors must live on one GPU."""
-
-    def __init__(self, stream, *tensors):
-        device = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
-                raise TypeError("arguments must be CUDA tensors")
-            if device is None:
-                device = t.device
-            elif t.device != device:
-                raise ValueError(f"tensors on different devices: {device} and {t.device}")
-        self.device = device
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors on {device}")
-        self._stream = stream
-        self._contexts = []
-
-    def __enter__(self):
-        if self._stream is not None:
-            self._contexts = [torch.cuda.stream(self._stream)]
-        elif torch.cuda.current_device() != self.device.index:
-            self._contexts = [torch.cuda.device(self.device)]
-        for c in self._contexts:
-            c.__enter__()
-        self.handle = torch.cuda.current_stream(self.device).cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        for c in reversed(self._contexts):
-            c.__exit__(*exc)
-        return False
-
-    def workspace(self, nbytes: int):
-        if nbytes < 0:
-            raise GemmError(6, "the library takes no problem of this size")
-        return torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
+def _device_of(*tensors) -> int:
+    """Index of the one GPU that holds all the tensors (None ones aside)."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("arguments must be CUDA tensors")
+        if device is None:
+            device = t.get_device()
+        elif t.get_device() != device:
+            raise ValueError(f"tensors on different devices: cuda:{device} and {t.device}")
+    return device
 
 
-def _ld_any(t: torch.Tensor, what: str, shape=None, dtypes=None) -> int:
-    """Leading dimension of a row-major matrix argument, after its checks."""
-    if t.dim() != 2 or (dtypes is not None and t.dtype not in dtypes):
-        raise TypeError(f"{what} must be a 2-D tensor of {', '.join(str(d) for d in dtypes or ())}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what} must be row-major (unit column stride)")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if t.shape[0] > 1 and ld < t.shape[1]:
-        raise ValueError(f"{what}'s rows overlap (row stride {ld}, {t.shape[1]} columns)")
-    return max(ld, t.shape[1], 1)
+def _elsewhere(stream, device: int) -> bool:
+    """Whether a call has to change torch's current stream or device first."""
+    return stream is not None or device != torch._C._cuda_getDevice()
 
 
-def _vector(t: torch.Tensor | None, what: str, n: int, dtypes) -> None:
-    if t is None:
+@contextlib.contextmanager
+def _placed(stream, device: int):
+    """The tensors' device current and, if a stream is given, that stream
+    torch's current one: outputs and workspaces allocated inside belong to the
+    stream the kernels run on."""
+    if stream is None:
+        with torch.cuda.device(device):
+            yield
         return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device.index != device:
+        raise ValueError(f"stream of {stream.device} for tensors on cuda:{device}")
+    with torch.cuda.stream(stream):
+        yield
+
+
+def _workspace(like: torch.Tensor, nbytes: int):
+    """(tensor, address, bytes) of a workspace of torch's; a size of -1 is
+    left for the call itself to name the error."""
+    if nbytes <= 0:
+        return None, None, 0
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
+    return ws, ws.data_ptr(), nbytes
+
+
+def _row_major(t: torch.Tensor, what: str) -> int:
+    """Leading dimension of a 2-D row-major tensor."""
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{what} must be row-major (unit column stride)")
+    if rows <= 1:
+        return cols or 1
+    if s0 < cols:
+        raise ValueError(f"{what}'s rows overlap (row stride {s0}, {cols} columns)")
+    return s0 or 1
+
+
+def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dtype) -> int:
+    """Leading dimension of a matrix argument of known shape and dtype."""
+    if t.dim() != 2 or t.dtype is not dtype:
+        raise TypeError(f"{what} must be a 2-D tensor of {dtype}")
+    if t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    return _row_major(t, what)
+
+
+def _vector(t: torch.Tensor, what: str, n: int, dtypes) -> None:
     if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.dtype not in dtypes:
         raise TypeError(f"{what} must be a contiguous vector of {n} values of {', '.join(str(d) for d in dtypes)}")
 
 
-def _linear_call(launch, op_a, op_b, M, N, K, A, lda, B, ldb, C, ldc, ep) -> None:
-    """gemm_mixed_epilogue with a workspace of torch's."""
-    lib = load_library()
-    fmt = _FORMAT_OF_DTYPE[A.dtype]
-    head = (op_a, op_b, fmt, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb)
-    ref = ctypes.byref(ep)
-    nbytes = lib.gemm_mixed_epilogue_workspace_size(*head, ref)
-    ws = launch.workspace(nbytes) if nbytes > 0 else None          # -1: the call itself names the error
-    _check(lib.gemm_mixed_epilogue(*head, C.data_ptr(), ldc, ref, None if ws is None else ws.data_ptr(),
-                                   max(nbytes, 0), launch.handle))
-
-
 def _factors(A, B, op_a, op_b):
-    """(op_a, op_b, M, N, K, lda, ldb) of a 16-bit product's checked factors."""
-    oa, ob = int(OPS[op_a]), int(OPS[op_b])
-    dt = tuple(_FORMAT_OF_DTYPE)
-    lda, ldb = _ld_any(A, "the first factor", dtypes=dt), _ld_any(B, "the second factor", dtypes=dt)
-    if A.dtype != B.dtype:
-        raise TypeError("the factors must have the same 16-bit dtype")
-    M, K = A.shape[::-1] if oa else A.shape
-    K2, N = B.shape[::-1] if ob else B.shape
+    """(format, op_a, op_b, M, N, K, lda, ldb) of a 16-bit product's factors."""
+    oa, ob = OPS[op_a], OPS[op_b]
+    fmt = _FORMAT_OF_DTYPE.get(A.dtype)
+    if fmt is None or B.dtype is not A.dtype or A.dim() != 2 or B.dim() != 2:
+        raise TypeError("the factors must be 2-D bfloat16 or float16 tensors of one dtype")
+    lda, ldb = _row_major(A, "the first factor"), _row_major(B, "the second factor")
+    M, K = A.shape
+    K2, N = B.shape
+    if oa:
+        M, K = K, M
+    if ob:
+        K2, N = N, K2
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    return oa, ob, M, N, K, lda, ldb
+    return fmt, oa, ob, M, N, K, lda, ldb
+
+
+def _output(out, out_dtype, like: torch.Tensor, M: int, N: int):
+    """(out, its leading dimension), allocated if None."""
+    if out is None:
+        dtype = out_dtype or like.dtype
+        if dtype is not like.dtype and dtype is not torch.float32:
+            raise TypeError(f"out has the factors' dtype or float32, not {dtype}")
+        return (like.new_empty((M, N)) if dtype is like.dtype else like.new_empty((M, N), dtype=dtype)), N or 1
+    if out_dtype is not None and out.dtype is not out_dtype:
+        raise TypeError(f"out is {out.dtype}, not {out_dtype}")
+    return out, _matrix(out, "out", M, N, torch.float32 if out.dtype is torch.float32 else like.dtype)
+
+
+def _linear_call(fmt, oa, ob, M, N, K, A, lda, B, ldb, C, ldc, ep) -> None:
+    """gemm_mixed_epilogue on the current stream with a workspace of torch's."""
+    lib = load_library()
+    a, b, ref = A.data_ptr(), B.data_ptr(), ctypes.byref(ep)
+    ws, addr, nbytes = _workspace(A, lib.gemm_mixed_epilogue_workspace_size(oa, ob, fmt, M, N, K, a, lda, b, ldb, ref))
+    _check(lib.gemm_mixed_epilogue(oa, ob, fmt, M, N, K, a, lda, b, ldb, C.data_ptr(), ldc, ref, addr, nbytes,
+                                   torch._C._cuda_getCurrentRawStream(A.get_device())))
 
 
 def linear(X, W, bias=None, activation="none", residual=None, out=None, out_dtype=None, return_preact=False,
@@ -624,19 +644,27 @@ def linear(X, W, bias=None, activation="none", residual=None, out=None, out_dtyp
     be ``out``; ``bias`` has the factors' dtype or float32.  With
     ``return_preact`` returns (out, Z), Z = op_a(X) @ op_b(W) + bias in the
     factors' dtype, for the backward pass."""
-    with _Launch(stream, X, W, bias, residual, out) as launch:
-        oa, ob, M, N, K, lda, ldb = _factors(X, W, op_a, op_b)
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype or X.dtype, device=X.device)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            raise TypeError(f"out is {out.dtype}, not {out_dtype}")
-        ldc = _ld_any(out, "out", (M, N), (X.dtype, torch.float32))
+    device = _device_of(X, W, bias, residual, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return linear(X, W, bias, activation, residual, out, out_dtype, return_preact, op_a, op_b)
+    fmt, oa, ob, M, N, K, lda, ldb = _factors(X, W, op_a, op_b)
+    out, ldc = _output(out, out_dtype, X, M, N)
+    c_type = _TYPE_OF_DTYPE[out.dtype]
+    ep = Epilogue(c_type, _activation(activation))
+    if bias is not None:
         _vector(bias, "bias", N, (X.dtype, torch.float32))
-        ldr = 0 if residual is None else _ld_any(residual, "residual", (M, N), (out.dtype,))
-        preact = torch.empty((M, N), dtype=X.dtype, device=X.device) if return_preact else None
-        ep = epilogue(_TYPE_OF_DTYPE[out.dtype], activation, 0, bias,
-                      0 if bias is None else _TYPE_OF_DTYPE[bias.dtype], residual, ldr, preact, max(N, 1))
-        _linear_call(launch, oa, ob, M, N, K, X, lda, W, ldb, out, ldc, ep)
+        ep.bias_type = _TYPE_OF_DTYPE[bias.dtype]
+        ep.bias = bias.data_ptr()
+    if residual is not None:
+        ep.ld_residual = _matrix(residual, "residual", M, N, out.dtype)
+        ep.residual = residual.data_ptr()
+    preact = None
+    if return_preact:
+        preact = X.new_empty((M, N))
+        ep.preact = preact.data_ptr()
+        ep.ld_preact = N or 1
+    _linear_call(fmt, oa, ob, M, N, K, X, lda, W, ldb, out, ldc, ep)
     return (out, preact) if return_preact else out
 
 
@@ -651,20 +679,27 @@ def linear_grad(dZ, W, preact=None, activation="none", residual=None, out=None, 
     ``residual`` a gradient that arrives past this layer (out's dtype).  With
     ``return_bias_grad`` returns (out, column sums in float32): the bias
     gradient of the layer before."""
-    with _Launch(stream, dZ, W, preact, residual, out) as launch:
-        oa, ob, M, N, K, lda, ldb = _factors(dZ, W, op_a, op_b)
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype or dZ.dtype, device=dZ.device)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            raise TypeError(f"out is {out.dtype}, not {out_dtype}")
-        ldc = _ld_any(out, "out", (M, N), (dZ.dtype, torch.float32))
-        if preact is None and _activation(activation):
-            raise ValueError("the gradient of an activation needs preact")
-        ldz = 0 if preact is None else _ld_any(preact, "preact", (M, N), (dZ.dtype,))
-        ldr = 0 if residual is None else _ld_any(residual, "residual", (M, N), (out.dtype,))
-        sums = torch.empty(N, dtype=torch.float32, device=dZ.device) if return_bias_grad else None
-        ep = epilogue(_TYPE_OF_DTYPE[out.dtype], activation, 1, None, 0, residual, ldr, preact, ldz, sums)
-        _linear_call(launch, oa, ob, M, N, K, dZ, lda, W, ldb, out, ldc, ep)
+    device = _device_of(dZ, W, preact, residual, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return linear_grad(dZ, W, preact, activation, residual, out, out_dtype, return_bias_grad, op_a, op_b)
+    fmt, oa, ob, M, N, K, lda, ldb = _factors(dZ, W, op_a, op_b)
+    out, ldc = _output(out, out_dtype, dZ, M, N)
+    act = _activation(activation)
+    if preact is None and act:
+        raise ValueError("the gradient of an activation needs preact")
+    ep = Epilogue(_TYPE_OF_DTYPE[out.dtype], act, 1)
+    if preact is not None:
+        ep.ld_preact = _matrix(preact, "preact", M, N, dZ.dtype)
+        ep.preact = preact.data_ptr()
+    if residual is not None:
+        ep.ld_residual = _matrix(residual, "residual", M, N, out.dtype)
+        ep.residual = residual.data_ptr()
+    sums = None
+    if return_bias_grad:
+        sums = dZ.new_empty(N, dtype=torch.float32)
+        ep.bias_grad = sums.data_ptr()
+    _linear_call(fmt, oa, ob, M, N, K, dZ, lda, W, ldb, out, ldc, ep)
     return (out, sums) if return_bias_grad else out
 
 
@@ -673,24 +708,32 @@ def activation_backward(dY, preact=None, activation="none", out=None, return_bia
     """(dZ, db): dZ = dY * act'(preact) in dY's dtype, db its column sums in
     float32 (None without ``return_bias_grad``); with ``return_dz`` false only
     the sums are computed and dZ is None.  ``out`` may be dY."""
-    with _Launch(stream, dY, preact, out) as launch:
-        lib = load_library()
-        ldy = _ld_any(dY, "dY", None, tuple(_FORMAT_OF_DTYPE))
-        M, N = dY.shape
-        act = _activation(activation)
-        if preact is None and act:
-            raise ValueError("the gradient of an activation needs preact")
-        ldz = 0 if preact is None else _ld_any(preact, "preact", (M, N), (dY.dtype,))
-        if not return_dz:
-            out = None
-        elif out is None:
-            out = torch.empty((M, N), dtype=dY.dtype, device=dY.device)
-        ldo = 0 if out is None else _ld_any(out, "out", (M, N), (dY.dtype,))
-        sums = torch.empty(N, dtype=torch.float32, device=dY.device) if return_bias_grad else None
-        nbytes = lib.activation_grad_workspace_size(M, N) if return_bias_grad else 0
-        ws = launch.workspace(nbytes)
-        _check(lib.activation_grad(act, _FORMAT_OF_DTYPE[dY.dtype], M, N, dY.data_ptr(), ldy, _addr(preact), ldz,
-                                   _addr(out), ldo, _addr(sums), _addr(ws), nbytes, launch.handle))
+    device = _device_of(dY, preact, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return activation_backward(dY, preact, activation, out, return_bias_grad, return_dz)
+    lib = load_library()
+    fmt = _FORMAT_OF_DTYPE.get(dY.dtype)
+    if fmt is None or dY.dim() != 2:
+        raise TypeError("dY must be a 2-D bfloat16 or float16 tensor")
+    ldy = _row_major(dY, "dY")
+    M, N = dY.shape
+    act = _activation(activation)
+    if preact is None and act:
+        raise ValueError("the gradient of an activation needs preact")
+    ldz = 0 if preact is None else _matrix(preact, "preact", M, N, dY.dtype)
+    if not return_dz:
+        out, ldo = None, 0
+    elif out is None:
+        out, ldo = dY.new_empty((M, N)), N or 1
+    else:
+        ldo = _matrix(out, "out", M, N, dY.dtype)
+    sums, ws, addr, nbytes = None, None, None, 0
+    if return_bias_grad:
+        sums = dY.new_empty(N, dtype=torch.float32)
+        ws, addr, nbytes = _workspace(dY, lib.activation_grad_workspace_size(M, N))
+    _check(lib.activation_grad(act, fmt, M, N, dY.data_ptr(), ldy, _addr(preact), ldz, _addr(out), ldo, _addr(sums),
+                               addr, nbytes, torch._C._cuda_getCurrentRawStream(device)))
     return out, sums
 
 
@@ -700,30 +743,28 @@ def linear_backward(dY, X, W, preact=None, activation="none", weight_grad_dtype=
     layout and dtype (or float32 with ``weight_grad_dtype``).  dZ is rounded
     to dY's dtype between the two, for the matrix units.  The gradient of a
     residual added after the activation is dY itself."""
-    with _Launch(stream, dY, X, W, preact) as launch:
-        ob = int(OPS[op_b])
-        M, N = dY.shape
-        dt = (dY.dtype,)
-        ldx = _ld_any(X, "X", (M, X.shape[-1]), dt)
-        K = X.shape[1]
-        ldw = _ld_any(W, "W", (N, K) if ob else (K, N), dt)
-        if _activation(activation):
-            dZ, db = activation_backward(dY, preact, activation)
-        else:
-            dZ = dY
-            _, db = activation_backward(dY, return_dz=False)
-        lddz = _ld_any(dZ, "dY", (M, N), tuple(_FORMAT_OF_DTYPE))
-        dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device)
-        ep = epilogue(_TYPE_OF_DTYPE[dX.dtype])
-        _linear_call(launch, 0, 1 - ob, M, K, N, dZ, lddz, W, ldw, dX, max(K, 1), ep)
-        dW = torch.empty(tuple(W.shape), dtype=weight_grad_dtype or W.dtype, device=W.device)
-        if dW.dtype not in (W.dtype, torch.float32):
-            raise TypeError("dW has W's dtype or float32")
-        ep = epilogue(_TYPE_OF_DTYPE[dW.dtype])
-        if ob:
-            _linear_call(launch, 1, 0, N, K, M, dZ, lddz, X, ldx, dW, max(K, 1), ep)
-        else:
-            _linear_call(launch, 1, 0, K, N, M, X, ldx, dZ, lddz, dW, max(N, 1), ep)
+    device = _device_of(dY, X, W, preact)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return linear_backward(dY, X, W, preact, activation, weight_grad_dtype, op_b)
+    fmt, _, ob, M, N, K, ldx, ldw = _factors(X, W, "N", op_b)
+    lddz = _matrix(dY, "dY", M, N, X.dtype)
+    if weight_grad_dtype not in (None, W.dtype, torch.float32):
+        raise TypeError("dW has W's dtype or float32")
+    if _activation(activation):
+        dZ, db = activation_backward(dY, preact, activation)
+        lddz = N or 1
+    else:
+        dZ = dY
+        _, db = activation_backward(dY, return_dz=False)
+    dX = dY.new_empty((M, K))
+    _linear_call(fmt, 0, 1 - ob, M, K, N, dZ, lddz, W, ldw, dX, K or 1, Epilogue(fmt))
+    dW, lddw = _output(None, weight_grad_dtype, W, *W.shape)
+    ep = Epilogue(_TYPE_OF_DTYPE[dW.dtype])
+    if ob:
+        _linear_call(fmt, 1, 0, N, K, M, dZ, lddz, X, ldx, dW, lddw, ep)
+    else:
+        _linear_call(fmt, 1, 0, K, N, M, X, ldx, dZ, lddz, dW, lddw, ep)
     return dX, dW, db
 
 
@@ -733,49 +774,67 @@ def layer_norm(X, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     """(Y, mean, rstd) of the layer norm over X's rows (2-D, bfloat16, float16
     or float32; Y of X's dtype, mean and rstd float32).  ``weight`` and
     ``bias`` are vectors of one dtype of the three; ``out`` may be X."""
-    with _Launch(stream, X, weight, bias, out) as launch:
-        ldx = _ld_any(X, "X", None, tuple(_TYPE_OF_DTYPE))
-        rows, cols = X.shape
-        _vector(weight, "weight", cols, tuple(_TYPE_OF_DTYPE))
-        _vector(bias, "bias", cols, tuple(_TYPE_OF_DTYPE) if weight is None else (weight.dtype,))
-        if out is None:
-            out = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
-        ldy = _ld_any(out, "out", (rows, cols), (X.dtype,))
-        stats = torch.empty((2, rows), dtype=torch.float32, device=X.device)
-        param = weight if weight is not None else bias
-        _check(load_library().layer_norm(
-            _TYPE_OF_DTYPE[X.dtype], rows, cols, X.data_ptr(), ldx, 2 if param is None else _TYPE_OF_DTYPE[param.dtype],
-            _addr(weight), _addr(bias), float(eps), out.data_ptr(), ldy, stats.data_ptr(),
-            stats.data_ptr() + 4 * rows, launch.handle))
-    return out, stats[0], stats[1]
+    device = _device_of(X, weight, bias, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return layer_norm(X, weight, bias, eps, out)
+    t = _TYPE_OF_DTYPE.get(X.dtype)
+    if t is None or X.dim() != 2:
+        raise TypeError("X must be a 2-D bfloat16, float16 or float32 tensor")
+    ldx = _row_major(X, "X")
+    rows, cols = X.shape
+    param, gamma, beta = 2, None, None
+    if weight is not None:
+        _vector(weight, "weight", cols, _TYPE_OF_DTYPE)
+        param, gamma = _TYPE_OF_DTYPE[weight.dtype], weight.data_ptr()
+    if bias is not None:
+        _vector(bias, "bias", cols, _TYPE_OF_DTYPE if weight is None else (weight.dtype,))
+        param, beta = _TYPE_OF_DTYPE[bias.dtype], bias.data_ptr()
+    if out is None:
+        out, ldy = X.new_empty((rows, cols)), cols
+    else:
+        ldy = _matrix(out, "out", rows, cols, X.dtype)
+    mean, rstd = X.new_empty(rows, dtype=torch.float32), X.new_empty(rows, dtype=torch.float32)
+    _check(load_library().layer_norm(t, rows, cols, X.data_ptr(), ldx, param, gamma, beta, eps, out.data_ptr(), ldy,
+                                     mean.data_ptr(), rstd.data_ptr(), torch._C._cuda_getCurrentRawStream(device)))
+    return out, mean, rstd
 
 
 def layer_norm_backward(dY, X, mean, rstd, weight=None, residual_grad=None, out=None, stream=None):
     """(dX, dweight, dbias) of layer_norm; ``residual_grad`` (dY's dtype) is
     added to dX.  dweight and dbias are float32.  ``out`` may be dY or
     ``residual_grad``."""
-    with _Launch(stream, dY, X, mean, rstd, weight, residual_grad, out) as launch:
-        lib = load_library()
-        lddy = _ld_any(dY, "dY", None, tuple(_TYPE_OF_DTYPE))
-        rows, cols = dY.shape
-        ldx = _ld_any(X, "X", (rows, cols), (dY.dtype,))
-        _vector(mean, "mean", rows, (torch.float32,))
-        _vector(rstd, "rstd", rows, (torch.float32,))
-        _vector(weight, "weight", cols, tuple(_TYPE_OF_DTYPE))
-        ldr = 0 if residual_grad is None else _ld_any(residual_grad, "residual_grad", (rows, cols), (dY.dtype,))
-        if out is None:
-            out = torch.empty((rows, cols), dtype=dY.dtype, device=dY.device)
-        lddx = _ld_any(out, "out", (rows, cols), (dY.dtype,))
-        sums = torch.empty((2, cols), dtype=torch.float32, device=dY.device)
-        t = _TYPE_OF_DTYPE[dY.dtype]
-        nbytes = lib.layer_norm_backward_workspace_size(t, rows, cols)
-        ws = launch.workspace(nbytes) if nbytes > 0 else None      # -1: the call itself names the error
-        _check(lib.layer_norm_backward(
-            t, rows, cols, dY.data_ptr(), lddy, X.data_ptr(), ldx, mean.data_ptr(), rstd.data_ptr(),
-            2 if weight is None else _TYPE_OF_DTYPE[weight.dtype], _addr(weight), _addr(residual_grad), ldr,
-            out.data_ptr(), lddx, sums.data_ptr(), sums.data_ptr() + 4 * cols, _addr(ws), max(nbytes, 0),
-            launch.handle))
-    return out, sums[0], sums[1]
+    device = _device_of(dY, X, mean, rstd, weight, residual_grad, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return layer_norm_backward(dY, X, mean, rstd, weight, residual_grad, out)
+    lib = load_library()
+    t = _TYPE_OF_DTYPE.get(dY.dtype)
+    if t is None or dY.dim() != 2:
+        raise TypeError("dY must be a 2-D bfloat16, float16 or float32 tensor")
+    lddy = _row_major(dY, "dY")
+    rows, cols = dY.shape
+    ldx = _matrix(X, "X", rows, cols, dY.dtype)
+    _vector(mean, "mean", rows, (torch.float32,))
+    _vector(rstd, "rstd", rows, (torch.float32,))
+    param, gamma, rgrad, ldr = 2, None, None, 0
+    if weight is not None:
+        _vector(weight, "weight", cols, _TYPE_OF_DTYPE)
+        param, gamma = _TYPE_OF_DTYPE[weight.dtype], weight.data_ptr()
+    if residual_grad is not None:
+        ldr = _matrix(residual_grad, "residual_grad", rows, cols, dY.dtype)
+        rgrad = residual_grad.data_ptr()
+    if out is None:
+        out, lddx = dY.new_empty((rows, cols)), cols
+    else:
+        lddx = _matrix(out, "out", rows, cols, dY.dtype)
+    dweight, dbias = dY.new_empty(cols, dtype=torch.float32), dY.new_empty(cols, dtype=torch.float32)
+    ws, addr, nbytes = _workspace(dY, lib.layer_norm_backward_workspace_size(t, rows, cols))
+    _check(lib.layer_norm_backward(t, rows, cols, dY.data_ptr(), lddy, X.data_ptr(), ldx, mean.data_ptr(),
+                                   rstd.data_ptr(), param, gamma, rgrad, ldr, out.data_ptr(), lddx,
+                                   dweight.data_ptr(), dbias.data_ptr(), addr, nbytes,
+                                   torch._C._cuda_getCurrentRawStream(device)))
+    return out, dweight, dbias
 
 
 # ---------------------------------------------------------- Newton-Schulz
@@ -788,28 +847,29 @@ def newton_schulz(G, steps=5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7,
     float16 or float32) orthogonalised by ``steps`` Newton-Schulz steps of the
     odd polynomial with ``coefficients`` (a, b, c); see gemm_f32.h.  ``out``
     (G's shape and dtype) may be G."""
-    with _Launch(stream, G, out) as launch:
-        lib = load_library()
-        if G.dim() not in (2, 3) or G.dtype not in _TYPE_OF_DTYPE:
-            raise TypeError("G must be a 2-D or 3-D bfloat16, float16 or float32 tensor")
-        if out is None:
-            out = torch.empty(tuple(G.shape), dtype=G.dtype, device=G.device)
-        elif out.shape != G.shape or out.dtype != G.dtype:
-            raise ValueError("out must have G's shape and dtype")
-        batch = G.shape[0] if G.dim() == 3 else 1
-        rows, cols = G.shape[-2:]
+    device = _device_of(G, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return newton_schulz(G, steps, coefficients, eps, out)
+    lib = load_library()
+    t = _TYPE_OF_DTYPE.get(G.dtype)
+    if t is None or G.dim() not in (2, 3):
+        raise TypeError("G must be a 2-D or 3-D bfloat16, float16 or float32 tensor")
+    if out is None:
+        out = G.new_empty(G.shape)
+    elif out.shape != G.shape or out.dtype is not G.dtype:
+        raise ValueError("out must have G's shape and dtype")
+    batch = G.shape[0] if G.dim() == 3 else 1
+    rows, cols = G.shape[-2:]
 
-        def strides(t, what):
-            ld = _ld_any(t if t.dim() == 2 else t.as_strided(t.shape[1:], t.stride()[1:]), what)
-            step = t.stride(0) if t.dim() == 3 and batch > 1 else max(rows - 1, 0) * ld + cols
-            return ld, step
+    def strides(m, what):
+        ld = _row_major(m if m.dim() == 2 else m.as_strided(m.shape[1:], m.stride()[1:]), what)
+        return ld, (m.stride(0) if m.dim() == 3 and batch > 1 else max(rows - 1, 0) * ld + cols)
 
-        ldg, stride_g = strides(G, "G")
-        ldo, stride_o = strides(out, "out")
-        t = _TYPE_OF_DTYPE[G.dtype]
-        a, b, c = (float(v) for v in coefficients)
-        nbytes = lib.newton_schulz_workspace_size(t, batch, rows, cols)
-        ws = launch.workspace(nbytes) if nbytes > 0 else None      # -1: the call itself names the error
-        _check(lib.newton_schulz(t, batch, rows, cols, G.data_ptr(), ldg, stride_g, int(steps), a, b, c, float(eps),
-                                 out.data_ptr(), ldo, stride_o, _addr(ws), max(nbytes, 0), launch.handle))
+    ldg, stride_g = strides(G, "G")
+    ldo, stride_o = strides(out, "out")
+    a, b, c = (float(v) for v in coefficients)
+    ws, addr, nbytes = _workspace(G, lib.newton_schulz_workspace_size(t, batch, rows, cols))
+    _check(lib.newton_schulz(t, batch, rows, cols, G.data_ptr(), ldg, stride_g, int(steps), a, b, c, float(eps),
+                             out.data_ptr(), ldo, stride_o, addr, nbytes, torch._C._cuda_getCurrentRawStream(device)))
     return out
