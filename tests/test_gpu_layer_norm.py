@@ -14,7 +14,7 @@ EPS = 1e-5
 # one row, one column, both sides of every chunk and group width, long rows
 SIZES = [(1, 1), (5, 1), (1, 2), (3, 7), (64, 8), (4, 63), (9, 64), (5, 65), (2, 511), (33, 512), (7, 513), (300, 1000),
          (1000, 1001), (17, 2047), (6, 2048), (3, 2050), (2, 4095), (70, 4096), (8, 4104), (5, 8192), (3, 8200),
-         (2, 16384), (3, 16385), (2, 33000), (1, 70001), (3000, 24), (5003, 130), (2100, 768)]
+         (2, 16384), (3, 16385), (2, 33000), (1, 70001), (3000, 24), (5003, 130), (2100, 768), (600, 5120), (40, 14336), (1030, 512)]
 
 
 def make(seed, M, N, dtype, shift=0.5, scale=2.0):
