@@ -70,8 +70,10 @@ int check_linear(int op_a, int op_b, int format, int64_t M, int64_t N, int64_t K
         (ep->residual != nullptr && !extent_fits(M, N, ep->ld_residual)) ||
         (uses_z && !extent_fits(M, N, ep->ld_preact)))
         return GEMM_F32_ERR_TOO_LARGE;
-    const int64_t blocks16 = ((M + 15) / 16) * ((N + 15) / 16);
-    if (blocks16 > (int64_t)0xFFFFFFFF / 256) return GEMM_F32_ERR_TOO_LARGE;
+    // at most one block of 256 threads per 64 x 64 entries: keep the grid below
+    // 2^32 work-items
+    const int64_t blocks64 = ((M + 63) / 64) * ((N + 63) / 64);
+    if (blocks64 > (int64_t)0xFFFFFFFF / 256) return GEMM_F32_ERR_TOO_LARGE;
     return GEMM_F32_OK;
 }
 

@@ -174,6 +174,9 @@ struct Plan {
 };
 
 int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
+// A factor of `rows` rows whose copies' 32-bit offsets hold, a tile's
+// overhang included.
+bool offsets_hold(int64_t rows, int64_t ld) { return ld < (1ll << 30) / (rows + 256); }
 
 // Estimated time of an M x N x K product on `tile` x `tile` tiles, in us
 // (MI355X, each kernel alone).  A round of 256 blocks takes the K loop,
@@ -217,13 +220,6 @@ Plan make_plan(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
     q.K = p.K;
     q.lda = p.lda;
     q.ldb = p.ldb;
-    if (p.M <= kLinearRowsMax && !op_a && p.K > 0 && p.K < (1 << 30)) {
-        q.kind = kRows;
-        q.splits = linear_rows_splits(p.M, p.N, p.K);
-        if (q.splits > 1 || e.gradient) q.main_bytes = align256(4 * (int64_t)q.splits * p.M * p.N);
-        q.part_rows = e.bias_grad ? 1 : 0;
-        return q;
-    }
     // The tile kernels copy 4 bytes at a time at least: even leading
     // dimensions, widths of mn-contiguous factors, and K where a factor is
     // k-contiguous; the split-K ones 16 bytes along K.
@@ -232,11 +228,26 @@ Plan make_plan(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
     q.pack_a = pad_k || (reinterpret_cast<uintptr_t>(p.A) & 3) != 0 || p.lda % 2 != 0 || (op_a && p.M % 2 != 0);
     q.pack_b = pad_k || (reinterpret_cast<uintptr_t>(p.B) & 3) != 0 || p.ldb % 2 != 0 || (!op_b && p.N % 2 != 0);
     if (pad_k) q.K = (int)(pad8(p.K) > INT_MAX ? 0 : pad8(p.K));
+    // Few rows, unless the weight is stored N x K and 64-column tiles fill
+    // half the CUs: those copy it in whole cache lines (24 x 8192 x 4096: 16.5
+    // us on 64 tiles, 20.9 on the few-row kernel; with N = 4096 12.6 against
+    // 10.1 for one row).
+    const bool tiles64 = op_b && p.N > 64 * 127 && p.K % 8 == 0 && !q.pack_a && !q.pack_b &&
+                         offsets_hold(p.M, p.lda) && offsets_hold(p.N, p.ldb);
+    if (p.M <= kLinearRowsMax && !op_a && p.K > 0 && p.K < (1 << 30) && !tiles64) {
+        q.kind = kRows;
+        q.K = p.K;
+        q.pack_a = q.pack_b = false;
+        q.splits = linear_rows_splits(p.M, p.N, p.K);
+        if (q.splits > 1 || e.gradient) q.main_bytes = align256(4 * (int64_t)q.splits * p.M * p.N);
+        q.part_rows = e.bias_grad ? 1 : 0;
+        return q;
+    }
     const int64_t a_rows = op_a ? q.K : p.M, b_rows = op_b ? p.N : q.K;
     if (q.pack_a) q.lda = pad8(op_a ? p.M : q.K);
     if (q.pack_b) q.ldb = pad8(op_b ? q.K : p.N);
     q.kind = kTiles;
-    if (q.K == 0 || 2 * (a_rows + 256) * q.lda >= (1ll << 31) || 2 * (b_rows + 256) * q.ldb >= (1ll << 31)) {
+    if (q.K == 0 || !offsets_hold(a_rows, q.lda) || !offsets_hold(b_rows, q.ldb)) {
         q.kind = kGeneral;
         q.pack_a = q.pack_b = false;
         q.main_bytes = align256(4 * (int64_t)p.M * p.N);

@@ -1,8 +1,9 @@
 // linear_rows.hip -- the product with its epilogue for few rows (a decoder's
 // tokens): M <= 64, where the weight is read once and its bytes set the time.
 //
-// Blocks of four waves take 128 columns and a share of K; wave w of a block
-// takes its 32-deep steps w, w + 4, ...  A step is 8 matrix instructions
+// Blocks of four waves take 128 columns and a share of K, each wave a quarter
+// of it in 32-deep steps (consecutive ones: with the weight stored N x K two
+// steps share a cache line).  A step is 8 matrix instructions
 // v_mfma_f32_16x16x32 per 16 rows of X, straight from registers: X's fragment
 // (lane l: row l % 16, k 8 (l / 16) .. + 7) and, for instruction j, the weight's
 // column 8 (l % 16) + j of the block.  With the weight stored N x K that is one
@@ -49,8 +50,10 @@ void linear_rows_kernel(Gemm16Args p, EpilogueArgs e, int k_per_split, float* pl
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int n0 = blockIdx.x * kCols;
-    const int k_begin = blockIdx.y * k_per_split;
-    const int k_end = min(p.K, k_begin + k_per_split);      // k_per_split: a multiple of 4 kStep
+    // The block's share of K, a quarter of it (whole steps) for each wave.
+    const int share = k_per_split / kWaves;                 // k_per_split: a multiple of kWaves kStep
+    const int k_begin = (int)blockIdx.y * k_per_split + wave * share;
+    const int k_end = min(p.K, k_begin + share);
 
     struct Step {
         u32x4 x[MT], w[8];
@@ -58,14 +61,24 @@ void linear_rows_kernel(Gemm16Args p, EpilogueArgs e, int k_per_split, float* pl
     const uint16_t* xrow[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) xrow[t] = p.A + (int64_t)min(16 * t + c, p.M - 1) * p.lda;
+    // Columns as loaded: those past N repeat others, and a chunk across N reads
+    // on into the next row -- unless there is none, or rows are too short for
+    // it to be the next one.
     const bool inside = n0 + kCols <= p.N;                  // the block's columns all exist
+    const int whole_k = inside ? p.K : p.ldb >= 8 ? p.K - 1 : 0;   // rows below it load whole chunks
+    const uint16_t* wcol[TB ? 8 : 1];
+    if constexpr (TB) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wcol[j] = p.B + (int64_t)min(n0 + 8 * c + j, p.N - 1) * p.ldb;
+    } else {
+        wcol[0] = p.B + (n0 + 8 * c < p.N ? n0 + 8 * c : 0);
+    }
     auto load = [&](Step& s, int k0) __attribute__((always_inline)) {
         const int k = k0 + 8 * g;
-        if (k0 + kStep <= k_end && (TB || inside)) {
+        if (k0 + kStep <= k_end && (TB || k0 + kStep <= whole_k)) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint16_t* q = TB ? p.B + (int64_t)min(n0 + 8 * c + j, p.N - 1) * p.ldb + k
-                                       : p.B + (int64_t)(k + j) * p.ldb + n0 + 8 * c;
+                const uint16_t* q = TB ? wcol[TB ? j : 0] + k : wcol[0] + (int64_t)(k + j) * p.ldb;
                 __builtin_memcpy(&s.w[j], q, 16);
             }
 #pragma unroll
@@ -74,7 +87,7 @@ void linear_rows_kernel(Gemm16Args p, EpilogueArgs e, int k_per_split, float* pl
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if constexpr (TB)
-                    s.w[j] = load8(p.B + (int64_t)min(n0 + 8 * c + j, p.N - 1) * p.ldb + k, k_end - k);
+                    s.w[j] = load8(wcol[j] + k, k_end - k);
                 else
                     s.w[j] = load8(p.B + (int64_t)(k + j) * p.ldb + n0 + 8 * c, k + j < k_end ? p.N - (n0 + 8 * c) : 0);
             }
@@ -107,12 +120,12 @@ void linear_rows_kernel(Gemm16Args p, EpilogueArgs e, int k_per_split, float* pl
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[t][j] = mfma16x16<FMT>(s.x[t], b[j], acc[t][j]);
     };
-    int k0 = k_begin + kStep * wave;
+    int k0 = k_begin;
     if (k0 < k_end) {
         Step s0, s1;
         load(s0, k0);
         for (;;) {
-            const int k1 = k0 + kWaves * kStep, k2 = k1 + kWaves * kStep;
+            const int k1 = k0 + kStep, k2 = k1 + kStep;
             if (k1 < k_end) load(s1, k1);
             compute(s0);
             if (k1 >= k_end) break;
@@ -172,10 +185,11 @@ void launch_tiles(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int
 
 }  // namespace
 
-// Two blocks per CU, but at least two steps per wave, and no empty split.
+// One block per CU (24 x 8192 x 4096: 17 us with 256 blocks, 20 with 512 or
+// 128), but at least two steps per wave, and no empty split.
 int linear_rows_splits(int M, int N, int K) {
     const int blocks = ceil_div(N, kCols), steps = ceil_div(K, kStep * kWaves);
-    int splits = 512 / blocks;
+    int splits = 256 / blocks;
     if (splits > steps / 2) splits = steps / 2;
     if (splits < 1) return 1;
     return ceil_div(steps, steps_per_split(K, splits));

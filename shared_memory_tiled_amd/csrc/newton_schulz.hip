@@ -100,7 +100,10 @@ void ns_write_kernel(NewtonSchulzArgs a, float unscale, const uint16_t* x, int r
     }
 }
 
-// Workspace: partial norms, X's planes twice, S's and T's planes, d and e.
+// Workspace: partial norms, X's planes twice, S's and T's planes, d and e; then
+// room for a large tile's rows past a matrix's last, which the product kernels
+// copy and do not use (a copy's scalar offset, here the second plane's, is no
+// part of its range check).
 struct Layout {
     int rp, cp, mp;
     int64_t x_stride, s_stride;               // elements per matrix
@@ -120,7 +123,7 @@ Layout layout(const NewtonSchulzArgs& a) {
     l.t = l.s + 2 * l.s_stride * a.batch;
     l.d = l.t + 2 * l.s_stride * a.batch;
     l.e = l.d + 4 * (int64_t)l.mp * a.batch;
-    l.bytes = l.e + 4 * (int64_t)l.mp * a.batch;
+    l.bytes = l.e + 4 * (int64_t)l.mp * a.batch + 2 * 256 * (int64_t)(l.rp > l.cp ? l.rp : l.cp);
     return l;
 }
 

@@ -58,7 +58,7 @@ def test_activations(kind, dtype, op_b):
 # every tile, one-value factors
 SIZES = [(1, 64, 64), (1, 1, 1), (1, 1000, 4096), (2, 129, 8), (3, 7, 5), (8, 256, 8192), (15, 130, 96), (16, 128, 32),
          (17, 1000, 264), (31, 33, 4096), (32, 512, 1000), (33, 66, 40), (48, 4096, 136), (63, 65, 257), (64, 640, 1024),
-         (65, 320, 1024), (100, 100, 100), (127, 129, 131), (200, 1, 64), (257, 255, 1), (1000, 500, 24),
+         (3, 8200, 136), (40, 8192, 72), (5, 9, 300), (65, 320, 1024), (100, 100, 100), (127, 129, 131), (200, 1, 64), (257, 255, 1), (1000, 500, 24),
          (1000, 1002, 998), (999, 1001, 999), (2048, 200, 4096)]
 
 
