@@ -9,13 +9,14 @@
 // here before the entry leaves the chip.
 //
 // The product runs on the tiles of least estimated time (pick_tile, below),
-// on the few-row kernel up to 64 rows, or, split by rows, on 256 x 256 tiles
-// and smaller ones for the rest.  Factors those kernels do not take (an odd
-// width, leading dimension or K, a base of 2-byte alignment) are first copied
-// into the workspace with padded rows: two passes over a factor cost less
-// than the element-wise kernels would (999 x 1001 x 77 ..).  What is left
-// (factors of 2 GiB and more, K = 0) runs the library's product into a
-// binary32 matrix in the workspace and the epilogue as a pass over it.
+// on the few-row kernel up to 64 rows, split by rows on 256 x 256 tiles and
+// smaller ones for the rest, or, few tiles and a long K, with K split over
+// blocks.  Factors those kernels do not take (an odd width, leading dimension
+// or K, a base of 2-byte alignment) are first copied into the workspace with
+// padded rows: that costs less than the product's element-wise kernels would
+// (999 x 1001 x 1001: 15 us against 100).  What is left (factors of 2 GiB and
+// more, K = 0) runs the library's product into a binary32 matrix in the
+// workspace and the epilogue as a pass over it.
 //
 // epilogue_kernel is the pass over finished sums: it adds the planes of a
 // product whose K was split over blocks (or reads a matrix of 16-bit
@@ -167,6 +168,7 @@ struct Plan {
     // split), rest_tile for the others
     int tile, rows, rest_tile;
     int splits;                               // kRows: blocks along K
+    int k_share;                              // kTiles on 64 tiles: K per block, if below K
     bool pack_a, pack_b;                      // factors copied into the workspace
     int K;                                    // as the product runs it (padded if packed)
     int64_t lda, ldb;                         // of the copies, where packed
@@ -183,13 +185,18 @@ bool offsets_hold(int64_t rows, int64_t ld) { return ld < (1ll << 30) / (rows + 
 // `slow` per 64-deep phase once all CUs are busy (`fast` up to half of them:
 // the clock drops, and the small tiles' copies share the L2), and `fixed` for
 // start and epilogue (with a kept pre-activation; the activation adds the
-// same everywhere).  128 tiles copy k-contiguous factors in runs of 64 bytes:
-// 0.06 more for each.  4096^3: 106 / 135 / 165 / 160 / 262 us on 256 / 192 /
-// 160 / 128 / 64 tiles; 1000 x 2000 x 1000: 41 / 26 / 22 / 21 / 17.
+// same everywhere).  64 tiles: 4.4 and 0.0037 per k, but 0.0017 up to 16 of
+// them whose factors are both mn-contiguous (the L2 has whole lines for those).
+// 128 tiles copy k-contiguous factors in runs of 64 bytes: 0.06 more for each.  4096^3: 106 / 135 / 165 / 160 / 262
+// us on 256 / 192 / 160 / 128 / 64 tiles; 1000 x 2000 x 1000: 41 / 26 / 22 / 21
+// / 17.
 double tile_time(int tile, int M, int N, int K, int k_contiguous) {
     const double tiles = (double)ceil_div(M, tile) * ceil_div(N, tile);
     const double rounds = ceil(tiles / 256.0);
-    if (tile == 64) return rounds * (4.4 + 0.0037 * K);
+    if (tile == 64) {
+        const double shared = k_contiguous ? 1.0 : fmin(1.0, fmax(0.0, (tiles - 16.0) / 48.0));
+        return rounds * (4.4 + (0.0017 + 0.0020 * shared) * K);
+    }
     static const struct { int tile; double fast, slow, fixed; } kCost[] = {
         {256, 1.00, 1.38, 20.0}, {192, 0.70, 0.86, 13.0}, {160, 0.62, 0.70, 10.8}, {128, 0.31, 0.36, 16.0}};
     for (const auto& c : kCost)
@@ -213,6 +220,60 @@ int pick_tile(int M, int N, int K, bool split_k, int k_contiguous, double* time)
         }
     }
     return best;
+}
+
+// Share of K per block on 64 tiles whose blocks split K, for few tiles and a
+// long K: at most 256 blocks, shares of at least 256.  time: the product's,
+// no less than its factors' read at 4.8 TB/s, and the pass's over the planes
+// (from 5 us; 4 TB/s).  A small layer's weight gradient: 256 x 256 x 8192 11.5
+// us against 18.3 unsplit, 512 x 512 x 8192 19 against 36; 24 x 8192 x 4096,
+// bound by its weight's read, stays unsplit (16.5 against 18.1).
+int pick_share(int M, int N, int K, double* time) {
+    const int64_t tiles = (int64_t)ceil_div(M, 64) * ceil_div(N, 64);
+    int64_t splits = 256 / tiles;
+    if (splits > K / 256) splits = K / 256;
+    *time = 1e30;
+    if (splits < 2) return K;
+    const int share = (ceil_div(K, (int)splits) + 63) / 64 * 64;
+    const double product = fmax(4.4 + 0.0037 * share, 4.0 + 2.0 * ((double)M + N) * K / 4.8e6);
+    *time = product + 5.0 + 8.0 * ceil_div(K, share) * (double)M * N / 4e6;
+    return share;
+}
+
+// The estimates' choice among 64 tiles with K split over blocks and all
+// tiles; fills q's tile, rows, rest_tile and k_share and returns the time.
+double pick_product(int M, int N, int K, bool split_k, int k_contiguous, Plan* q) {
+    double time;
+    q->tile = pick_tile(M, N, K, split_k, k_contiguous, &time);
+    q->rows = M;
+    q->rest_tile = q->tile;
+    q->k_share = K;
+    // All rounds of 256 x 256 tiles but the last, the rows of that one on
+    // smaller tiles.
+    const int64_t tn = ceil_div(N, 256), tiles = ceil_div(M, 256) * tn, full = tiles / 256;
+    const int64_t rows = full > 0 ? 256 * (256 * full / tn) : 0;
+    if (rows > 0 && rows < M) {
+        double rest;
+        const int rest_tile = pick_tile(M - (int)rows, N, K, split_k, k_contiguous, &rest);
+        const double top = tile_time(256, (int)rows, N, K, k_contiguous);
+        if (top + rest < time) {
+            time = top + rest;
+            q->tile = 256;
+            q->rows = (int)rows;
+            q->rest_tile = rest_tile;
+        }
+    }
+    if (split_k) {
+        double split;
+        const int share = pick_share(M, N, K, &split);
+        if (split < time) {
+            time = split;
+            q->tile = q->rest_tile = 64;
+            q->rows = M;
+            q->k_share = share;
+        }
+    }
+    return time;
 }
 
 Plan make_plan(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
@@ -243,6 +304,20 @@ Plan make_plan(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
         q.part_rows = e.bias_grad ? 1 : 0;
         return q;
     }
+    const int kc = (op_a ? 0 : 1) + (op_b ? 1 : 0);
+    double time = q.K > 0 ? pick_product(p.M, p.N, q.K, both_mn || q.K % 8 == 0, kc, &q) : 0.0;
+    // K even but no multiple of 8 leaves the large tiles only: with few tiles
+    // and a long K the copy into padded rows (from 4 us; 3 TB/s) and the split
+    // of K cost less (395 x 72 x 2132: 12 us against 28).
+    if (!both_mn && !pad_k && p.K % 8 != 0 && p.K < INT_MAX - 8) {
+        Plan packed = q;
+        packed.K = (int)pad8(p.K);
+        const double copy = 4.0 + 4.0 * ((double)p.M + p.N) * packed.K / 3e6;
+        if (copy + pick_product(p.M, p.N, packed.K, true, kc, &packed) < time) {
+            q = packed;
+            q.pack_a = q.pack_b = true;
+        }
+    }
     const int64_t a_rows = op_a ? q.K : p.M, b_rows = op_b ? p.N : q.K;
     if (q.pack_a) q.lda = pad8(op_a ? p.M : q.K);
     if (q.pack_b) q.ldb = pad8(op_b ? q.K : p.N);
@@ -256,26 +331,7 @@ Plan make_plan(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
     }
     if (q.pack_a) q.a_bytes = align256(2 * a_rows * q.lda);
     if (q.pack_b) q.b_bytes = align256(2 * b_rows * q.ldb);
-    const bool split_k = both_mn || q.K % 8 == 0;
-    const int kc = (op_a ? 0 : 1) + (op_b ? 1 : 0);
-    double time;
-    q.tile = pick_tile(p.M, p.N, q.K, split_k, kc, &time);
-    q.rows = p.M;
-    q.rest_tile = q.tile;
-    // All rounds of 256 x 256 tiles but the last, the rows of that one on
-    // smaller tiles.
-    const int64_t tn = ceil_div(p.N, 256), tiles = ceil_div(p.M, 256) * tn, full = tiles / 256;
-    const int64_t rows = full > 0 ? 256 * (256 * full / tn) : 0;
-    if (rows > 0 && rows < p.M) {
-        double rest;
-        const int rest_tile = pick_tile(p.M - (int)rows, p.N, q.K, split_k, kc, &rest);
-        const double top = tile_time(256, (int)rows, p.N, q.K, kc);
-        if (top + rest < time) {
-            q.tile = 256;
-            q.rows = (int)rows;
-            q.rest_tile = rest_tile;
-        }
-    }
+    if (q.k_share < q.K) q.main_bytes = align256(4 * (int64_t)ceil_div(q.K, q.k_share) * p.M * p.N);
     if (e.bias_grad)
         q.part_rows = ceil_div(q.rows, q.tile) + (q.rows < p.M ? ceil_div(p.M - q.rows, q.rest_tile) : 0);
     return q;
@@ -283,7 +339,7 @@ Plan make_plan(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
 
 int64_t sums_bytes(const Plan& q, const EpilogueArgs& e) {
     if (!e.bias_grad) return 0;
-    return q.kind == kTiles ? align256(4 * q.part_rows * e.N) : epilogue_pass_workspace(e.M, e.N);
+    return q.kind == kTiles && q.k_share == q.K ? align256(4 * q.part_rows * e.N) : epilogue_pass_workspace(e.M, e.N);
 }
 
 // rows x cols 16-bit values (leading dimension ld_in, any alignment) into
@@ -397,6 +453,11 @@ hipError_t launch_linear(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t
     // dword.  The epilogue keeps to e.M and e.N.
     if (op_a) r.M = p.M + p.M % 2;
     if (!op_b) r.N = p.N + p.N % 2;
+    if (q.k_share < q.K) {
+        err = launch_linear_ksplit_planes(r, e.M, e.N, s, format, op_a, op_b, q.k_share, main);
+        if (err != hipSuccess) return err;
+        return launch_epilogue_pass(e, 2, main, p.N, ceil_div(q.K, q.k_share), (int64_t)p.M * p.N, partials, s);
+    }
     float* const part = e.bias_grad ? partials : nullptr;
     const bool split = q.rows < p.M;
     Gemm16Args top = r;

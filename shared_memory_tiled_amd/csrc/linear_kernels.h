@@ -25,6 +25,11 @@ hipError_t launch_linear_ksplit128(const Gemm16Args& p, const EpilogueArgs& e, h
 hipError_t launch_linear_ksplit(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_a,
                                 int op_b, float* partials);
 
+// The 64 tiles with K split over blocks too: k_share (a multiple of 64) of K
+// each, a plane of M x N floats per share.
+hipError_t launch_linear_ksplit_planes(const Gemm16Args& p, int M, int N, hipStream_t s, int format, int op_a, int op_b,
+                                       int k_share, float* planes);
+
 // Few rows (linear_rows.hip): M <= kLinearRowsMax, A as stored, any alignment
 // and sizes.  K is split over `splits` blocks; with one the epilogue runs in
 // the kernel (forward mode), else the planes (M x N floats each) go to `planes`.

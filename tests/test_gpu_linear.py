@@ -59,7 +59,7 @@ def test_activations(kind, dtype, op_b):
 SIZES = [(1, 64, 64), (1, 1, 1), (1, 1000, 4096), (2, 129, 8), (3, 7, 5), (8, 256, 8192), (15, 130, 96), (16, 128, 32),
          (17, 1000, 264), (31, 33, 4096), (32, 512, 1000), (33, 66, 40), (48, 4096, 136), (63, 65, 257), (64, 640, 1024),
          (3, 8200, 136), (40, 8192, 72), (5, 9, 300), (65, 320, 1024), (100, 100, 100), (127, 129, 131), (200, 1, 64), (257, 255, 1), (1000, 500, 24),
-         (1000, 1002, 998), (999, 1001, 999), (2048, 200, 4096)]
+         (1000, 1002, 998), (999, 1001, 999), (2048, 200, 4096), (200, 190, 5000), (395, 72, 2132), (132, 414, 3923), (130, 130, 2050)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=str)
@@ -161,7 +161,7 @@ def grad_tol(D, V, Sv, K, Zd, kind, dtype):
 
 @pytest.mark.parametrize("kind", R.ACTS)
 @pytest.mark.parametrize("size", [(1, 40, 64), (20, 200, 136), (70, 200, 136), (333, 1000, 72), (999, 1001, 77),
-                                  (2300, 2310, 264), (4100, 4090, 72)], ids=str)
+                                  (2300, 2310, 264), (4100, 4090, 72), (130, 200, 3000)], ids=str)
 def test_linear_grad(size, kind):
     M, N, K = size
     for dtype, out_dtype, residual in [(torch.bfloat16, None, False), (torch.float16, torch.float32, True)]:
@@ -207,7 +207,7 @@ def test_activation_backward(size, kind):
 
 
 @pytest.mark.parametrize("size", [(1, 64, 64), (64, 64, 64), (100, 72, 40), (999, 300, 130), (1001, 77, 501),
-                                  (3001, 1000, 520), (2050, 2100, 2200)], ids=str)
+                                  (3001, 1000, 520), (2050, 2100, 2200), (8193, 128, 256)], ids=str)
 @pytest.mark.parametrize("op_b", ["N", "T"])
 def test_linear_backward(size, op_b):
     M, N, K = size
