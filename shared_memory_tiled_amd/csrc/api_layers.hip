@@ -17,6 +17,10 @@ bool misaligned_type(const void* p, int type) { return ((uintptr_t)p & (type == 
 bool misaligned16(const void* p) { return ((uintptr_t)p & 15u) != 0; }
 int64_t at_least_one(int64_t n) { return n > 1 ? n : 1; }
 
+// Columns of the epilogue pass: 256 threads per 128 of them, below 2^32
+// work-items.
+constexpr int64_t kMaxPassCols = INT_MAX - 127;
+
 int check_device() {
     int dev = -1;
     return hipGetDevice(&dev) == hipSuccess && dev >= 0 ? GEMM_F32_OK : GEMM_F32_ERR_DEVICE;
@@ -135,7 +139,7 @@ extern "C" int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, in
 }
 
 extern "C" int64_t activation_grad_workspace_size(int64_t M, int64_t N) {
-    if (M < 0 || N < 0 || M > INT_MAX || N > INT_MAX) return -1;
+    if (M < 0 || N < 0 || M > INT_MAX || N > kMaxPassCols) return -1;
     return M == 0 || N == 0 ? 0 : epilogue_pass_workspace((int)M, (int)N);
 }
 
@@ -150,7 +154,7 @@ extern "C" int activation_grad(int activation, int format, int64_t M, int64_t N,
         return GEMM_F32_ERR_INVALID_LD;
     if (N == 0) return GEMM_F32_OK;
     if (misaligned(bias_grad)) return GEMM_F32_ERR_MISALIGNED;
-    if (M > INT_MAX || N > INT_MAX) return GEMM_F32_ERR_TOO_LARGE;
+    if (M > INT_MAX || N > kMaxPassCols) return GEMM_F32_ERR_TOO_LARGE;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     int st;
     if (M == 0) {

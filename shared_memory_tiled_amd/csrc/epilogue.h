@@ -142,9 +142,12 @@ __device__ __forceinline__ float activate_derivative_one(float z) {
     if constexpr (ACT == kActGeluTanh) {
         const float u2 = -2.0f * kTanhC * z * __builtin_fmaf(kTanhCubic * z, z, 1.0f);
         const float s = fast_rcp(1.0f + fast_exp(u2));
-        // d u2 / dz = -2 c (1 + 3 0.044715 z^2); s' = -s (1 - s) du2
-        const float du = 2.0f * kTanhC * __builtin_fmaf(3.0f * kTanhCubic * z, z, 1.0f);
-        return __builtin_fmaf(z * du, s * (1.0f - s), s);
+        // d u2 / dz = -2 c (1 + 3 0.044715 z^2); s' = -s (1 - s) du2.  Past 30, s
+        // is 0 or 1 and s (1 - s) is 0: z^2 is held there, so that it meets no
+        // infinity.
+        const float far = __builtin_fabsf(z) > 30.0f ? 30.0f : z;
+        const float du = 2.0f * kTanhC * __builtin_fmaf(3.0f * kTanhCubic * far, far, 1.0f);
+        return __builtin_fmaf(z, du * (s * (1.0f - s)), s);
     }
     if constexpr (ACT == kActSilu) {
         const float s = fast_rcp(1.0f + fast_exp(-z));

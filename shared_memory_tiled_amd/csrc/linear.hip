@@ -44,12 +44,13 @@ void epilogue_kernel(EpilogueArgs e, const void* in, int64_t ld, int planes, int
     const int tc = threadIdx.x % 32, tr = threadIdx.x / 32;
     const int col = blockIdx.x * kPassCols + 4 * tc;
     const int first = blockIdx.y * rows_per_block;
-    const int last = min(e.M, first + rows_per_block);
+    const int rows = min(e.M - first, rows_per_block);       // first + rows_per_block may pass 2^31
     float sums[4] = {0.f, 0.f, 0.f, 0.f};
     if (col < e.N) {
         float bias[4];
         if constexpr (!GRADIENT) load_bias(e, col, bias);
-        for (int row = first + tr; row < last; row += 8) {
+        for (int r = tr; r < rows; r += 8) {
+            const int row = first + r;
             EpilogueRun<4, GRADIENT> run;
             run.load(e, row, col);
             float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -95,21 +96,26 @@ void epilogue_kernel(EpilogueArgs e, const void* in, int64_t ld, int planes, int
 
 // out[c] = sum of partials[i][c], i < count, in a fixed order: 8 threads take
 // every eighth partial of a column, their sums are added in thread order.
+// 32 columns per block and turn.
+constexpr int kSumBlocks = 1 << 20;
 __global__ __launch_bounds__(256)
 void column_sum_kernel(int count, int n, const float* partials, float* out) {
     __shared__ float part[8][32];
     const int tc = threadIdx.x % 32, tr = threadIdx.x / 32;
-    const int c = blockIdx.x * 32 + tc;
-    float s = 0.f;
-    if (c < n)
-        for (int i = tr; i < count; i += 8) s += partials[(int64_t)i * n + c];
-    part[tr][tc] = s;
-    __syncthreads();
-    if (tr == 0 && c < n) {
-        float t = 0.f;
+    for (int64_t first = 32 * (int64_t)blockIdx.x; first < n; first += 32 * (int64_t)gridDim.x) {
+        const int64_t c = first + tc;
+        float s = 0.f;
+        if (c < n)
+            for (int i = tr; i < count; i += 8) s += partials[(int64_t)i * n + c];
+        part[tr][tc] = s;
+        __syncthreads();
+        if (tr == 0 && c < n) {
+            float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += part[i][tc];
-        out[c] = t;
+            for (int i = 0; i < 8; ++i) t += part[i][tc];
+            out[c] = t;
+        }
+        __syncthreads();                                     // part is read
     }
 }
 
@@ -126,7 +132,9 @@ int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 }  // namespace
 
 hipError_t launch_column_sums(int count, int n, const float* partials, float* out, hipStream_t s) {
-    hipLaunchKernelGGL(column_sum_kernel, dim3(ceil_div(n, 32)), dim3(256), 0, s, count, n, partials, out);
+    const int blocks = ceil_div(n, 32);
+    hipLaunchKernelGGL(column_sum_kernel, dim3(blocks < kSumBlocks ? blocks : kSumBlocks), dim3(256), 0, s, count, n,
+                       partials, out);
     return hipGetLastError();
 }
 

@@ -137,3 +137,29 @@ def test_factor_past_2_gib():
         cols = [0, 1, 16383, 16384, 32999]
         Y, Z, S = R.linear_ref(X, W[cols].t().contiguous(), None, "silu", None)
         R.within(y[:, cols], Y, R.linear_tol(Y, Z, S, K, "silu", None, y.dtype), f"M={M}")
+
+
+def test_activation_backward_rows_to_the_limit():
+    """2^31 - 1 rows of one column: the last block's rows end at the type's
+    last number.  Column sum over five entries that are not zero (exact)."""
+    M = 2 ** 31 - 1
+    say(f"activation gradient of {M} rows")
+    dY = torch.zeros(M, 1, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 12345, 2 ** 30, M - 9, M - 1]
+    for i, r in enumerate(rows):
+        dY[r] = float(2 ** i)
+    dz, db = binding.activation_backward(dY, activation="none")
+    assert db.item() == 31.0
+    assert [dz[r].item() for r in rows] == [1.0, 2.0, 4.0, 8.0, 16.0]
+    assert torch.equal(dz[M - 4096:], dY[M - 4096:])
+
+
+def test_column_sums_of_many_columns():
+    """More columns than the column sums have blocks for at a time."""
+    M, N = 3, 40_000_001
+    say(f"activation gradient of {M} x {N}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    dY = torch.randint(-8, 9, (M, N), generator=gen, device="cuda").bfloat16()
+    _, db = binding.activation_backward(dY, return_dz=False)
+    assert torch.equal(db, dY.float().sum(0))                    # small integers: exact

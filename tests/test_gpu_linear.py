@@ -309,3 +309,18 @@ def test_streams_and_graph_replay():
         torch.cuda.synchronize()
         for o in outs:
             assert torch.equal(o, eager[0])
+
+
+@pytest.mark.parametrize("kind", R.ACTS[1:])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_derivative_far_from_zero(kind, dtype):
+    """Finite pre-activations of any size have a finite gradient: 0 or dY
+    where the activation is flat or the identity."""
+    far = [9.0, 29.0, 31.0, 100.0, 3000.0, 65504.0]
+    if dtype is torch.bfloat16:
+        far += [1e10, 1e13, 1e15, 1e19, 1e25, 3e38]
+    z = torch.tensor([s * v for v in far for s in (1, -1)], device="cuda").to(dtype)[None, :].repeat(5, 1).contiguous()
+    dY = normal(1, *z.shape, dtype=dtype)
+    D = dY.double() * R.act_derivative(z.double(), kind)
+    dz, _ = binding.activation_backward(dY, z, kind)
+    R.within(dz, D, R.HALF[dtype] * D.abs() + R.TINY[dtype] + 32 * R.U * dY.double().abs(), kind)

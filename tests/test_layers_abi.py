@@ -193,3 +193,11 @@ def test_tensor_forms_refuse_host_tensors():
                lambda: binding.newton_schulz(x)):
         with pytest.raises(TypeError):
             fn()
+
+
+def test_activation_grad_column_limit(lib):
+    """One block of 256 threads per 128 columns: the grid ends below 2^32."""
+    n = 2 ** 31 - 64
+    args = (0, 0, 1, n, FAKE, n, None, 0, None, 0, FAKE)
+    assert lib.activation_grad_workspace_size(1, n) == -1
+    assert lib.activation_grad(*args, FAKE, BIG, None) == CODES["GEMM_F32_ERR_TOO_LARGE"]
