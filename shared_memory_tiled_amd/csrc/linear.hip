@@ -94,25 +94,34 @@ void epilogue_kernel(EpilogueArgs e, const void* in, int64_t ld, int planes, int
     }
 }
 
-// out[c] = sum of partials[i][c], i < count, in a fixed order: 8 threads take
-// every eighth partial of a column, their sums are added in thread order.
-// 32 columns per block and turn.
+// out[c] = sum of partials[i][c], i < count, in a fixed order: 32 threads take
+// every 32nd partial of a column, four loads in flight, and their sums are
+// added in thread order.  32 columns per block and turn.  125 x 500: 2.8 us
+// against 6.9 with 8 threads per column (both mostly the launch and the loads'
+// latency).
 constexpr int kSumBlocks = 1 << 20;
-__global__ __launch_bounds__(256)
+__global__ __launch_bounds__(1024)
 void column_sum_kernel(int count, int n, const float* partials, float* out) {
-    __shared__ float part[8][32];
+    __shared__ float part[32][33];
     const int tc = threadIdx.x % 32, tr = threadIdx.x / 32;
     for (int64_t first = 32 * (int64_t)blockIdx.x; first < n; first += 32 * (int64_t)gridDim.x) {
         const int64_t c = first + tc;
         float s = 0.f;
-        if (c < n)
-            for (int i = tr; i < count; i += 8) s += partials[(int64_t)i * n + c];
+        if (c < n) {
+            for (int i = tr; i < count; i += 128) {
+                float v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[u] = i + 32 * u < count ? partials[(int64_t)(i + 32 * u) * n + c] : 0.f;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) s += v[u];
+            }
+        }
         part[tr][tc] = s;
         __syncthreads();
         if (tr == 0 && c < n) {
             float t = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t += part[i][tc];
+            for (int i = 0; i < 32; ++i) t += part[i][tc];
             out[c] = t;
         }
         __syncthreads();                                     // part is read
@@ -133,7 +142,7 @@ int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 hipError_t launch_column_sums(int count, int n, const float* partials, float* out, hipStream_t s) {
     const int blocks = ceil_div(n, 32);
-    hipLaunchKernelGGL(column_sum_kernel, dim3(blocks < kSumBlocks ? blocks : kSumBlocks), dim3(256), 0, s, count, n,
+    hipLaunchKernelGGL(column_sum_kernel, dim3(blocks < kSumBlocks ? blocks : kSumBlocks), dim3(1024), 0, s, count, n,
                        partials, out);
     return hipGetLastError();
 }

@@ -31,20 +31,39 @@ constexpr int kThreads = 256;
 constexpr int kNormBlocks = 256;
 
 // The sum of squares in binary64 (no overflow or underflow for any binary32
-// input): block b of matrix blockIdx.y takes rows b, b + 256, ...
+// input).  Block b of matrix blockIdx.y takes runs of 8 columns in turn, four
+// loads in flight (4096^2 bf16: 9.4 us, a row per block and turn 18.3).
 template <int TYPE>
 __global__ __launch_bounds__(kThreads)
 void ns_square_sum_kernel(NewtonSchulzArgs a, double* partials) {
     __shared__ double slots[kThreads];
     const int64_t base = (int64_t)blockIdx.y * a.stride_g;
+    const unsigned chunks = (unsigned)(a.cols + 7) / 8, total = chunks * (unsigned)a.rows;   // below 2^28
+    constexpr unsigned STEP = kNormBlocks * kThreads;
     double s = 0.0;
-    for (int64_t r = blockIdx.x; r < a.rows; r += kNormBlocks)
-        for (int c = 8 * threadIdx.x; c < a.cols; c += 8 * kThreads) {
-            float v[8];
-            load_values<TYPE>(a.G, base + r * a.ldg + c, a.cols - c, v);
+    auto add = [&](const float (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += (double)v[e] * v[e];
+        for (int e = 0; e < 8; ++e) s += (double)v[e] * v[e];
+    };
+    unsigned i = blockIdx.x * kThreads + threadIdx.x;
+    if (a.cols % 8 == 0) {                               // no run in part: loads without a branch
+        for (; i + 3 * STEP < total; i += 4 * STEP) {
+            float v[4][8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const unsigned r = (i + u * STEP) / chunks, c = 8 * (i + u * STEP - r * chunks);
+                load_values<TYPE>(a.G, base + (int64_t)r * a.ldg + c, 8, v[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(v[u]);
         }
+    }
+    for (; i < total; i += STEP) {
+        const unsigned r = i / chunks, c = 8 * (i - r * chunks);
+        float v[8];
+        load_values<TYPE>(a.G, base + (int64_t)r * a.ldg + c, a.cols - (int)c, v);
+        add(v);
+    }
     slots[threadIdx.x] = s;
     for (int h = kThreads / 2; h > 0; h >>= 1) {
         __syncthreads();
