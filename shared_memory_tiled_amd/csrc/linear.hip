@@ -185,6 +185,7 @@ struct Plan {
     // split), rest_tile for the others
     int tile, rows, rest_tile;
     int splits;                               // kRows: blocks along K
+    bool fused;                               // kRows: the fused kernel
     int k_share;                              // kTiles on 64 tiles: K per block, if below K
     bool pack_a, pack_b;                      // factors copied into the workspace
     int K;                                    // as the product runs it (padded if packed)
@@ -317,6 +318,8 @@ Plan make_plan(const Gemm16Args& p, const EpilogueArgs& e, int op_a, int op_b) {
         q.K = p.K;
         q.pack_a = q.pack_b = false;
         q.splits = linear_rows_splits(p.M, p.N, p.K);
+        q.fused = q.splits > 1 && !e.gradient && linear_rows_fused(p.M, p.N, p.K, op_b);
+        if (q.fused) q.splits = 1;
         if (q.splits > 1 || e.gradient) q.main_bytes = align256(4 * (int64_t)q.splits * p.M * p.N);
         q.part_rows = e.bias_grad ? 1 : 0;
         return q;
@@ -430,6 +433,7 @@ hipError_t launch_linear(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t
     float* const partials = reinterpret_cast<float*>(ws + q.a_bytes + q.b_bytes + q.main_bytes);
     hipError_t err;
     if (q.kind == kRows) {
+        if (q.fused) return launch_linear_rows_fused(p, e, s, format, op_b);
         const bool planes = q.splits > 1 || e.gradient;
         err = launch_linear_rows(p, e, s, format, op_b, q.splits, planes ? main : nullptr);
         if (err != hipSuccess || !planes) return err;

@@ -37,5 +37,9 @@ constexpr int kLinearRowsMax = 64;
 int linear_rows_splits(int M, int N, int K);
 hipError_t launch_linear_rows(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_b,
                               int splits, float* planes);
+// Whether narrower blocks that take all of K and end in the epilogue (forward
+// mode) are faster than K split over blocks, and their launcher.
+bool linear_rows_fused(int M, int N, int K, int op_b);
+hipError_t launch_linear_rows_fused(const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_b);
 
 }  // namespace gemmf32

@@ -324,3 +324,14 @@ def test_derivative_far_from_zero(kind, dtype):
     D = dY.double() * R.act_derivative(z.double(), kind)
     dz, _ = binding.activation_backward(dY, z, kind)
     R.within(dz, D, R.HALF[dtype] * D.abs() + R.TINY[dtype] + 32 * R.U * dY.double().abs(), kind)
+
+
+@pytest.mark.parametrize("N,K", [(31, 256), (33, 600), (64, 2048), (1000, 1001), (2047, 513), (4097, 2048), (8192, 264),
+                                 (4100, 2100)], ids=str)
+@pytest.mark.parametrize("M", [1, 7, 16, 17, 32])
+def test_few_rows_whole_depth(M, N, K):
+    """Few rows whose blocks take all of K: ragged widths and depths, both
+    storages, rows with a leading dimension, NaN beside them."""
+    check_forward(M, N, K, torch.bfloat16, "silu", op_b="N")
+    check_forward(M, N, K, torch.float16, "gelu", op_b="T", strides=True)
+    check_forward(M, N, K, torch.bfloat16, "none", op_b="N", strides=True, out_dtype=torch.float32, preact=False)
