@@ -640,8 +640,8 @@ def linear(X, W, bias=None, activation="none", residual=None, out=None, out_dtyp
     W, in one product kernel with the rest in its epilogue.
 
     ``op_b="T"``: W is stored N x K.  ``out`` (or ``out_dtype``) has the
-    factors' dtype (default) or float32; ``residual`` has out's dtype and may
-    be ``out``; ``bias`` has the factors' dtype or float32.  With
+    factors' dtype (default) or float32 and overlaps neither of them;
+    ``residual`` has out's dtype and may be ``out``; ``bias`` has the factors' dtype or float32.  With
     ``return_preact`` returns (out, Z), Z = op_a(X) @ op_b(W) + bias in the
     factors' dtype, for the backward pass."""
     device = _device_of(X, W, bias, residual, out)
@@ -676,7 +676,8 @@ def linear_grad(dZ, W, preact=None, activation="none", residual=None, out=None, 
     With the defaults dZ is M x N and W the K x N weight of
     ``linear(X, W)``, the result M x K; ``preact`` is what
     ``linear(..., return_preact=True)`` of the layer before returned,
-    ``residual`` a gradient that arrives past this layer (out's dtype).  With
+    ``residual`` a gradient that arrives past this layer (out's dtype; may be
+    ``out``, which overlaps no other argument).  With
     ``return_bias_grad`` returns (out, column sums in float32): the bias
     gradient of the layer before."""
     device = _device_of(dZ, W, preact, residual, out)
