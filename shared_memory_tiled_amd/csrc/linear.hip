@@ -129,11 +129,15 @@ void column_sum_kernel(int count, int n, const float* partials, float* out) {
 }
 
 // Rows per block of the pass: enough blocks for the device's 256 CUs (eight
-// each), then as many rows as that leaves, for fewer partial sums.
+// each), then as many rows as that leaves, for fewer partial sums; a multiple
+// of 8 between 8 and M, or the one above M (below 2^31: the largest M, 2^31 - 1,
+// gives 2^31 - 8 and a second block of rows).
 int pass_rows(int M, int N) {
     const int64_t cols = ceil_div(N, kPassCols);
     const int64_t rows = ((int64_t)M * cols + 2047) / 2048;
-    return 8 * (int)((rows + 7) / 8 > 0 ? (rows + 7) / 8 : 1);
+    const int64_t most = ((int64_t)M + 7) / 8 < INT_MAX / 8 ? ((int64_t)M + 7) / 8 : INT_MAX / 8;
+    const int64_t eights = (rows + 7) / 8;
+    return 8 * (int)(eights < 1 ? 1 : eights < most ? eights : most);
 }
 
 int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }

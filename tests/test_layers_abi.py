@@ -201,3 +201,15 @@ def test_activation_grad_column_limit(lib):
     args = (0, 0, 1, n, FAKE, n, None, 0, None, 0, FAKE)
     assert lib.activation_grad_workspace_size(1, n) == -1
     assert lib.activation_grad(*args, FAKE, BIG, None) == CODES["GEMM_F32_ERR_TOO_LARGE"]
+
+
+@pytest.mark.parametrize("M,N", [(2 ** 30, 2 ** 20), (2 ** 31 - 1, 2 ** 20), (2 ** 31 - 1, 2 ** 19), (2 ** 31 - 1, 2 ** 18),
+                                 (2 ** 31 - 1, 2 ** 31 - 128), (1, 2 ** 31 - 128), (2 ** 31 - 1, 1), (1, 1), (9, 2 ** 31 - 128)])
+def test_activation_grad_size_of_any_matrix(lib, M, N):
+    """One partial row of N binary32 sums per block of rows; at most 2048
+    blocks (and one more for the rest), at most one per 8 rows, and no fewer
+    than one."""
+    need = lib.activation_grad_workspace_size(M, N)
+    assert 4 * N <= need <= 4 * N * min(2049, -(-M // 8)) + 256
+    args = (0, 0, M, N, FAKE, N, None, 0, None, 0, FAKE)
+    assert lib.activation_grad(*args, FAKE, need - 1, None) == CODES["GEMM_F32_ERR_WORKSPACE"]
