@@ -583,6 +583,9 @@ int layer_norm_backward(int type, int64_t rows, int64_t cols, const void *dy, in
  *   X <- a X + X (b S + c S^2) with S = X^T X          (rows > cols)
  * so that every singular value s of X goes to a s + b s^3 + c s^5.
  *   type        of G and out: GEMM_MIXED_BF16, _F16 or _F32
+ *   batch       at most 65535
+ *   rows, cols  4 (rows + 256) (cols + 256) below 2^31, each first rounded up
+ *               to a multiple of 64 (22848 x 22848, 16384 x 32000)
  *   G           matrix z's element (r, c) at G[z*stride_g + r*ldg + c], ldg >=
  *               cols, stride_g >= 0
  *   out         likewise with ldo, stride_o; matrices must not overlap

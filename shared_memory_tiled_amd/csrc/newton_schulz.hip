@@ -217,10 +217,12 @@ bool newton_schulz_bounds(int steps, double a, double b, double c, double* bound
 }
 
 int64_t newton_schulz_workspace(const NewtonSchulzArgs& a) {
-    // both planes of a matrix, with a tile's overhang, within 2^31 bytes
-    const Layout l = layout(a);
-    if (4 * ((int64_t)l.rp + 256) * (l.cp + 256) >= (1ll << 31) || a.batch > 65535) return -1;
-    return l.bytes;
+    // both planes of a matrix, padded to 64 and with a tile's overhang, within
+    // 2^31 bytes; refused before anything is padded in 32 bits
+    auto span = [](int n) { return ((int64_t)n + 63) / 64 * 64 + 256; };
+    const int64_t rows = span(a.rows), cols = span(a.cols);      // below 2^32
+    if (rows > ((1ll << 29) - 1) / cols || a.batch > 65535) return -1;   // 4 rows cols >= 2^31
+    return layout(a).bytes;
 }
 
 hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, void* workspace, hipStream_t s) {

@@ -213,3 +213,23 @@ def test_activation_grad_size_of_any_matrix(lib, M, N):
     assert 4 * N <= need <= 4 * N * min(2049, -(-M // 8)) + 256
     args = (0, 0, M, N, FAKE, N, None, 0, None, 0, FAKE)
     assert lib.activation_grad(*args, FAKE, need - 1, None) == CODES["GEMM_F32_ERR_WORKSPACE"]
+
+
+@pytest.mark.parametrize("rows,cols", [(2 ** 31 - 1, 1), (1, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 64, 2),
+                                       (3 * 2 ** 29, 3 * 2 ** 29), (2 ** 30, 2 ** 30), (2 ** 16, 2 ** 16), (2 ** 23, 1)])
+@pytest.mark.parametrize("batch", [1, 3])
+def test_newton_schulz_matrices_past_the_limit(lib, batch, rows, cols):
+    """Both planes of a matrix, padded to 64 and with 256 more rows and
+    columns, have to stay below 2^31 bytes."""
+    assert lib.newton_schulz_workspace_size(0, batch, rows, cols) == -1
+    code = schulz(lib, batch=batch, rows=rows, cols=cols, ldg=cols, ldo=cols, sg=0, so=rows * cols)
+    assert code == CODES["GEMM_F32_ERR_TOO_LARGE"]
+
+
+def test_newton_schulz_matrices_up_to_the_limit(lib):
+    for rows, cols in ((16384, 16384), (64, 2 ** 20), (1, 2 ** 20), (22848, 22848)):
+        padded = -(-rows // 64) * 64 + 256, -(-cols // 64) * 64 + 256
+        assert 4 * padded[0] * padded[1] < 2 ** 31
+        assert lib.newton_schulz_workspace_size(2, 1, rows, cols) > 8 * rows * cols
+    assert lib.newton_schulz_workspace_size(2, 65535, 64, 64) > 0
+    assert lib.newton_schulz_workspace_size(2, 65536, 64, 64) == -1
