@@ -14,10 +14,18 @@
 // (three) reads and one write.  A row stays in registers between its passes:
 // `THREADS` threads hold it in CH chunks of 16 bytes each, a wave, a block of
 // 256 or one of 1024 by its length, and the parameters stay in registers from
-// row to row (blocks walk the rows).  The variance is taken from the
-// deviations, a second reduction, for rows whose mean is far from zero.  Rows
-// longer than a block's registers go through the kernels at the end, which
-// read them again.
+// row to row (blocks walk the rows).  Rows longer than a block's registers go
+// through the kernels at the end, which read them again.
+//
+// The binary32 sum of a row rounds, so its mean m is off by a few units of the
+// row's size, even where all values are equal: up to 2.5e-7 of 4096 of them,
+// which a row constant at 1000 would turn into 0.08 at rstd = 316.  A second
+// reduction therefore takes the deviations d = x - m, which are exact where the
+// row is near its mean, both squared and as they are: delta = <d> is what m
+// lacks, the deviations become d - delta, the mean m + delta, and
+// <(d - delta)^2> = <d^2> - delta^2.  Where delta^2 is more than 2^-6 of <d^2>
+// (rows as good as constant) that difference cancels, and the squares are
+// taken again.
 #include "epilogue.h"
 
 namespace gemmf32 {
@@ -46,6 +54,36 @@ __device__ __forceinline__ float group_total(float v, float* slots) {
         for (int i = 1; i < THREADS / 64; ++i) v += slots[i];
     }
     return v;
+}
+
+// Two sums at once, with one pair of barriers; slots: two floats per wave.
+template <int THREADS>
+__device__ __forceinline__ void group_totals(float& v, float& w, float* slots) {
+    v = wave_total(v);
+    w = wave_total(w);
+    if constexpr (THREADS > 64) {
+        __syncthreads();                                  // the slots' last readers are done
+        if ((threadIdx.x & 63) == 0) {
+            slots[2 * (threadIdx.x >> 6)] = v;
+            slots[2 * (threadIdx.x >> 6) + 1] = w;
+        }
+        __syncthreads();
+        v = slots[0];
+        w = slots[1];
+#pragma unroll
+        for (int i = 1; i < THREADS / 64; ++i) {
+            v += slots[2 * i];
+            w += slots[2 * i + 1];
+        }
+    }
+}
+// Whether the squares' mean has to be taken again about the corrected mean
+// (the same in every thread of a row; false for NaN).
+__device__ __forceinline__ bool near_constant(float delta, float square) { return delta * delta > 0.015625f * square; }
+
+// The corrected mean; m itself for rows with infinities.
+__device__ __forceinline__ float corrected(float m, float delta) {
+    return __builtin_fabsf(delta) < __builtin_inff() ? m + delta : m;
 }
 
 // A 16-byte chunk that exists in whole, as loaded, and its values.
@@ -102,7 +140,7 @@ template <int TYPE, int THREADS, int CH, int FIT>
 __global__ __launch_bounds__(THREADS == 1024 ? 1024 : 256)
 void layer_norm_kernel(LayerNormArgs a) {
     constexpr int V = kChunk<TYPE>, BLOCK = THREADS == 1024 ? 1024 : 256, GROUPS = BLOCK / THREADS;
-    __shared__ float slots[BLOCK / 64];
+    __shared__ float slots[2 * (BLOCK / 64)];
     const int t = threadIdx.x % THREADS, g = threadIdx.x / THREADS;
     float gamma[CH][V], beta[CH][V];
     load_params<TYPE>(a, a.gamma, 1.0f, t, THREADS, gamma);
@@ -141,23 +179,44 @@ void layer_norm_kernel(LayerNormArgs a) {
         for (int k = 0; k < CH; ++k)
 #pragma unroll
             for (int e = 0; e < V; ++e) s += v[k][e];
-        const float mean = group_total<THREADS>(s, slots) / (float)a.cols;   // exact for a constant row
-        s = 0.0f;
+        const float m = group_total<THREADS>(s, slots) / (float)a.cols;
+        auto inside = [&](int k, int e) __attribute__((always_inline)) {
+            return FIT == kWhole || V * (t + k * THREADS) + e < a.cols;
+        };
+        float delta = 0.0f, square = 0.0f;
 #pragma unroll
         for (int k = 0; k < CH; ++k)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float d = FIT == kWhole || V * (t + k * THREADS) + e < a.cols ? v[k][e] - mean : 0.0f;
+                const float d = inside(k, e) ? v[k][e] - m : 0.0f;
                 v[k][e] = d;
-                s = __builtin_fmaf(d, d, s);
+                delta += d;
+                square = __builtin_fmaf(d, d, square);
             }
-        const float rstd = 1.0f / sqrtf(__builtin_fmaf(group_total<THREADS>(s, slots), inv, a.eps));
+        group_totals<THREADS>(delta, square, slots);
+        delta *= inv;
+        square *= inv;
+        float var = __builtin_fmaf(-delta, delta, square);
+        if (near_constant(delta, square)) {
+            s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float d = inside(k, e) ? v[k][e] - delta : 0.0f;
+                    s = __builtin_fmaf(d, d, s);
+                }
+            var = group_total<THREADS>(s, slots) * inv;
+        }
+        const float mean = corrected(m, delta), rstd = 1.0f / sqrtf(var + a.eps);
+        const float shift = -delta * rstd;
         char* const y = const_cast<char*>(row_of<TYPE>(a.y, row, a.ldy));
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const int c = V * (t + k * THREADS);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[k][e] = __builtin_fmaf(v[k][e] * rstd, gamma[k][e], beta[k][e]);
+            for (int e = 0; e < V; ++e)
+                v[k][e] = __builtin_fmaf(__builtin_fmaf(v[k][e], rstd, shift), gamma[k][e], beta[k][e]);
             if (FIT == kWhole || c < a.cols) store_values<TYPE>(y, c, FIT != kRagged ? V : a.cols - c, v[k]);
         }
         if (t == 0) {
@@ -355,7 +414,7 @@ template <int TYPE>
 __global__ __launch_bounds__(kThreads)
 void layer_norm_long_kernel(LayerNormArgs a) {
     constexpr int V = kChunk<TYPE>;
-    __shared__ float slots[4];
+    __shared__ float slots[8];
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const char* const x = row_of<TYPE>(a.x, row, a.ldx);
         char* const y = const_cast<char*>(row_of<TYPE>(a.y, row, a.ldy));
@@ -366,18 +425,33 @@ void layer_norm_long_kernel(LayerNormArgs a) {
 #pragma unroll
             for (int e = 0; e < V; ++e) s += v[e];
         }
-        const float mean = group_total<kThreads>(s, slots) / (float)a.cols;
-        s = 0.0f;
-        for (int64_t c = V * threadIdx.x; c < a.cols; c += V * kThreads) {
-            float v[V];
-            load_chunk<TYPE>(x, (int)c, a.cols, v);
+        const float m = group_total<kThreads>(s, slots) / (float)a.cols;
+        // the sums of x - m - shift and of its square
+        auto deviations = [&](float shift, float& sum, float& square) __attribute__((always_inline)) {
+            sum = square = 0.0f;
+            for (int64_t c = V * threadIdx.x; c < a.cols; c += V * kThreads) {
+                float v[V];
+                load_chunk<TYPE>(x, (int)c, a.cols, v);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = c + e < a.cols ? v[e] - mean : 0.0f;
-                s = __builtin_fmaf(d, d, s);
+                for (int e = 0; e < V; ++e) {
+                    const float d = c + e < a.cols ? v[e] - m - shift : 0.0f;
+                    sum += d;
+                    square = __builtin_fmaf(d, d, square);
+                }
             }
+            group_totals<kThreads>(sum, square, slots);
+        };
+        float delta, square;
+        deviations(0.0f, delta, square);
+        delta /= (float)a.cols;
+        square /= (float)a.cols;
+        float var = __builtin_fmaf(-delta, delta, square);
+        if (near_constant(delta, square)) {
+            float left;
+            deviations(delta, left, square);
+            var = square / (float)a.cols;
         }
-        const float rstd = 1.0f / sqrtf(group_total<kThreads>(s, slots) / (float)a.cols + a.eps);
+        const float mean = corrected(m, delta), rstd = 1.0f / sqrtf(var + a.eps);
         for (int64_t c = V * threadIdx.x; c < a.cols; c += V * kThreads) {
             float v[V], g[V], b[V];
             load_chunk<TYPE>(x, (int)c, a.cols, v);
@@ -390,7 +464,7 @@ void layer_norm_long_kernel(LayerNormArgs a) {
             if (a.gamma) load_values(a.param_type, a.gamma, c, valid, g);
             if (a.beta) load_values(a.param_type, a.beta, c, valid, b);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf((v[e] - mean) * rstd, g[e], b[e]);
+            for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf((v[e] - m - delta) * rstd, g[e], b[e]);
             store_values<TYPE>(y, c, valid, v);
         }
         if (threadIdx.x == 0) {

@@ -211,3 +211,54 @@ def test_graph_replay():
             eager = both()
             torch.cuda.synchronize()
             assert all(torch.equal(a, e) for a, e in zip(kept, eager)), (M, N, seed)
+
+
+def near_mean_tols(x, y, rstd, xhat, dtype):
+    """For rows close to their mean: the first sum misses it by at most depth
+    roundings of |x|, the deviations from that are exact (a subtraction of
+    values within a factor of two), and their mean corrects the first one to
+    depth roundings of the deviations."""
+    N = x.shape[1]
+    depth = N / 64 + 20
+    xd = x.double()
+    mean = xd.mean(1)
+    first = depth * R.U * xd.abs().mean(1)
+    left = depth * R.U * ((xd - mean[:, None]).abs().mean(1) + first)
+    # relative error of the variance plus eps: sums and squares, and the shift that is left
+    e_rel = (depth + 8) * R.U + (left * rstd) ** 2
+    e_y = R.HALF[dtype] * y.abs() + xhat.abs() * (e_rel[:, None] + 6 * R.U) + (left * rstd)[:, None] * (1 + 4 * R.U)
+    return left + R.U * mean.abs(), rstd * (e_rel + 3 * R.U), e_y
+
+
+@pytest.mark.parametrize("N", [1, 3, 64, 1000, 1001, 4096, 4100, 8192, 10000, 16384, 33000, 70001])
+def test_rows_of_one_value(N):
+    """Every value equal: the mean is that value, y is zero but for what is
+    left of the sums' roundings, though the sums themselves are not exact."""
+    values = torch.tensor([0.1, 1000.3, 12345.678, -3.3e-5, 1.0 / 3.0, -7.7e4], device="cuda")
+    for dt in (torch.float32, torch.float16, torch.bfloat16):
+        c = values[values.abs() < (6e4 if dt == torch.float16 else 1e30)].to(dt)
+        x = c[:, None].repeat(1, N).contiguous()
+        y, mean, rstd = binding.layer_norm(x, eps=EPS)
+        say(f"{N} {dt}: largest |y| {y.abs().max().item():.1e}")
+        # depth roundings of depth roundings of the value, far below its own rounding
+        left = ((N / 64 + 20) * R.U) ** 2 * c.double().abs()
+        assert torch.equal(mean, c.float())
+        R.within(y, torch.zeros_like(y), left[:, None] * EPS ** -0.5 * 1.01 + 1e-30, "y")
+        R.within(rstd, torch.full_like(rstd, EPS ** -0.5), EPS ** -0.5 * (left ** 2 / EPS + 4 * R.U), "rstd")
+
+
+@pytest.mark.parametrize("shift,scale", [(1e5, 1.0), (3e4, 0.05), (-7e6, 3.0), (100.0, 1e-4)])
+@pytest.mark.parametrize("N", [100, 1001, 4096, 8192, 16384, 33000])
+def test_rows_near_their_mean(N, shift, scale):
+    """Means up to 10^6 deviations away, deviations down to a few units of the
+    last place: y keeps the accuracy of the deviations."""
+    x = make(N, 5, N, torch.float32, shift, scale)
+    x[1] = shift
+    x[1, N // 2] = torch.nextafter(x[1, N // 2], torch.tensor(float("inf"), device="cuda"))
+    for eps in (1e-5, 1e-12):
+        y, mean, rstd = binding.layer_norm(x, eps=eps)
+        ry, rmean, rrstd, xhat = R.layer_norm_ref(x, None, None, float(torch.tensor(eps)))
+        tm, tr, ty = near_mean_tols(x, ry, rrstd, xhat, torch.float32)
+        R.within(mean, rmean, tm, "mean")
+        R.within(rstd, rrstd, tr, "rstd")
+        R.within(y, ry, ty, "y")
