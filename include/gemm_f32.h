@@ -470,7 +470,9 @@ int gemm_mixed_op(int op_a, int op_b, int format, int64_t M, int64_t N, int64_t 
  * binary32. */
 #define GEMM_MIXED_F32 2
 
-/* Activations. */
+/* Activations.  At infinities each takes its limit, -0 or +0 and +inf, and so
+ * does its derivative, 0 and 1: a kept pre-activation past binary16's range is
+ * infinite.  NaN stays NaN. */
 #define GEMM_ACT_NONE      0
 #define GEMM_ACT_RELU      1  /* max(z, 0), NaN stays NaN; derivative 0 at 0            */
 #define GEMM_ACT_GELU      2  /* z Phi(z), Phi the normal distribution function         */

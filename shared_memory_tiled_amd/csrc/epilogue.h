@@ -110,7 +110,10 @@ __device__ __forceinline__ float normal_cdf(float z, float* density) {
     return z > 0.0f ? 1.0f - tail : tail;
 }
 
-// Activations (GEMM_ACT_*) and their derivatives.  NaN stays NaN.
+// Activations (GEMM_ACT_*) and their derivatives.  NaN stays NaN; infinities
+// give the limits (0 and +inf, derivatives 0 and 1): a pre-activation past
+// binary16's range is kept as one.  So the factor z, which would meet a zero
+// there, is held at a finite value where the other factor is zero already.
 //   gelu_tanh: (1 + tanh u) / 2 = 1 / (1 + e^(-2 u)), u = c (z + 0.044715 z^3),
 //   c = sqrt(2 / pi).
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
@@ -118,16 +121,17 @@ constexpr float kTanhC = 0.79788456080286536f, kTanhCubic = 0.044715f;
 
 template <int ACT>
 __device__ __forceinline__ float activate_one(float z) {
+    const float finite = __builtin_fmaxf(z, -3.4028234663852886e38f);   // NaN is in the other factor
     if constexpr (ACT == kActRelu) return z <= 0.0f ? 0.0f : z;
     if constexpr (ACT == kActGelu) {
         float g;
-        return z * normal_cdf(z, &g);
+        return finite * normal_cdf(z, &g);
     }
     if constexpr (ACT == kActGeluTanh) {
         const float u2 = -2.0f * kTanhC * z * __builtin_fmaf(kTanhCubic * z, z, 1.0f);
-        return z * fast_rcp(1.0f + fast_exp(u2));
+        return finite * fast_rcp(1.0f + fast_exp(u2));
     }
-    if constexpr (ACT == kActSilu) return z * fast_rcp(1.0f + fast_exp(-z));
+    if constexpr (ACT == kActSilu) return finite * fast_rcp(1.0f + fast_exp(-z));
     return z;
 }
 
@@ -137,21 +141,22 @@ __device__ __forceinline__ float activate_derivative_one(float z) {
     if constexpr (ACT == kActGelu) {
         float g;
         const float cdf = normal_cdf(z, &g);
-        return __builtin_fmaf(z * 0.39894228040143268f, g, cdf);
+        const float near = __builtin_fabsf(z) > 30.0f ? 30.0f : z;      // g is 0 past 30
+        return __builtin_fmaf(near * 0.39894228040143268f, g, cdf);
     }
     if constexpr (ACT == kActGeluTanh) {
         const float u2 = -2.0f * kTanhC * z * __builtin_fmaf(kTanhCubic * z, z, 1.0f);
         const float s = fast_rcp(1.0f + fast_exp(u2));
         // d u2 / dz = -2 c (1 + 3 0.044715 z^2); s' = -s (1 - s) du2.  Past 30, s
-        // is 0 or 1 and s (1 - s) is 0: z^2 is held there, so that it meets no
-        // infinity.
-        const float far = __builtin_fabsf(z) > 30.0f ? 30.0f : z;
-        const float du = 2.0f * kTanhC * __builtin_fmaf(3.0f * kTanhCubic * far, far, 1.0f);
-        return __builtin_fmaf(z, du * (s * (1.0f - s)), s);
+        // is 0 or 1 and s (1 - s) is 0.
+        const float near = __builtin_fabsf(z) > 30.0f ? 30.0f : z;
+        const float du = 2.0f * kTanhC * __builtin_fmaf(3.0f * kTanhCubic * near, near, 1.0f);
+        return __builtin_fmaf(near, du * (s * (1.0f - s)), s);
     }
     if constexpr (ACT == kActSilu) {
         const float s = fast_rcp(1.0f + fast_exp(-z));
-        return __builtin_fmaf(z, s * (1.0f - s), s);
+        const float near = __builtin_fabsf(z) > 100.0f ? 100.0f : z;    // s is 0 or 1 past 100
+        return __builtin_fmaf(near, s * (1.0f - s), s);
     }
     return 1.0f;
 }

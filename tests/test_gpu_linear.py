@@ -335,3 +335,57 @@ def test_few_rows_whole_depth(M, N, K):
     check_forward(M, N, K, torch.bfloat16, "silu", op_b="N")
     check_forward(M, N, K, torch.float16, "gelu", op_b="T", strides=True)
     check_forward(M, N, K, torch.bfloat16, "none", op_b="N", strides=True, out_dtype=torch.float32, preact=False)
+
+
+@pytest.mark.parametrize("kind", R.ACTS)
+def test_infinite_preactivations(kind):
+    """Infinities take the limits: activation 0 and +inf, derivative 0 and 1
+    (without one the product's entry itself); NaN stays NaN.  A binary16
+    pre-activation past 65504 is such an infinity."""
+    inf, nan = float("inf"), float("nan")
+    one_sided = kind != "none"
+    z = torch.tensor([inf, -inf, 2.0, inf, nan, -inf, 0.5, -1.0], device="cuda")
+    # forward: the bias is the whole pre-activation; few rows, and tiles of every size
+    for M, N, K in ((3, 8, 16), (70, 200, 32), (1000, 1100, 2056), (2900, 2952, 130)):
+        say(f"{kind} forward {M} {N} {K}")
+        b = z.repeat(-(-N // 8))[:N].contiguous()
+        X, W = torch.zeros(M, K, dtype=torch.float16, device="cuda"), torch.zeros(K, N, dtype=torch.float16, device="cuda")
+        y, kept = binding.linear(X, W, bias=b, activation=kind, out_dtype=torch.float32, return_preact=True)
+        want = torch.where(b == -inf, torch.zeros_like(b) if one_sided else b, b)
+        special = ~b.isfinite()
+        for rows in (y[0], y[-1]):
+            assert torch.equal(torch.nan_to_num(rows[special], nan=7.0, posinf=8.0, neginf=9.0),
+                               torch.nan_to_num(want[special], nan=7.0, posinf=8.0, neginf=9.0))
+            assert bool(rows[~special].isfinite().all())
+        assert torch.equal(kept[0].isnan(), b.isnan()) and torch.equal(kept[0].abs() == inf, b.abs() == inf)
+    for dtype in (torch.bfloat16, torch.float16):
+        D = {-inf: 0.0 if one_sided else 1.0, inf: 1.0}
+        for M, N, K in ((3, 40, 64), (70, 200, 72), (1000, 1096, 2056), (2900, 2952, 130)):
+            say(f"{kind} gradient {M} {N} {K} {dtype}")
+            zz = normal(5, M, N, dtype=dtype)
+            zz[:, 3], zz[:, N - 1], zz[M - 1, 7], zz[M - 1, 8] = inf, -inf, inf, nan
+            dY, W = normal(6, M, K, dtype=dtype), normal(7, N, K, dtype=dtype, scale=K ** -0.5)
+            plain = binding.linear_grad(dY, W)                               # no activation
+            d, sums = binding.linear_grad(dY, W, preact=zz, activation=kind, return_bias_grad=True)
+            e, _ = binding.activation_backward(plain, zz, kind)
+            for got in (d, e):
+                for mask, factor in ((zz == inf, D[inf]), (zz == -inf, D[-inf])):
+                    assert torch.equal(got[mask], plain[mask] * factor)
+                assert torch.equal(got.isnan(), zz.isnan() if one_sided else torch.zeros_like(zz, dtype=torch.bool))
+            assert torch.equal(sums.isnan(), d.isnan().any(0))
+
+
+def test_preactivation_past_binary16():
+    """Z near 10^5 keeps a finite binary32 result, an infinite binary16 Z and
+    the gradient of the identity or of zero."""
+    X = torch.full((33, 64), 40.0, dtype=torch.float16, device="cuda")
+    W = torch.full((64, 72), 40.0, dtype=torch.float16, device="cuda")
+    W[:, 1::2] = -40.0
+    for kind in R.ACTS[1:]:
+        y, z = binding.linear(X, W, activation=kind, out_dtype=torch.float32, return_preact=True)
+        assert bool((y[:, ::2] == 102400.0).all()) and bool((y[:, 1::2] == 0).all()) and bool(z.isinf().all())
+        dY = normal(1, 33, 72, dtype=torch.float16)
+        dX, dW, db = binding.linear_backward(dY, X, W, preact=z, activation=kind)
+        dZ, _ = binding.activation_backward(dY, z, kind)
+        assert torch.equal(dZ[:, ::2], dY[:, ::2]) and bool((dZ[:, 1::2] == 0).all())
+        assert bool(dX.isfinite().all()) and bool(dW.isfinite().all()) and bool(db.isfinite().all())
