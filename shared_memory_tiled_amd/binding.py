@@ -569,9 +569,9 @@ def _workspace(like: torch.Tensor, nbytes: int):
 
 
 def _row_major(t: torch.Tensor, what: str) -> int:
-    """Leading dimension of a 2-D row-major tensor."""
-    rows, cols = t.shape
-    s0, s1 = t.stride()
+    """Leading dimension of a row-major matrix, or of each of a batch of them."""
+    rows, cols = t.shape[-2:]
+    s0, s1 = t.stride()[-2:]
     if cols > 1 and s1 != 1:
         raise ValueError(f"{what} must be row-major (unit column stride)")
     if rows <= 1:
@@ -864,7 +864,7 @@ def newton_schulz(G, steps=5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7,
     rows, cols = G.shape[-2:]
 
     def strides(m, what):
-        ld = _row_major(m if m.dim() == 2 else m.as_strided(m.shape[1:], m.stride()[1:]), what)
+        ld = _row_major(m, what)
         return ld, (m.stride(0) if m.dim() == 3 and batch > 1 else max(rows - 1, 0) * ld + cols)
 
     ldg, stride_g = strides(G, "G")

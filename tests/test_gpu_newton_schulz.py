@@ -156,3 +156,12 @@ def test_streams_and_graph_replay():
         torch.cuda.synchronize()
         assert all(torch.equal(t, eager) for t in a)
         assert math.isfinite(eager.float().sum().item())
+
+
+@pytest.mark.parametrize("shape", [(0, 4, 6), (3, 0, 5), (3, 5, 0), (0, 7), (7, 0), (0, 0, 0)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_no_matrices(shape, dtype):
+    G = torch.empty(shape, dtype=R.DTYPES[dtype], device="cuda")
+    got = binding.newton_schulz(G)
+    assert got.shape == G.shape and got.dtype == G.dtype
+    assert binding.newton_schulz(G, out=G) is G
