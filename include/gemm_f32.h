@@ -518,7 +518,8 @@ typedef struct gemm_epilogue {
  *            it.  Two calls that may overlap need a workspace each.
  * Products and sums are accumulated in binary32 and every stored value is
  * rounded once.  C must not overlap A, B or preact, nor residual unless it
- * is residual.  K == 0 leaves a product of zeros to the epilogue; M == 0
+ * is residual (the same pointer with another leading dimension is refused with
+ * GEMM_F32_ERR_INVALID_LD, here and below).  K == 0 leaves a product of zeros to the epilogue; M == 0
  * writes +0 to bias_grad; N == 0 is a no-op.  Statuses as for gemm_mixed,
  * with GEMM_F32_ERR_INVALID_TYPE, _ACTIVATION and _EPILOGUE for the
  * epilogue's fields and GEMM_F32_ERR_WORKSPACE.  Enqueue-only on `stream`;
@@ -537,8 +538,8 @@ int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, int64_t N, in
  *   dY          M x N, ld_dy >= max(1, N)
  *   preact      Z, M x N, ld_preact >= max(1, N); may be NULL if the
  *               activation is GEMM_ACT_NONE
- *   dZ          M x N, ld_dz >= max(1, N), may be dY itself, or NULL for the
- *               sums alone
+ *   dZ          M x N, ld_dz >= max(1, N), may be dY itself (same pointer and
+ *               leading dimension), or NULL for the sums alone
  *   bias_grad   N binary32 sums (of dZ before its rounding, in a fixed
  *               order), or NULL; needs the workspace
  * Rules as for gemm_mixed_epilogue. */
@@ -551,7 +552,8 @@ int activation_grad(int activation, int format, int64_t M, int64_t N, const uint
  *   mean = <x>, rstd = 1 / sqrt(<(x - mean)^2> + eps), <.> over a row
  *   y = (x - mean) rstd gamma + beta
  *   type         of x and y: GEMM_MIXED_BF16, _F16 or _F32
- *   x, y         element (r, c) at x[r*ldx + c], ldx >= cols; y may be x
+ *   x, y         element (r, c) at x[r*ldx + c], ldx >= cols; y may be x with
+ *                the same leading dimension
  *   gamma, beta  cols values of param_type (any of the three), or NULL (1, 0)
  *   eps          >= 0, finite
  *   mean, rstd   rows binary32 values for the backward pass, or NULL
@@ -565,7 +567,7 @@ int layer_norm(int type, int64_t rows, int64_t cols, const void *x, int64_t ldx,
  *   dx     = rstd (g - <g> - xhat <g xhat>) + residual_grad
  *   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
  *   dy, x, dx      of type, with leading dimensions >= cols; dx may be dy or
- *                  residual_grad
+ *                  residual_grad, with the same leading dimension
  *   mean, rstd     as the forward pass wrote them
  *   gamma          cols values of param_type, or NULL (1)
  *   residual_grad  the gradient that reaches x past the layer, of type, or NULL

@@ -21,6 +21,12 @@ int64_t at_least_one(int64_t n) { return n > 1 ? n : 1; }
 // work-items.
 constexpr int64_t kMaxPassCols = INT_MAX - 127;
 
+// An output in place of an input: the same pointer is the same matrix only
+// with the same leading dimension (or one row).
+bool other_matrix(const void* out, int64_t ldo, const void* in, int64_t ldi, int64_t rows) {
+    return out == in && ldo != ldi && rows > 1;
+}
+
 int check_device() {
     int dev = -1;
     return hipGetDevice(&dev) == hipSuccess && dev >= 0 ? GEMM_F32_OK : GEMM_F32_ERR_DEVICE;
@@ -130,6 +136,7 @@ extern "C" int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, in
     }
     if (C == nullptr) return GEMM_F32_ERR_NULL_PTR;
     if (misaligned_type(C, epilogue->c_type)) return GEMM_F32_ERR_MISALIGNED;
+    if (other_matrix(C, ldc, epilogue->residual, epilogue->ld_residual, M)) return GEMM_F32_ERR_INVALID_LD;
     const Gemm16Args p{(int)M, (int)N, (int)K, A, lda, B, ldb, nullptr, ldc};
     const EpilogueArgs e = epilogue_args(format, M, N, C, ldc, epilogue);
     st = check_workspace(linear_workspace(p, e, op_a, op_b), workspace, workspace_bytes);
@@ -168,6 +175,7 @@ extern "C" int activation_grad(int activation, int format, int64_t M, int64_t N,
     if (!extent_fits(M, N, ld_dy) || (dZ != nullptr && !extent_fits(M, N, ld_dz)) ||
         (reads_z && !extent_fits(M, N, ld_preact)))
         return GEMM_F32_ERR_TOO_LARGE;
+    if (other_matrix(dZ, ld_dz, dY, ld_dy, M)) return GEMM_F32_ERR_INVALID_LD;
     if (dZ == nullptr && bias_grad == nullptr) return GEMM_F32_OK;        // nothing to write
     st = check_workspace(bias_grad != nullptr ? epilogue_pass_workspace((int)M, (int)N) : 0, workspace, workspace_bytes);
     if (st != GEMM_F32_OK) return st;
@@ -213,6 +221,7 @@ extern "C" int layer_norm(int type, int64_t rows, int64_t cols, const void* x, i
         return GEMM_F32_ERR_MISALIGNED;
     if (rows > INT_MAX || cols > INT_MAX || !extent_fits(rows, cols, ldx) || !extent_fits(rows, cols, ldy))
         return GEMM_F32_ERR_TOO_LARGE;
+    if (other_matrix(y, ldy, x, ldx, rows)) return GEMM_F32_ERR_INVALID_LD;
     if ((st = check_device()) != GEMM_F32_OK) return st;
     LayerNormArgs a{};
     a.rows = rows;
@@ -264,6 +273,8 @@ extern "C" int layer_norm_backward(int type, int64_t rows, int64_t cols, const v
     if (!extent_fits(rows, cols, lddy) || !extent_fits(rows, cols, ldx) || !extent_fits(rows, cols, lddx) ||
         (residual_grad != nullptr && !extent_fits(rows, cols, ld_residual)))
         return GEMM_F32_ERR_TOO_LARGE;
+    if (other_matrix(dx, lddx, dy, lddy, rows) || other_matrix(dx, lddx, residual_grad, ld_residual, rows))
+        return GEMM_F32_ERR_INVALID_LD;
     st = check_workspace(layer_norm_backward_workspace(type, rows, (int)cols), workspace, workspace_bytes);
     if (st != GEMM_F32_OK) return st;
     if ((st = check_device()) != GEMM_F32_OK) return st;

@@ -233,3 +233,24 @@ def test_newton_schulz_matrices_up_to_the_limit(lib):
         assert lib.newton_schulz_workspace_size(2, 1, rows, cols) > 8 * rows * cols
     assert lib.newton_schulz_workspace_size(2, 65535, 64, 64) > 0
     assert lib.newton_schulz_workspace_size(2, 65536, 64, 64) == -1
+
+
+def test_in_place_needs_the_same_leading_dimension(lib):
+    """An output at an input's address with another leading dimension is
+    another matrix over the same memory: refused; one row has none."""
+    bad, ws = CODES["GEMM_F32_ERR_INVALID_LD"], CODES["GEMM_F32_ERR_WORKSPACE"]
+    out = FAKE << 4
+    assert call(lib, C=out, ldc=16, residual=out, ld_residual=24) == bad
+    assert call(lib, C=out, ldc=24, residual=out, ld_residual=16, gradient=1) == bad
+    # the next check is the workspace's, which a gradient of few rows needs
+    assert call(lib, C=out, ldc=24, residual=out, ld_residual=24, gradient=1, ws_bytes=0) == ws
+    assert call(lib, C=out, ldc=24, residual=out, ld_residual=16, gradient=1, M=1, ws_bytes=0) == ws
+    grad = (0, 0, 4, 8, out, 8, None, 0, out, 9, FAKE)
+    assert lib.activation_grad(*grad, FAKE, BIG, None) == bad
+    assert lib.activation_grad(*grad[:9], 8, FAKE, FAKE, 0, None) == ws
+    assert norm(lib, x=out, y=out, ldx=8, ldy=9) == bad
+    assert norm(lib, x=out, y=out, ldx=10, ldy=9) == bad
+    assert norm_backward(lib, dy=out, lddy=8, dx=out, lddx=9) == bad
+    assert norm_backward(lib, r=out, ldr=12, dx=out, lddx=9) == bad
+    assert norm_backward(lib, dy=out, lddy=9, dx=out, lddx=9, ws_bytes=0) == ws
+    assert norm_backward(lib, r=out, ldr=12, dx=out, lddx=9, rows=1, ws_bytes=0) == ws
