@@ -573,7 +573,8 @@ int layer_norm(int type, int64_t rows, int64_t cols, const void *x, int64_t ldx,
  *   residual_grad  the gradient that reaches x past the layer, of type, or NULL
  *   dgamma, dbeta  cols binary32 sums, added in a fixed order, or NULL;
  *                  +0 when rows == 0
- *   workspace      as for gemm_mixed_epilogue */
+ *   workspace      as for gemm_mixed_epilogue; none is needed with dgamma and
+ *                  dbeta both NULL */
 int64_t layer_norm_backward_workspace_size(int type, int64_t rows, int64_t cols);   /* bytes; -1 if invalid */
 int layer_norm_backward(int type, int64_t rows, int64_t cols, const void *dy, int64_t lddy, const void *x,
                         int64_t ldx, const float *mean, const float *rstd, int param_type, const void *gamma,

@@ -275,7 +275,8 @@ extern "C" int layer_norm_backward(int type, int64_t rows, int64_t cols, const v
         return GEMM_F32_ERR_TOO_LARGE;
     if (other_matrix(dx, lddx, dy, lddy, rows) || other_matrix(dx, lddx, residual_grad, ld_residual, rows))
         return GEMM_F32_ERR_INVALID_LD;
-    st = check_workspace(layer_norm_backward_workspace(type, rows, (int)cols), workspace, workspace_bytes);
+    const bool sums = dgamma != nullptr || dbeta != nullptr;
+    st = check_workspace(sums ? layer_norm_backward_workspace(type, rows, (int)cols) : 0, workspace, workspace_bytes);
     if (st != GEMM_F32_OK) return st;
     if ((st = check_device()) != GEMM_F32_OK) return st;
     LayerNormArgs a{};

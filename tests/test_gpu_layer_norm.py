@@ -262,3 +262,17 @@ def test_rows_near_their_mean(N, shift, scale):
         R.within(mean, rmean, tm, "mean")
         R.within(rstd, rrstd, tr, "rstd")
         R.within(y, ry, ty, "y")
+
+
+def test_backward_without_parameter_gradients():
+    """dgamma and dbeta NULL: no workspace, the same dx bits."""
+    lib = binding.load_library()
+    for M, N, dt, t in ((5, 100, torch.bfloat16, 0), (300, 4096, torch.float16, 1), (7, 40000, torch.float32, 2)):
+        x, dy = make(1, M, N, dt), make(2, M, N, dt)
+        _, mean, rstd = binding.layer_norm(x)
+        want = binding.layer_norm_backward(dy, x, mean, rstd)[0]
+        dx = torch.empty_like(x)
+        assert lib.layer_norm_backward(t, M, N, dy.data_ptr(), N, x.data_ptr(), N, mean.data_ptr(), rstd.data_ptr(), 2,
+                                       None, None, 0, dx.data_ptr(), N, None, None, None, 0,
+                                       torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(dx, want)

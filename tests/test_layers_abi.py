@@ -254,3 +254,15 @@ def test_in_place_needs_the_same_leading_dimension(lib):
     assert norm_backward(lib, r=out, ldr=12, dx=out, lddx=9) == bad
     assert norm_backward(lib, dy=out, lddy=9, dx=out, lddx=9, ws_bytes=0) == ws
     assert norm_backward(lib, r=out, ldr=12, dx=out, lddx=9, rows=1, ws_bytes=0) == ws
+
+
+def test_layer_norm_backward_needs_no_workspace_without_sums(lib):
+    """Past the workspace's check the call meets the missing device."""
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not memory: only where no kernel can start")
+    bare = dict(dgamma=None, dbeta=None, ws=None, ws_bytes=0)
+    assert norm_backward(lib, **bare) == CODES["GEMM_F32_ERR_DEVICE"]
+    assert norm_backward(lib, **bare, rows=3, cols=40000, lddy=40000, ldx=40000, ldr=40000, lddx=40000) == \
+        CODES["GEMM_F32_ERR_DEVICE"]
+    for one in ("dgamma", "dbeta"):
+        assert norm_backward(lib, **{**bare, one: FAKE}) == CODES["GEMM_F32_ERR_WORKSPACE"]
