@@ -846,8 +846,9 @@ NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 def newton_schulz(G, steps=5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, out=None, stream=None):
     """The matrix G (2-D, or 3-D: a batch of matrices of one shape; bfloat16,
     float16 or float32) orthogonalised by ``steps`` Newton-Schulz steps of the
-    odd polynomial with ``coefficients`` (a, b, c); see gemm_f32.h.  ``out``
-    (G's shape and dtype) may be G."""
+    odd polynomial with ``coefficients`` (a, b, c); see gemm_f32.h.  Accurate
+    relative to the matrix: entries below 2^-39 of its norm count as 0.
+    ``out`` (G's shape and dtype) may be G."""
     device = _device_of(G, out)
     if _elsewhere(stream, device):
         with _placed(stream, device):

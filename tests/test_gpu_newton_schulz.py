@@ -165,3 +165,56 @@ def test_no_matrices(shape, dtype):
     got = binding.newton_schulz(G)
     assert got.shape == G.shape and got.dtype == G.dtype
     assert binding.newton_schulz(G, out=G) is G
+
+
+@pytest.mark.parametrize("shape", [(48, 80), (80, 48), (300, 500), (500, 300), (1000, 600), (600, 1000)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("by_row", [True, False])
+def test_badly_scaled(shape, dtype, by_row):
+    """Rows (columns) scaled over 1 .. 1e-9, judged row by row.
+
+    Relative to its own row an entry has check()'s error.  To that comes what
+    the planes cannot hold: half their last step, 2^-25 over a scale of 2^14, is
+    q = 2^-39 of the norm, in the root mean square 2^-24 / 2^14 / sqrt(12) =
+    2^-39.8.  An entry of X is off by it once for X itself and once for T, S and
+    S S: those steps meet a column of X, whose norm is at most 1.3, with weights
+    1, |b| = 4.8 and 2 |c| |S| = 2 * 2.03 * 1.7 = 6.9: together
+    sqrt(1 + 1.3^2 (1 + 4.8^2 + 6.9^2)) = 11.1 of it per step.  The steps after
+    it multiply an error by at most 3.4445 each, five steps' together by
+    sqrt(sum of 3.4445^(2 j), j < 5) = 147.  Six root mean squares at the
+    maximum: 6 * 147 * 11.1 * 2^-39.8 < 2^-26.5; a row's own root mean square
+    error 147 * 11.1 * 2^-39.8 < 2^-29.1."""
+    dt = R.DTYPES[dtype]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(sum(shape))
+    n = shape[0] if by_row else shape[1]
+    d = 10.0 ** (-9 * torch.arange(n, device="cuda") / (n - 1))
+    G = (torch.randn(*shape, generator=gen, device="cuda") * (d[:, None] if by_row else d)).to(dt)
+    got, ref = binding.newton_schulz(G).double(), R.newton_schulz_ref(G)
+    if not by_row:
+        got, ref = got.t(), ref.t()
+    r = ref.square().mean(1, keepdim=True).sqrt()
+    step = 2.0 ** -23.8 + math.sqrt(max(shape) / 2) * 2.0 ** -25.3
+    rel = 2.0 ** -12.8 if dt == torch.bfloat16 else step
+    R.within(got, ref, R.HALF[dt] * ref.abs() + 138 * rel * r + 2.0 ** -26.5, "entries")
+    rms = (got - ref).square().mean(1).sqrt()
+    R.within(rms, torch.zeros_like(rms), (R.HALF[dt] + 23 * rel) * r[:, 0] + 2.0 ** -29.1, "rows")
+
+
+def test_below_the_planes():
+    """Entries below half the planes' last step, 2^-39 of the norm, are 0;
+    those above it have their polynomial's value: relative to it check()'s
+    error, and the planes' 2^-39 at the start and after each step, which a
+    further step multiplies by at most 3.4445."""
+    for dt, rel in ((torch.float32, 138 * 2.0 ** -23.8), (torch.bfloat16, 2.0 ** -5.6)):
+        values = [1.0, 2.0 ** -41, 2.0 ** -30, 2.0 ** -10]
+        G = torch.zeros(70, 90, dtype=dt, device="cuda")
+        for i, v in enumerate(values):
+            G[i, i] = v
+        got, ref = binding.newton_schulz(G, steps=3).double(), R.newton_schulz_ref(G, 3)
+        assert got[1, 1].item() == 0
+        assert got.count_nonzero().item() == 3
+        floor = 2.0 ** -39 * sum(3.4445 ** k for k in range(4))
+        for i in (0, 2, 3):
+            error = (got[i, i] - ref[i, i]).abs().item()
+            assert error <= (R.HALF[dt] + rel) * ref[i, i].item() + floor, (dt, values[i], error, ref[i, i].item())
