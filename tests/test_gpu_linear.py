@@ -1,6 +1,8 @@
 """The product with its epilogue and its backward pass against binary64."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -389,3 +391,106 @@ def test_preactivation_past_binary16():
         dZ, _ = binding.activation_backward(dY, z, kind)
         assert torch.equal(dZ[:, ::2], dY[:, ::2]) and bool((dZ[:, 1::2] == 0).all())
         assert bool(dX.isfinite().all()) and bool(dW.isfinite().all()) and bool(db.isfinite().all())
+
+
+GRAD_SIZES = [(3, 200, 130), (40, 129, 257), (130, 258, 190), (300, 500, 264), (700, 1000, 72), (1000, 1100, 2056),
+              (2900, 2951, 130), (2300, 2312, 264), (130, 200, 3001)]
+
+
+@pytest.mark.parametrize("size", GRAD_SIZES, ids=str)
+@pytest.mark.parametrize("op_a,op_b", [("N", "T"), ("N", "N"), ("T", "T"), ("T", "N")])
+def test_linear_grad_strides_and_in_place(size, op_a, op_b):
+    """Every argument with a leading dimension of its own, NaN beside the
+    factors, pre-activation and residual, a frame around the output; and the
+    residual's place as output."""
+    M, N, K = size
+    for dtype, ot, kind in ((torch.bfloat16, torch.bfloat16, "gelu"), (torch.float16, torch.float32, "silu")):
+        say(f"linear_grad {size} {op_a}{op_b} {dtype} -> {ot} {kind}, strides")
+        dZ, W = normal(1, M, K, dtype=dtype), normal(2, N, K, dtype=dtype, scale=K ** -0.5)
+        z, r = normal(3, M, N, dtype=dtype), normal(4, M, N, dtype=ot)
+        V = dZ.double() @ W.double().t() + r.double()
+        Sv = dZ.double().abs() @ W.double().abs().t() + r.double().abs()
+        D = V * R.act_derivative(z.double(), kind)
+        tol = grad_tol(D, V, Sv, K, z, kind, ot)
+        unrounded = tol - R.HALF[ot] * D.abs()
+        sums_tol = unrounded.sum(0) + (M + 8) * R.U * D.abs().sum(0)
+        dZs, Ws = (dZ.t().contiguous() if op_a == "T" else dZ), (W if op_b == "T" else W.t().contiguous())
+        dZs, _ = R.padded(dZs, dZs.shape[1] + 3, 1)
+        Ws, _ = R.padded(Ws, Ws.shape[1] + 5, 3)
+        zs, _ = R.padded(z, N + 7, 3)
+        rs, _ = R.padded(r, N + 2, 1)
+        out, buf = R.padded(torch.zeros(M, N, dtype=ot, device="cuda"), N + 1, 5, fill=7.0)
+        got, sums = binding.linear_grad(dZs, Ws, preact=zs, activation=kind, residual=rs, out=out, return_bias_grad=True,
+                                        op_a=op_a, op_b=op_b)
+        assert got is out
+        R.within(out, D, tol, "D")
+        R.within(sums, D.sum(0), sums_tol, "sums")
+        R.untouched(buf, M, N, N + 1, 5)
+        place, buf = R.padded(r, N + 3, 2, fill=7.0)
+        got, sums2 = binding.linear_grad(dZs, Ws, preact=zs, activation=kind, residual=place, out=place,
+                                         return_bias_grad=True, op_a=op_a, op_b=op_b)
+        assert got is place and torch.equal(place, out) and torch.equal(sums, sums2)
+        R.untouched(buf, M, N, N + 3, 2)
+
+
+@pytest.mark.parametrize("size", [(3, 200, 130), (64, 64, 72), (1001, 77, 501), (999, 300, 130), (2050, 2100, 264),
+                                  (8193, 128, 256)], ids=str)
+@pytest.mark.parametrize("op_b", ["N", "T"])
+def test_linear_backward_strides(size, op_b):
+    """Arguments with leading dimensions of their own and NaN beside them: the
+    bits of the contiguous call up to the order of sums, so within twice its
+    tolerance of binary64 (checked there) -- here against binary64 itself."""
+    M, N, K = size
+    dtype, kind = torch.bfloat16, "gelu_tanh"
+    say(f"linear_backward {size} {op_b}, strides")
+    X, W = normal(1, M, K, dtype=dtype), normal(2, K, N, dtype=dtype, scale=K ** -0.5)
+    dY, z = normal(3, M, N, dtype=dtype), normal(4, M, N, dtype=dtype)
+    Xs, _ = R.padded(X, K + 3, 1)
+    Ws, _ = R.padded(W.t().contiguous() if op_b == "T" else W, (K if op_b == "T" else N) + 5, 3)
+    dYs, _ = R.padded(dY, N + 9, 1)
+    zs, _ = R.padded(z, N + 1, 2)
+    dX, dW, db = binding.linear_backward(dYs, Xs, Ws, preact=zs, activation=kind, op_b=op_b)
+    D = dY.double() * R.act_derivative(z.double(), kind)
+    ed = R.HALF[dtype] * D.abs() + 32 * R.U * dY.double().abs()
+    ref = D @ W.double().t()
+    tol = R.HALF[dtype] * ref.abs() + (ed + (N + 2) * R.U * D.abs()) @ W.double().abs().t() * 1.01
+    R.within(dX, ref, tol, "dX")
+    refw = X.double().t() @ D
+    tolw = R.HALF[dtype] * refw.abs() + X.double().abs().t() @ (ed + (M + 2) * R.U * D.abs()) * 1.01
+    if op_b == "T":
+        refw, tolw = refw.t(), tolw.t()
+    R.within(dW, refw, tolw, "dW")
+    R.within(db, D.sum(0), 32 * R.U * dY.double().abs().sum(0) + (M + 8) * R.U * D.abs().sum(0), "db")
+
+
+@pytest.mark.parametrize("size", [(256, 256, 8192), (130, 100, 5000), (129, 131, 8191), (500, 60, 4100), (72, 300, 6002)],
+                         ids=str)
+@pytest.mark.parametrize("op_a,op_b", [("T", "N"), ("N", "N"), ("N", "T"), ("T", "T")])
+def test_few_tiles_and_a_long_depth(size, op_a, op_b):
+    """K split over blocks: strides, odd sizes, the epilogue on the planes."""
+    check_forward(*size, torch.bfloat16, "none", op_b, op_a=op_a, strides=True, bias=False, residual=False, preact=False)
+    check_forward(*size, torch.float16, "silu", op_b, op_a=op_a, strides=True, seed=3)
+    check_forward(*size, torch.bfloat16, "gelu", op_b, op_a=op_a, out_dtype=torch.float32, seed=5)
+
+
+def test_small_tails_keep_their_relative_accuracy():
+    """Activations of negative pre-activations far from zero, relative to their
+    value, in units U = 2^-24 of it: the exponential is within 2 + 1.23 |x| at
+    argument x (its unit's last place, the argument's scaling), reciprocals
+    within 2, sums and products 1 each.
+      silu       x = z: with 1 + e, reciprocal, product and store 5
+      gelu       x = z^2 / 2, its own rounding 1 |x|; t and the polynomial 7e-7
+                 (12 U), three products and the store 4.  The reference takes
+                 erfc: torch's ndtr adds 1 to erf, in steps of 2^-54
+      gelu_tanh  x = 2 u: four roundings of it 4 |x|; 5 as for silu"""
+    z = torch.linspace(-12.0, -0.01, 6000, device="cuda")
+    X, W = torch.zeros(3, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, z.numel(), dtype=torch.bfloat16, device="cuda")
+    for kind, x, own, rest in (("silu", z, 0, 5), ("gelu", z * z / 2, 1, 12 + 4),
+                               ("gelu_tanh", 1.6 * (z + 0.044715 * z ** 3), 4, 5)):
+        y = binding.linear(X, W, bias=z, activation=kind, out_dtype=torch.float32)
+        zd = z.double()
+        ref = zd * 0.5 * torch.special.erfc(-zd / math.sqrt(2.0)) if kind == "gelu" else R.act(zd, kind)
+        normal_range = ref.abs() > 2.0 ** -120
+        tol = ref.abs() * (2 + rest + (1.23 + own) * x.double().abs()) * R.U
+        R.within(y[1][normal_range], ref[normal_range], tol[normal_range], kind)
+        assert bool((y[1][~normal_range].abs() <= 2.0 ** -119).all())
