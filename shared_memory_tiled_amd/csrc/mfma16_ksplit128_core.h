@@ -82,7 +82,10 @@ struct Ksplit128Core {
         // the prologue and by the first two phases (peeled), and every copy in
         // the loop is the same.
         const int nph = TERMS * ceil_div(p.K, BK);
-        const int kbase = TERMS == 1 ? p.K - BK * nph : 0;   // -24 .. 0, a multiple of 8
+        // -24 .. 0 and a multiple of 8 with a k-contiguous factor (K is one then: a
+        // lane's 8 values lie on one side of k = 0); -31 .. 0 with two mn-contiguous
+        // ones, whose lanes bring one k each
+        const int kbase = TERMS == 1 ? p.K - BK * nph : 0;
         const int P = nph > w ? (nph - 1 - w) / 4 + 1 : 0;
         const int odd = P & 1;
         const int P2 = P + odd < 2 ? 2 : P + odd;
