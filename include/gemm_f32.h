@@ -505,8 +505,10 @@ typedef struct gemm_epilogue {
 } gemm_epilogue;
 
 /* The 16-bit product with its epilogue: the fully connected layer of the
- * same deep-learning chapter ("FC Layer = GEMM", "Backward") without a
- * binary32 product in memory between its steps.
+ * same deep-learning chapter ("FC Layer = GEMM", "Backward"), the epilogue in
+ * the product's kernel.  A product of few tiles whose K is split over blocks
+ * (and one of operands past 2 GiB, or of K == 0) passes through binary32
+ * planes in the workspace.
  *   op_a, op_b, format, M, N, K, A, lda, B, ldb   as for gemm_mixed_op; any
  *            alignment of 2 bytes and any leading dimension are taken
  *   C        M x N of epilogue->c_type, element (i, j) at C[i*ldc + j];

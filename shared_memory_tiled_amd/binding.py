@@ -637,7 +637,8 @@ def _linear_call(fmt, oa, ob, M, N, K, A, lda, B, ldb, C, ldc, ep) -> None:
 def linear(X, W, bias=None, activation="none", residual=None, out=None, out_dtype=None, return_preact=False,
            op_a="N", op_b="N", stream=None):
     """act(op_a(X) @ op_b(W) + bias) + residual for bfloat16 or float16 X and
-    W, in one product kernel with the rest in its epilogue.
+    W, with the rest in the product kernel's epilogue (few rows or tiles with a
+    long K: in a pass over binary32 partial sums).
 
     ``op_b="T"``: W is stored N x K.  ``out`` (or ``out_dtype``) has the
     factors' dtype (default) or float32 and overlaps neither of them;
