@@ -611,8 +611,9 @@ int layer_norm_backward(int type, int64_t rows, int64_t cols, const void *dy, in
  * matrices whose rows or columns are scaled over 1 .. 1e-9 (1000 x 600): 1e-6 or
  * less of a row's root mean square down to 1e-3 of the largest, 1.4e-4 at 1e-6,
  * 0.13 at 1e-9; bfloat16 results 2e-3, 2e-3, 0.13.  Products of a binary32
- * result take 22-bit factors, those of a bfloat16 one 11-bit factors (error
- * 1.7e-3 of the result's root mean square, with the rounding of the result).
+ * result take 22-bit factors, those of a bfloat16 one past 64 x 64 11-bit
+ * factors (error 1.7e-3 to 2e-3 of the result's root mean square, 1.66e-3 of it
+ * the rounding of the result).
  * A matrix with a NaN or an infinity gives NaN throughout; the other
  * matrices of the batch do not see it.  Statuses as above. */
 int64_t newton_schulz_workspace_size(int type, int64_t batch, int64_t rows, int64_t cols);   /* bytes; -1 if invalid */

@@ -17,7 +17,8 @@
 // product of the high planes alone, X itself and the diagonals of A and B
 // still in 22 and 24 bits: measured against binary64 their error, 5e-4 to
 // 7e-4 of an entry's root mean square, is a third of the result's own
-// rounding (1.7e-3), where products of bfloat16 factors give 1.4e-2 and more.
+// rounding (1.7e-3), where products of bfloat16 factors give 1.4e-2 and more
+// (matrices of at most 64 x 64 take both planes too, see the launcher).
 // Scales are powers of two from bounds on the singular values, so no plane
 // overflows; one scale serves a matrix.  The 22 bits hold for entries above
 // 2^-16 of the norm; below, the low plane runs out of binary16's exponents, and
@@ -265,7 +266,14 @@ hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, void* workspace, hipS
     }
     const bool wide = a.rows <= a.cols;
     const int64_t x_plane = l.x_stride / 2, s_plane = l.s_stride / 2;
-    const int terms = a.type == 0 ? 1 : 3;
+    // Matrices of one 64 x 64 tile have too few entries for the 11-bit factors'
+    // errors to average out where singular values lie close together: of 4096
+    // random 2 x 2 matrices the worst was 2.3e-2 of its root mean square off with
+    // one term, 3.2e-3 (the result's rounding) with three; 8 x 8 4.8e-3 and 2.2e-3.
+    // 64 x 64 takes 70 us for 61 with three.  From 80 x 80 on, and of long matrices,
+    // the worst stays within 2.0e-3.
+    const bool one_tile = l.rp == 64 && l.cp == 64;
+    const int terms = a.type == 0 && !one_tile ? 1 : 3;
     for (int k = 0; k < a.steps; ++k) {
         const double bx = a.bounds[k], ba = bx * bx, bt = (fabs((double)a.b) + fabs((double)a.c) * ba) * ba * 1.01;
         const float ss = plane_scale(ba), st = plane_scale(bt);

@@ -218,3 +218,65 @@ def test_below_the_planes():
         for i in (0, 2, 3):
             error = (got[i, i] - ref[i, i]).abs().item()
             assert error <= (R.HALF[dt] + rel) * ref[i, i].item() + floor, (dt, values[i], error, ref[i, i].item())
+
+
+def amplification(sigma, a, b, c, steps):
+    """Per matrix, how much an error made before step k = 0 .. steps (after
+    the last one for k = steps) counts in the result, to first order: in the
+    basis of the singular vectors a step multiplies the parts of a change of X
+    by the divided differences (p(s) - p(t)) / (s - t), (p(s) + p(t)) / (s + t) of
+    its pairs of singular values (p'(s) for equal ones; t = 0 for the directions
+    that only the longer side has)."""
+    s = torch.cat([sigma, torch.zeros_like(sigma[..., :1])], -1)
+    factors = []
+    for _ in range(steps):
+        x, y = s[..., :, None], s[..., None, :]
+        xy, x2y2 = x * y, x * x + y * y
+        # p over the pairs, the division done: s^3 and s^5's quotients
+        minus = a + b * (x2y2 + xy) + c * (x ** 4 + x ** 3 * y + xy ** 2 + x * y ** 3 + y ** 4)
+        plus = a + b * (x2y2 - xy) + c * (x ** 4 - x ** 3 * y + xy ** 2 - x * y ** 3 + y ** 4)
+        factors.append(torch.stack([minus, plus]).abs())
+        s = s * (a + s ** 2 * (b + c * s ** 2))
+    after = [torch.ones_like(factors[0])]
+    for f in reversed(factors):
+        after.insert(0, f * after[0])
+    return [t.amax((0, -1, -2)) for t in after]
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (1, 2), (2, 2), (3, 2), (3, 3), (4, 4), (2, 7), (8, 8), (16, 16), (17, 16),
+                                   (32, 32), (64, 64)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_every_small_matrix(shape, dtype):
+    """Thousands of small matrices, each within a bound of its own that holds
+    for every one, not for most.  A product of factors of two planes is off by
+    at most u of the product of their Frobenius norms: 2^-23 for what the planes
+    of each factor do not hold and 2^-22 for the product of the low planes,
+    2^-21 together, and 64 * 2^-24 = 2^-18 for the binary32 sum of up to 64 terms.
+    With f = |X|_F a step then errs by 1.21 dT + u |T|_F f + 3.45 u f, where dS =
+    u f^2 and dT = 4.775 dS + 2.04 (2 * 1.21^2 dS + u |S|_F^2); it counts in the
+    result as amplification() says, and so does X_0's rounding, u f.  Half a
+    step of the result is added."""
+    a, b, c = binding.NEWTON_SCHULZ_COEFFICIENTS
+    dt = R.DTYPES[dtype]
+    n = 4096 if shape[0] <= 8 else 512
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(shape[0] * 100 + shape[1])
+    G = (torch.randn(n, *shape, generator=gen, device="cuda") * 1e-2).to(dt)
+    got, ref = binding.newton_schulz(G).double(), R.newton_schulz_ref(G)
+    error, size = ((t).square().sum((-1, -2)).sqrt().cpu() for t in (got - ref, ref))
+    sigma = torch.linalg.svdvals(G.double().cpu())
+    sigma = sigma / (sigma.square().sum(-1, keepdim=True).sqrt() + 1e-7)
+    u = 2.0 ** -21 + 2.0 ** -18
+    counts = amplification(sigma, a, b, c, 5)
+    total, s = u * counts[0], sigma
+    for k in range(5):
+        f, sf = s.square().sum(-1).sqrt(), (s ** 4).sum(-1).sqrt()
+        tf = (b * s ** 2 + c * s ** 4).square().sum(-1).sqrt()
+        ds = u * f ** 2
+        dt_ = 4.775 * ds + 2.04 * (2 * 1.21 ** 2 * ds + u * sf ** 2)
+        total = total + (1.21 * dt_ + u * tf * f + 3.45 * u * f) * counts[k + 1]
+        s = (s * (a + s ** 2 * (b + c * s ** 2))).abs()
+    bound = R.HALF[dt] * size + R.TINY[dt] * math.sqrt(shape[0] * shape[1]) + total
+    say(f"{shape} {dtype}: largest relative error {(error / size).max().item():.1e}, of its bound {(error / bound).max().item():.2f}, "
+        f"largest bound without the result's rounding {(total / size).max().item():.1e}")
+    assert bool((error <= bound).all())
