@@ -270,7 +270,7 @@ hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, void* workspace, hipS
     // errors to average out where singular values lie close together: of 4096
     // random 2 x 2 matrices the worst was 2.3e-2 of its root mean square off with
     // one term, 3.2e-3 (the result's rounding) with three; 8 x 8 4.8e-3 and 2.2e-3.
-    // 64 x 64 takes 70 us for 61 with three.  From 80 x 80 on, and of long matrices,
+    // 64 x 64 takes 68 us in a graph for 59 with three.  From 80 x 80 on, and of long matrices,
     // the worst stays within 2.0e-3.
     const bool one_tile = l.rp == 64 && l.cp == 64;
     const int terms = a.type == 0 && !one_tile ? 1 : 3;
