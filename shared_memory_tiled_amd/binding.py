@@ -739,26 +739,29 @@ def activation_backward(dY, preact=None, activation="none", out=None, return_bia
     return out, sums
 
 
-def linear_backward(dY, X, W, preact=None, activation="none", weight_grad_dtype=None, op_b="N", stream=None):
+def linear_backward(dY, X, W, preact=None, activation="none", weight_grad_dtype=None, op_b="N", stream=None,
+                    return_bias_grad=True):
     """(dX, dW, db) of Y = act(X @ op_b(W) + bias): dZ = dY * act'(preact), db
     its column sums (float32), dX = dZ @ op_b(W)^T in dY's dtype, dW in W's
     layout and dtype (or float32 with ``weight_grad_dtype``).  dZ is rounded
     to dY's dtype between the two, for the matrix units.  The gradient of a
-    residual added after the activation is dY itself."""
+    residual added after the activation is dY itself.  Without
+    ``return_bias_grad`` (a layer that has no bias) db is None, and without an
+    activation dY is then read by the products only."""
     device = _device_of(dY, X, W, preact)
     if _elsewhere(stream, device):
         with _placed(stream, device):
-            return linear_backward(dY, X, W, preact, activation, weight_grad_dtype, op_b)
+            return linear_backward(dY, X, W, preact, activation, weight_grad_dtype, op_b, None, return_bias_grad)
     fmt, _, ob, M, N, K, ldx, ldw = _factors(X, W, "N", op_b)
     lddz = _matrix(dY, "dY", M, N, X.dtype)
     if weight_grad_dtype not in (None, W.dtype, torch.float32):
         raise TypeError("dW has W's dtype or float32")
     if _activation(activation):
-        dZ, db = activation_backward(dY, preact, activation)
+        dZ, db = activation_backward(dY, preact, activation, return_bias_grad=return_bias_grad)
         lddz = N or 1
     else:
         dZ = dY
-        _, db = activation_backward(dY, return_dz=False)
+        db = activation_backward(dY, return_dz=False)[1] if return_bias_grad else None
     dX = dY.new_empty((M, K))
     _linear_call(fmt, 0, 1 - ob, M, K, N, dZ, lddz, W, ldw, dX, K or 1, Epilogue(fmt))
     dW, lddw = _output(None, weight_grad_dtype, W, *W.shape)
@@ -802,14 +805,16 @@ def layer_norm(X, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     return out, mean, rstd
 
 
-def layer_norm_backward(dY, X, mean, rstd, weight=None, residual_grad=None, out=None, stream=None):
+def layer_norm_backward(dY, X, mean, rstd, weight=None, residual_grad=None, out=None, stream=None,
+                        return_param_grads=True):
     """(dX, dweight, dbias) of layer_norm; ``residual_grad`` (dY's dtype) is
-    added to dX.  dweight and dbias are float32.  ``out`` may be dY or
-    ``residual_grad``."""
+    added to dX.  dweight and dbias are float32, None without
+    ``return_param_grads`` (a norm that has no parameters).  ``out`` may be dY
+    or ``residual_grad``."""
     device = _device_of(dY, X, mean, rstd, weight, residual_grad, out)
     if _elsewhere(stream, device):
         with _placed(stream, device):
-            return layer_norm_backward(dY, X, mean, rstd, weight, residual_grad, out)
+            return layer_norm_backward(dY, X, mean, rstd, weight, residual_grad, out, None, return_param_grads)
     lib = load_library()
     t = _TYPE_OF_DTYPE.get(dY.dtype)
     if t is None or dY.dim() != 2:
@@ -830,11 +835,13 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, residual_grad=None, out=
         out, lddx = dY.new_empty((rows, cols)), cols
     else:
         lddx = _matrix(out, "out", rows, cols, dY.dtype)
-    dweight, dbias = dY.new_empty(cols, dtype=torch.float32), dY.new_empty(cols, dtype=torch.float32)
-    ws, addr, nbytes = _workspace(dY, lib.layer_norm_backward_workspace_size(t, rows, cols))
+    dweight, dbias, ws, addr, nbytes = None, None, None, None, 0
+    if return_param_grads:
+        dweight, dbias = dY.new_empty(cols, dtype=torch.float32), dY.new_empty(cols, dtype=torch.float32)
+        ws, addr, nbytes = _workspace(dY, lib.layer_norm_backward_workspace_size(t, rows, cols))
     _check(lib.layer_norm_backward(t, rows, cols, dY.data_ptr(), lddy, X.data_ptr(), ldx, mean.data_ptr(),
                                    rstd.data_ptr(), param, gamma, rgrad, ldr, out.data_ptr(), lddx,
-                                   dweight.data_ptr(), dbias.data_ptr(), addr, nbytes,
+                                   _addr(dweight), _addr(dbias), addr, nbytes,
                                    torch._C._cuda_getCurrentRawStream(device)))
     return out, dweight, dbias
 

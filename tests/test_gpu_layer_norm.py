@@ -276,3 +276,8 @@ def test_backward_without_parameter_gradients():
                                        None, None, 0, dx.data_ptr(), N, None, None, None, 0,
                                        torch.cuda.current_stream().cuda_stream) == 0
         assert torch.equal(dx, want)
+        torch.cuda.synchronize()
+        for stream in (None, torch.cuda.Stream()):
+            got = binding.layer_norm_backward(dy, x, mean, rstd, stream=stream, return_param_grads=False)
+            torch.cuda.synchronize()
+            assert got[1] is None and got[2] is None and torch.equal(got[0], want)

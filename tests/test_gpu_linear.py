@@ -494,3 +494,17 @@ def test_small_tails_keep_their_relative_accuracy():
         tol = ref.abs() * (2 + rest + (1.23 + own) * x.double().abs()) * R.U
         R.within(y[1][normal_range], ref[normal_range], tol[normal_range], kind)
         assert bool((y[1][~normal_range].abs() <= 2.0 ** -119).all())
+
+
+@pytest.mark.parametrize("size", [(1, 64, 64), (300, 200, 136), (1001, 77, 501)], ids=str)
+def test_linear_backward_without_a_bias(size):
+    """The same bits of dX and dW, no sums; also on another stream."""
+    M, N, K = size
+    X, W, dY, z = normal(1, M, K), normal(2, K, N, scale=K ** -0.5), normal(3, M, N), normal(4, M, N)
+    for kind, pre in (("none", None), ("silu", z)):
+        dX, dW, _ = binding.linear_backward(dY, X, W, preact=pre, activation=kind)
+        torch.cuda.synchronize()
+        for stream in (None, torch.cuda.Stream()):
+            got = binding.linear_backward(dY, X, W, preact=pre, activation=kind, stream=stream, return_bias_grad=False)
+            torch.cuda.synchronize()
+            assert got[2] is None and torch.equal(got[0], dX) and torch.equal(got[1], dW)
