@@ -550,6 +550,59 @@ int activation_grad(int activation, int format, int64_t M, int64_t N, const uint
                     const uint16_t *preact, int64_t ld_preact, uint16_t *dZ, int64_t ld_dz, float *bias_grad,
                     void *workspace, int64_t workspace_bytes, void *stream);
 
+/* The layer whose rows belong to groups with a weight each: the experts of a
+ * mixture, each with the rows that were sent to it, sorted by expert.  Group
+ * g has the rows offsets[g] .. offsets[g + 1] - 1 of A, C, residual and preact:
+ *   Z = A op(B_g) + bias_g,  C = act(Z) + residual     for the rows of group g
+ * in one launch over all groups.  With B the weights in their other
+ * orientation it is also the backward pass's input gradient, dX = dZ W_g^T.
+ *   groups    0 .. 65535; a group may be empty
+ *   M         rows of A and C (those of all groups, and others)
+ *   B         group g's K x N matrix (op_b N; N x K for T) at B + g*stride_b,
+ *             leading dimension ldb; stride_b >= 0 elements
+ *   offsets   DEVICE pointer to groups + 1 int32 (4-byte aligned), read when
+ *             the call runs: not decreasing, 0 <= offsets[0], offsets[groups]
+ *             <= M.  The library cannot check them; others give undefined
+ *             values in C and preact, but no access outside the matrices.
+ *   epilogue  forward mode only (GEMM_F32_ERR_INVALID_EPILOGUE); bias_g at
+ *             bias + g*ld_bias elements, ld_bias >= 0
+ * Rows of no group (before offsets[0], from offsets[groups] on) are neither
+ * read nor written: C and preact keep what they held there.  Everything else
+ * as for gemm_mixed_epilogue: types, alignment of one element, any leading
+ * dimension, roundings, workspaces, graphs, statuses. */
+int64_t gemm_mixed_grouped_workspace_size(int op_b, int format, int64_t groups, int64_t M, int64_t N, int64_t K,
+                                          const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb,
+                                          int64_t stride_b, const int32_t* offsets, const gemm_epilogue* epilogue,
+                                          int64_t ld_bias);   /* bytes; -1 if invalid */
+int gemm_mixed_grouped(int op_b, int format, int64_t groups, int64_t M, int64_t N, int64_t K, const uint16_t* A,
+                       int64_t lda, const uint16_t* B, int64_t ldb, int64_t stride_b, const int32_t* offsets, void* C,
+                       int64_t ldc, const gemm_epilogue* epilogue, int64_t ld_bias, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* The weights' gradients of the same layer: C_g = A_g^T B_g, M x N, summed over
+ * the rows of group g (A = X, B = dZ for weights stored K x N; A = dZ, B = X for
+ * N x K).  An empty group's gradient is +0.
+ *   A, B      rows x M and rows x N, as stored
+ *   C         group g's at C + g*stride_c, of c_type (format or
+ *             GEMM_MIXED_F32), stride_c >= (M - 1) ldc + N if groups > 1
+ * Sums are binary32; the rest as above. */
+int64_t gemm_mixed_grouped_grad_workspace_size(int format, int64_t groups, int64_t rows, int64_t M, int64_t N,
+                                               const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb,
+                                               const int32_t* offsets, int c_type);   /* bytes; -1 if invalid */
+int gemm_mixed_grouped_grad(int format, int64_t groups, int64_t rows, int64_t M, int64_t N, const uint16_t* A,
+                            int64_t lda, const uint16_t* B, int64_t ldb, const int32_t* offsets, int c_type, void* C,
+                            int64_t ldc, int64_t stride_c, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* activation_grad for the same layer: dZ = dY * act'(Z) on the groups' rows
+ * (dZ keeps what it held on others), and bias_grad, groups x N binary32 sums of
+ * dZ over each group's rows, before its rounding, in a fixed order (+0 for an
+ * empty group). */
+int64_t activation_grad_grouped_workspace_size(int64_t groups, int64_t M, int64_t N);   /* bytes; -1 if invalid */
+int activation_grad_grouped(int activation, int format, int64_t groups, int64_t M, int64_t N, const uint16_t* dY,
+                            int64_t ld_dy, const uint16_t* preact, int64_t ld_preact, const int32_t* offsets,
+                            uint16_t* dZ, int64_t ld_dz, float* bias_grad, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+
 /* Layer norm over the rows of a rows x cols matrix (cols >= 1).
  *   mean = <x>, rstd = 1 / sqrt(<(x - mean)^2> + eps), <.> over a row
  *   y = (x - mean) rstd gamma + beta

@@ -132,6 +132,21 @@ def load_library():
         lib.activation_grad.argtypes = [ctypes.c_int, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                         _vp, _i64, _vp]
         lib.activation_grad.restype = ctypes.c_int
+        gsig = [ctypes.c_int, ctypes.c_int] + [_i64] * 4 + [_vp, _i64, _vp, _i64, _i64, _vp]
+        lib.gemm_mixed_grouped_workspace_size.argtypes = gsig + [ep, _i64]
+        lib.gemm_mixed_grouped_workspace_size.restype = _i64
+        lib.gemm_mixed_grouped.argtypes = gsig + [_vp, _i64, ep, _i64, _vp, _i64, _vp]
+        lib.gemm_mixed_grouped.restype = ctypes.c_int
+        gsig = [ctypes.c_int] + [_i64] * 4 + [_vp, _i64, _vp, _i64, _vp, ctypes.c_int]
+        lib.gemm_mixed_grouped_grad_workspace_size.argtypes = gsig
+        lib.gemm_mixed_grouped_grad_workspace_size.restype = _i64
+        lib.gemm_mixed_grouped_grad.argtypes = gsig + [_vp, _i64, _i64, _vp, _i64, _vp]
+        lib.gemm_mixed_grouped_grad.restype = ctypes.c_int
+        lib.activation_grad_grouped_workspace_size.argtypes = [_i64] * 3
+        lib.activation_grad_grouped_workspace_size.restype = _i64
+        lib.activation_grad_grouped.argtypes = [ctypes.c_int, ctypes.c_int] + [_i64] * 3 + \
+            [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp]
+        lib.activation_grad_grouped.restype = ctypes.c_int
         lib.layer_norm.argtypes = [ctypes.c_int, _i64, _i64, _vp, _i64, ctypes.c_int, _vp, _vp, ctypes.c_float, _vp,
                                    _i64, _vp, _vp, _vp]
         lib.layer_norm.restype = ctypes.c_int
@@ -770,6 +785,168 @@ def linear_backward(dY, X, W, preact=None, activation="none", weight_grad_dtype=
         _linear_call(fmt, 1, 0, N, K, M, dZ, lddz, X, ldx, dW, lddw, ep)
     else:
         _linear_call(fmt, 1, 0, K, N, M, X, ldx, dZ, lddz, dW, lddw, ep)
+    return dX, dW, db
+
+
+# ------------------------------------------- layers of experts: grouped rows
+
+def _groups(W, offsets, op_b):
+    """(groups, K, N, leading dimension, group stride) of a layer's weights."""
+    if W.dim() != 3:
+        raise TypeError("W must be 3-D: a weight per group")
+    _offsets(offsets, W.shape[0])
+    groups, K, N = W.shape
+    if OPS[op_b]:
+        K, N = N, K
+    return groups, K, N, _row_major(W, "W"), _group_stride(W, "W")
+
+
+def _group_stride(t, what) -> int:
+    if t.shape[0] > 1 and t.stride(0) < 0:
+        raise ValueError(f"{what}'s groups must not run backwards")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _offsets(offsets, groups) -> None:
+    if offsets.dim() != 1 or offsets.dtype is not torch.int32 or not offsets.is_contiguous():
+        raise TypeError("offsets must be a contiguous vector of int32")
+    if offsets.shape[0] != groups + 1:
+        raise ValueError(f"{offsets.shape[0]} offsets for {groups} groups, not {groups + 1}")
+
+
+def grouped_linear(X, W, offsets, bias=None, activation="none", residual=None, out=None, out_dtype=None,
+                   return_preact=False, op_b="N", stream=None):
+    """act(X_i @ op_b(W[g]) + bias[g]) + residual_i for the rows i of each
+    group g, offsets[g] <= i < offsets[g + 1]: the layer of a mixture of experts
+    on rows sorted by expert, in one launch.
+
+    X is M x K, W groups x K x N (``op_b="T"``: groups x N x K), both bfloat16 or
+    float16; ``bias`` groups x N; ``offsets`` groups + 1 int32 on the GPU, not
+    decreasing, from at least 0 to at most M (the call does not look at them).
+    Rows of no group keep what ``out`` held (undefined in one allocated here).
+    The rest as for ``linear``."""
+    device = _device_of(X, W, offsets, bias, residual, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return grouped_linear(X, W, offsets, bias, activation, residual, out, out_dtype, return_preact, op_b)
+    lib = load_library()
+    fmt = _FORMAT_OF_DTYPE.get(X.dtype)
+    if fmt is None or W.dtype is not X.dtype or X.dim() != 2:
+        raise TypeError("X (2-D) and W (3-D) must be bfloat16 or float16 tensors of one dtype")
+    groups, K, N, ldw, stride_w = _groups(W, offsets, op_b)
+    ldx, M = _row_major(X, "X"), X.shape[0]
+    if X.shape[1] != K:
+        raise ValueError(f"inner dimensions differ: {X.shape[1]} vs {K}")
+    out, ldc = _output(out, out_dtype, X, M, N)
+    ep = Epilogue(_TYPE_OF_DTYPE[out.dtype], _activation(activation))
+    ld_bias = 0
+    if bias is not None:
+        if bias.dtype is not X.dtype and bias.dtype is not torch.float32:
+            raise TypeError(f"bias has X's dtype or float32, not {bias.dtype}")
+        if tuple(bias.shape) != (groups, N):
+            raise ValueError(f"bias has shape {tuple(bias.shape)}, not {(groups, N)}")
+        if N > 1 and bias.stride(1) != 1:
+            raise ValueError("bias must have unit column stride")
+        ld_bias = _group_stride(bias, "bias")
+        ep.bias_type = _TYPE_OF_DTYPE[bias.dtype]
+        ep.bias = bias.data_ptr()
+    if residual is not None:
+        ep.ld_residual = _matrix(residual, "residual", M, N, out.dtype)
+        ep.residual = residual.data_ptr()
+    preact = None
+    if return_preact:
+        preact = X.new_empty((M, N))
+        ep.preact = preact.data_ptr()
+        ep.ld_preact = N or 1
+    _grouped_call(lib, OPS[op_b], fmt, groups, M, N, K, X, ldx, W, ldw, stride_w, offsets, out, ldc, ep, ld_bias)
+    return (out, preact) if return_preact else out
+
+
+def _grouped_call(lib, ob, fmt, groups, M, N, K, A, lda, B, ldb, stride_b, offsets, C, ldc, ep, ld_bias=0) -> None:
+    """gemm_mixed_grouped on the current stream with a workspace of torch's."""
+    head = (ob, fmt, groups, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, stride_b, offsets.data_ptr())
+    ref = ctypes.byref(ep)
+    ws, addr, nbytes = _workspace(A, lib.gemm_mixed_grouped_workspace_size(*head, ref, ld_bias))
+    _check(lib.gemm_mixed_grouped(*head, C.data_ptr(), ldc, ref, ld_bias, addr, nbytes,
+                                  torch._C._cuda_getCurrentRawStream(A.get_device())))
+
+
+def grouped_activation_backward(dY, offsets, preact=None, activation="none", out=None, return_bias_grad=True,
+                                return_dz=True, stream=None):
+    """(dZ, db) of ``activation_backward`` for rows that belong to groups: dZ =
+    dY * act'(preact) on the groups' rows (others keep what ``out`` held), db
+    groups x N, each group's column sums of dZ in float32.  ``out`` may be dY."""
+    device = _device_of(dY, offsets, preact, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return grouped_activation_backward(dY, offsets, preact, activation, out, return_bias_grad, return_dz)
+    lib = load_library()
+    fmt = _FORMAT_OF_DTYPE.get(dY.dtype)
+    if fmt is None or dY.dim() != 2:
+        raise TypeError("dY must be a 2-D bfloat16 or float16 tensor")
+    groups = max(offsets.numel() - 1, 0)
+    _offsets(offsets, groups)
+    ldy = _row_major(dY, "dY")
+    M, N = dY.shape
+    act = _activation(activation)
+    if preact is None and act:
+        raise ValueError("the gradient of an activation needs preact")
+    ldz = 0 if preact is None else _matrix(preact, "preact", M, N, dY.dtype)
+    if not return_dz:
+        out, ldo = None, 0
+    elif out is None:
+        out, ldo = dY.new_empty((M, N)), N or 1
+    else:
+        ldo = _matrix(out, "out", M, N, dY.dtype)
+    sums, ws, addr, nbytes = None, None, None, 0
+    if return_bias_grad:
+        sums = dY.new_empty((groups, N), dtype=torch.float32)
+        ws, addr, nbytes = _workspace(dY, lib.activation_grad_grouped_workspace_size(groups, M, N))
+    _check(lib.activation_grad_grouped(act, fmt, groups, M, N, dY.data_ptr(), ldy, _addr(preact), ldz,
+                                       offsets.data_ptr(), _addr(out), ldo, _addr(sums), addr, nbytes,
+                                       torch._C._cuda_getCurrentRawStream(device)))
+    return out, sums
+
+
+def grouped_linear_backward(dY, X, W, offsets, preact=None, activation="none", weight_grad_dtype=None, op_b="N",
+                            stream=None, return_bias_grad=True):
+    """(dX, dW, db) of ``grouped_linear``: dZ = dY * act'(preact) in dY's dtype,
+    dX its product with each group's transposed weight (rows of no group are
+    undefined), dW groups of X_g^T dZ_g in W's layout and dtype (or float32 with
+    ``weight_grad_dtype``; zeros for an empty group), db groups x N in float32
+    (None without ``return_bias_grad``).  The rest as for ``linear_backward``."""
+    device = _device_of(dY, X, W, offsets, preact)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return grouped_linear_backward(dY, X, W, offsets, preact, activation, weight_grad_dtype, op_b, None,
+                                           return_bias_grad)
+    lib = load_library()
+    fmt = _FORMAT_OF_DTYPE.get(X.dtype)
+    if fmt is None or W.dtype is not X.dtype or X.dim() != 2:
+        raise TypeError("X (2-D) and W (3-D) must be bfloat16 or float16 tensors of one dtype")
+    groups, K, N, ldw, stride_w = _groups(W, offsets, op_b)
+    ob, ldx, M = OPS[op_b], _row_major(X, "X"), X.shape[0]
+    if X.shape[1] != K:
+        raise ValueError(f"inner dimensions differ: {X.shape[1]} vs {K}")
+    lddz = _matrix(dY, "dY", M, N, X.dtype)
+    if weight_grad_dtype not in (None, W.dtype, torch.float32):
+        raise TypeError("dW has W's dtype or float32")
+    dZ, db = dY, None
+    if _activation(activation):
+        dZ, db = grouped_activation_backward(dY, offsets, preact, activation, return_bias_grad=return_bias_grad)
+        lddz = N or 1
+    elif return_bias_grad:
+        db = grouped_activation_backward(dY, offsets, return_dz=False)[1]
+    dX = dY.new_empty((M, K))
+    _grouped_call(lib, 1 - ob, fmt, groups, M, K, N, dZ, lddz, W, ldw, stride_w, offsets, dX, K or 1, Epilogue(fmt))
+    dW = W.new_empty(W.shape, dtype=weight_grad_dtype or W.dtype)
+    A, lda, B, ldb = (dZ, lddz, X, ldx) if ob else (X, ldx, dZ, lddz)
+    rows, cols = dW.shape[1:]
+    c_type = _TYPE_OF_DTYPE[dW.dtype]
+    head = (fmt, groups, M, rows, cols, A.data_ptr(), lda, B.data_ptr(), ldb, offsets.data_ptr(), c_type)
+    ws, addr, nbytes = _workspace(X, lib.gemm_mixed_grouped_grad_workspace_size(*head))
+    _check(lib.gemm_mixed_grouped_grad(*head, dW.data_ptr(), cols or 1, rows * cols, addr, nbytes,
+                                       torch._C._cuda_getCurrentRawStream(device)))
     return dX, dW, db
 
 

@@ -1,0 +1,322 @@
+// grouped.hip -- the layer whose rows belong to groups (experts) with a weight
+// each: choice of kernel, the tiles for any sizes and alignment, and the
+// activation's gradient with the groups' bias gradients.
+//
+// For the rows i of group g: Z_i = X_i W_g + b_g, Y_i = act(Z_i); backward,
+// dZ = dY act'(Z), dX_i = dZ_i W_g^T (the same product with the weight's other
+// orientation), dW_g = X_g^T dZ_g, db_g = the sum of dZ's rows of g.
+#include "epilogue.h"
+#include "grouped_kernels.h"
+#include "mfma16_common.h"
+#include "staged_tile.h"
+
+#include <limits.h>
+
+namespace gemmf32 {
+
+namespace {
+
+// ------------------------------------------------------ tiles for any problem
+
+// A tile of T rows of a factor, 64 deep, as 16-bit values in LDS: loaded by
+// 256 threads in runs of 8 that go through registers, so any alignment and
+// size will do (whole runs as one 16-byte load, runs across an edge value by
+// value, zeros past it), with 64-bit places.
+//   KC (k runs along the rows): T rows of 64, fragments read as 16 bytes of k
+//   else: 64 rows of T, fragments through the transposed read
+// Rows are padded by 16 bytes, which spreads them over the banks.
+template <bool KC, int T>
+struct GroupedTile {
+    static constexpr int BK = 64, PITCH = (KC ? BK : T) + 8, ELEMS = (KC ? T : BK) * PITCH;
+    static constexpr int RUNS = T * BK / 8 / 256;           // per thread
+    static constexpr int PER_ROW = (KC ? BK : T) / 8;
+    u32x4 held[RUNS];
+
+    // Rows (mn) mn0 .. of `mn`, k0 .. of `k`.
+    __device__ __forceinline__ void load(const uint16_t* base, int64_t ld, int mn0, int mn, int k0, int k) {
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+            const int c = i * 256 + threadIdx.x, r = c / PER_ROW, at = 8 * (c % PER_ROW);
+            const int row = (KC ? mn0 : k0) + r, col = (KC ? k0 : mn0) + at;
+            const int valid = row < (KC ? mn : k) ? (KC ? k : mn) - col : 0;
+            const uint16_t* const q = base + (int64_t)row * ld + col;
+            u32x4 v = {0, 0, 0, 0};
+            if (valid >= 8) {
+                __builtin_memcpy(&v, q, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < valid) v[e / 2] |= (unsigned)q[e] << (16 * (e % 2));
+            }
+            held[i] = v;
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t* lds) const {
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+            const int c = i * 256 + threadIdx.x;
+            *reinterpret_cast<u32x4*>(lds + c / PER_ROW * PITCH + 8 * (c % PER_ROW)) = held[i];
+        }
+    }
+    // Fragments of rows mn + 16 f, k 32 s + 8 (lane / 16) .. + 7.
+    template <int F>
+    __device__ static __forceinline__ void fragments(const uint16_t* lds, int mn, int s, int lane, u32x4 (&q)[F]) {
+        if constexpr (KC) {
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+                q[f] = *reinterpret_cast<const u32x4*>(lds + (mn + 16 * f + lane % 16) * PITCH + 32 * s + 8 * (lane / 16));
+        } else {
+            const int j = lane % 16;
+            const uint32_t at = lds_addr(lds + (32 * s + 8 * (lane / 16) + j / 4) * PITCH + mn + 4 * (j % 4));
+            u32x2 h[F][2];
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) h[f][i] = read_tr16(at + 2 * (4 * i * PITCH + 16 * f));
+            wait_halves(h);
+#pragma unroll
+            for (int f = 0; f < F; ++f) q[f] = u32x4{h[f][0][0], h[f][0][1], h[f][1][0], h[f][1][1]};
+        }
+    }
+    __device__ static __forceinline__ void wait_halves(u32x2 (&h)[4][2]) {
+        asm volatile("s_waitcnt lgkmcnt(0)"
+                     : "+v"(h[0][0]), "+v"(h[0][1]), "+v"(h[1][0]), "+v"(h[1][1]), "+v"(h[2][0]), "+v"(h[2][1]),
+                       "+v"(h[3][0]), "+v"(h[3][1])
+                     :
+                     : "memory");
+    }
+    __device__ static __forceinline__ void wait_halves(u32x2 (&h)[2][2]) {
+        asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(h[0][0]), "+v"(h[0][1]), "+v"(h[1][0]), "+v"(h[1][1]) : : "memory");
+    }
+};
+
+// The BT x BT tile at (m0, n0) of a product: four waves of BT / 2 x BT / 2, two
+// stages of LDS, the next phase's loads in registers while one is computed.
+template <int FMT, bool KCA, bool KCB, int BT>
+struct GroupedCore {
+    using TA = GroupedTile<KCA, BT>;
+    using TB = GroupedTile<KCB, BT>;
+    static constexpr int F = BT / 32;
+    using Staged = StagedTile<F, F>;
+    static constexpr int STAGE = TA::ELEMS + TB::ELEMS;
+    static constexpr int PATCHES = 4 * Staged::PATCH * 4;
+    static constexpr int LDS_BYTES = 4 * STAGE > PATCHES ? 4 * STAGE : PATCHES;
+
+    __device__ static __forceinline__ void run(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
+                                               floatx4 (&acc)[F][F]) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        uint16_t* const stage = reinterpret_cast<uint16_t*>(lds);
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+        TA a;
+        TB b;
+        const int phases = ceil_div(p.K, 64);
+        if (phases > 0) {
+            a.load(p.A, p.lda, m0, p.M, 0, p.K);
+            b.load(p.B, p.ldb, n0, p.N, 0, p.K);
+        }
+        for (int ph = 0; ph < phases; ++ph) {
+            uint16_t* const cur = stage + (ph & 1) * STAGE;
+            a.store(cur);
+            b.store(cur + TA::ELEMS);
+            __syncthreads();               // the other stage's readers passed the barrier before this one
+            if (ph + 1 < phases) {
+                a.load(p.A, p.lda, m0, p.M, 64 * (ph + 1), p.K);
+                b.load(p.B, p.ldb, n0, p.N, 64 * (ph + 1), p.K);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                u32x4 fa[F], fb[F];
+                TA::template fragments<F>(cur, wave / 2 * (BT / 2), s, lane, fa);
+                TB::template fragments<F>(cur + TA::ELEMS, wave % 2 * (BT / 2), s, lane, fb);
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+#pragma unroll
+                    for (int j = 0; j < F; ++j) acc[i][j] = mfma16x16<FMT>(fa[i], fb[j], acc[i][j]);
+            }
+        }
+        __syncthreads();
+    }
+
+    __device__ static __forceinline__ void finish(const floatx4 (&acc)[F][F], const EpilogueArgs& e, int m0, int n0,
+                                                  unsigned char* lds) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        float* const patch = reinterpret_cast<float*>(lds) + wave * Staged::PATCH;
+        const int row0 = m0 + wave / 2 * (BT / 2), col0 = n0 + wave % 2 * (BT / 2);
+        Staged::template rows<false, 0>(
+            acc, patch, nullptr, lane, false, [](int, int, u32x4 (&)[1]) {},
+            [&](int row, int col, float (&v)[8], const u32x4 (&)[1]) __attribute__((always_inline)) {
+                if (row0 + row >= e.M || col0 + col >= e.N) return;
+                float b[8];
+                load_bias(e, col0 + col, b);
+                EpilogueRun<8, false> run;
+                run.load(e, row0 + row, col0 + col);
+                run.finish(e, row0 + row, col0 + col, b, v);
+            },
+            [](int, int) {});
+    }
+};
+
+template <int FMT, bool KCB, int BT>
+__global__ __launch_bounds__(256)
+void grouped_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_n, int group_m) {
+    using Core = GroupedCore<FMT, true, KCB, BT>;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
+    const GroupRows r = locate_group_tile<BT>(a, (int)blockIdx.x, tiles_n, group_m);
+    if (r.rows < 0) return;
+    enter_group(a, r, &p, &e);
+    floatx4 acc[Core::F][Core::F];
+    Core::run(p, BT * r.tm, BT * r.tn, lds, acc);
+    Core::finish(acc, e, BT * r.tm, BT * r.tn, lds);
+}
+
+// The weights' gradient: group blockIdx.x / tiles, whose tiles the XCDs share
+// (groups differ in their rows, so whole groups to an XCD would not balance).
+template <int FMT, int BT>
+__global__ __launch_bounds__(256)
+void grouped_grad_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, int group_m) {
+    using Core = GroupedCore<FMT, false, false, BT>;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
+    const int tiles = tiles_m * tiles_n, g = (int)blockIdx.x / tiles;
+    int tm, tn, begin, end;
+    grouped_tile((int)blockIdx.x - g * tiles, tiles_m, tiles_n, group_m, &tm, &tn);
+    group_range(a, g, &begin, &end);
+    p.A += (int64_t)begin * p.lda;
+    p.B += (int64_t)begin * p.ldb;
+    p.K = end - begin;
+    e.C = static_cast<char*>(e.C) + (e.c_type == 2 ? 4 : 2) * (g * a.stride_b);
+    floatx4 acc[Core::F][Core::F];
+    Core::run(p, BT * tm, BT * tn, lds, acc);
+    Core::finish(acc, e, BT * tm, BT * tn, lds);
+}
+
+}  // namespace
+
+int64_t grouped_workspace(const GroupedArgs&, const Gemm16Args&, const EpilogueArgs&, int) { return 0; }
+
+hipError_t launch_grouped(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
+                          int op_b, void*) {
+    constexpr int BT = 128;
+    const int tn = ceil_div(p.N, BT);
+    const int64_t blocks = grouped_row_tiles(a.rows, a.groups, BT) * tn;
+    if (blocks > 0x7FFFFFFFll / 256) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), b(256);
+    if (format == 0 && op_b) hipLaunchKernelGGL((grouped_kernel<0, true, BT>), grid, b, 0, s, a, p, e, tn, 8);
+    else if (format == 0) hipLaunchKernelGGL((grouped_kernel<0, false, BT>), grid, b, 0, s, a, p, e, tn, 8);
+    else if (op_b) hipLaunchKernelGGL((grouped_kernel<1, true, BT>), grid, b, 0, s, a, p, e, tn, 8);
+    else hipLaunchKernelGGL((grouped_kernel<1, false, BT>), grid, b, 0, s, a, p, e, tn, 8);
+    return hipGetLastError();
+}
+
+int64_t grouped_grad_workspace(const GroupedArgs&, const Gemm16Args&, const EpilogueArgs&) { return 0; }
+
+hipError_t launch_grouped_grad(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                               int format, void*) {
+    constexpr int BT = 128;
+    const int tm = ceil_div(p.M, BT), tn = ceil_div(p.N, BT);
+    const int64_t blocks = (int64_t)tm * tn * a.groups;
+    if ((int64_t)tm * tn > 0x7FFFFFFFll / 256 || blocks > 0x7FFFFFFFll / 256) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), b(256);
+    if (format == 0) hipLaunchKernelGGL((grouped_grad_kernel<0, BT>), grid, b, 0, s, a, p, e, tm, tn, 8);
+    else hipLaunchKernelGGL((grouped_grad_kernel<1, BT>), grid, b, 0, s, a, p, e, tm, tn, 8);
+    return hipGetLastError();
+}
+
+// --------------------------------------------- the activation's gradient
+
+namespace {
+
+// dZ = dY act'(Z) over tiles of kActRows rows of one group x 256 columns, a
+// thread 8 columns of every eighth row; the tile's column sums, of dZ before
+// its rounding, go to partials[tile][N].  One tile row per row tile of the
+// groups; the last block of a column adds nothing: a second kernel adds each
+// group's tiles in order.
+constexpr int kActRows = 64, kActCols = 256;
+__global__ __launch_bounds__(256)
+void grouped_activation_kernel(GroupedArgs a, EpilogueArgs e, const uint16_t* dY, int64_t ld, int tiles_n, float* partials) {
+    __shared__ float part[8][kActCols];
+    const GroupRows r = locate_group_tile<kActRows>(a, (int)blockIdx.x, tiles_n, 1 << 20);
+    if (r.rows < 0) return;
+    const int c = 8 * (threadIdx.x & 31), w = threadIdx.x >> 5, col = r.tn * kActCols + c;
+    const int first = r.tm * kActRows, last = min(first + kActRows, r.rows);
+    float sums[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (col < e.N) {
+        for (int i = first + w; i < last; i += 8) {
+            const int64_t row = r.begin + i;
+            RawRun<8> y, z;
+            y.load(e.z_type, dY, row * ld + col, e.N - col);
+            float v[8], zv[8];
+            if (e.act != kActNone) z.load(e.z_type, e.preact, row * e.ldz + col, e.N - col);
+            y.values(e.z_type, v);
+            if (e.act != kActNone) {
+                z.values(e.z_type, zv);
+                times_derivative(e.act, zv, v);
+            }
+            if (e.C != nullptr) store_values(e.c_type, e.C, row * e.ldc + col, e.N - col, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sums[k] += v[k];
+        }
+    }
+    if (partials == nullptr) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[w][c + k] = sums[k];
+    __syncthreads();
+    const int at = threadIdx.x, out = r.tn * kActCols + at;
+    if (out >= e.N) return;
+    float s = part[0][at];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += part[k][at];
+    // The row tile's number over all groups: the tiles of the groups before
+    // end where this group's begin, at most one more per group than whole ones.
+    partials[((int64_t)r.begin / kActRows + r.group + r.tm) * e.N + out] = s;
+}
+
+// db[g][n] = the sum of group g's tiles, in order; a block per 64 columns and
+// group, four tiles at a time.
+__global__ __launch_bounds__(256)
+void grouped_sum_kernel(GroupedArgs a, int N, const float* partials, float* out) {
+    __shared__ float part[4][64];
+    int begin, end;
+    const int g = blockIdx.y;
+    group_range(a, g, &begin, &end);
+    const int col = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+    const int tiles = (end - begin + kActRows - 1) / kActRows;
+    const float* const q = partials + ((int64_t)begin / kActRows + g) * N;
+    float s = 0.f;
+    if (col < N)
+        for (int i = w; i < tiles; i += 4) s += q[(int64_t)i * N + col];
+    part[w][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (w == 0 && col < N)
+        out[(int64_t)g * N + col] = ((part[0][threadIdx.x] + part[1][threadIdx.x]) + part[2][threadIdx.x]) + part[3][threadIdx.x];
+}
+
+}  // namespace
+
+// Tile t of group g is partials row begin_g / kActRows + g + t.  Rows of
+// different groups do not meet: begin / 64 + tiles <= end / 64 + 1 for any
+// range, so a group's last row is below the next group's first.
+int64_t grouped_activation_workspace(int64_t rows, int64_t groups, int64_t N) {
+    return 4 * (rows / kActRows + groups + 1) * N;
+}
+
+hipError_t launch_grouped_activation(const GroupedArgs& a, const EpilogueArgs& e, const uint16_t* dY, int64_t ld,
+                                     float* partials, hipStream_t s) {
+    const int tn = ceil_div(e.N, kActCols);
+    const int64_t blocks = grouped_row_tiles(a.rows, a.groups, kActRows) * tn;
+    if (blocks > 0x7FFFFFFFll / 256 || a.groups > 65535) return hipErrorInvalidValue;
+    float* const part = e.bias_grad != nullptr ? partials : nullptr;
+    if (blocks > 0) {
+        hipLaunchKernelGGL(grouped_activation_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, e, dY, ld, tn, part);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    if (part == nullptr) return hipSuccess;
+    hipLaunchKernelGGL(grouped_sum_kernel, dim3(ceil_div(e.N, 64), (unsigned)a.groups), dim3(256), 0, s, a, e.N, part,
+                       e.bias_grad);
+    return hipGetLastError();
+}
+
+}  // namespace gemmf32

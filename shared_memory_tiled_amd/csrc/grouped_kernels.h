@@ -1,0 +1,139 @@
+// grouped_kernels.h -- the layer whose rows belong to groups (experts) with a
+// weight each: where a block's tile lies, and the launchers of its kernels (not
+// part of the public interface).
+//
+// Group g holds the rows offsets[g] .. offsets[g + 1] - 1 of A, sorted by
+// group; the offsets are on the device, so the host knows only how many row
+// tiles there can be and every block finds its own.  Offsets are read through
+// clamps: whatever they hold, no row outside the matrices is touched.
+#pragma once
+
+#include "launch.h"
+
+namespace gemmf32 {
+
+// Rows x N = A (rows x K) W_g + bias_g, or, for the weights' gradient, M x N =
+// A_g^T B_g.
+struct GroupedArgs {
+    int groups;
+    const int* offsets;                // groups + 1
+    int rows;                          // of A (and of B in the gradient)
+    int64_t stride_b;                  // elements from a group's weight to the next; gradient: of C
+    int64_t ld_bias;                   // elements from a group's bias to the next
+};
+
+// The smallest tile any launch uses: what the entry points bound the grid by.
+constexpr int kGroupedSmallTile = 64;
+
+// Row tiles of `tile` rows there can be: every group but the empty ones may
+// leave one tile partly filled.
+inline int64_t grouped_row_tiles(int64_t rows, int64_t groups, int64_t tile) {
+    const int64_t used = groups < rows ? groups : rows;
+    return (rows + used * (tile - 1)) / tile;
+}
+
+#if defined(__HIPCC__)
+namespace {
+
+struct GroupRows {
+    int group, begin, rows;            // of the group; rows < 0: none for this block
+    int tm, tn;                        // the tile within the group
+};
+
+__device__ __forceinline__ void group_range(const GroupedArgs& a, int g, int* begin, int* end) {
+    *begin = min(max(a.offsets[g], 0), a.rows);
+    *end = min(max(a.offsets[g + 1], *begin), a.rows);
+}
+
+// Inclusive sum over the wave's lanes: within rows of 16 lanes, then across.
+__device__ __forceinline__ int wave_inclusive_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);    // row_shr 1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // lane 15 of rows 0, 2 to rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // lane 31 to rows 2, 3
+    return v;
+}
+
+// Block b's tile among the groups' tiles of TILE rows x tiles_n columns, in the
+// order of the groups, within one as grouped_tile orders them, each XCD walking
+// a contiguous run.  Every wave computes it for itself: 64 groups at a time, a
+// lane each.
+template <int TILE>
+__device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int b, int tiles_n, int group_m) {
+    const int lane = threadIdx.x & 63;
+    int begin = 0, end = 0, incl = 0, total = 0;
+    const bool one = a.groups <= 64;
+    for (int g0 = 0; g0 < a.groups; g0 += 64) {
+        begin = end = 0;
+        if (g0 + lane < a.groups) group_range(a, g0 + lane, &begin, &end);
+        incl = wave_inclusive_sum((end - begin + TILE - 1) / TILE);
+        total += __builtin_amdgcn_readlane(incl, 63);
+    }
+    GroupRows r{0, 0, -1, 0, 0};
+    const int blocks = total * tiles_n;
+    if (b >= blocks) return r;
+    const int logical = xcd_contiguous(b, blocks);
+    const int row = logical / tiles_n;                      // row tile if the tiles went row by row
+    int before = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += 64) {
+        if (!one) {
+            begin = end = 0;
+            if (g0 + lane < a.groups) group_range(a, g0 + lane, &begin, &end);
+            incl = wave_inclusive_sum((end - begin + TILE - 1) / TILE);
+        }
+        const int sum = __builtin_amdgcn_readlane(incl, 63);
+        if (row < before + sum) {
+            const uint64_t past = __builtin_amdgcn_ballot_w64(before + incl > row);
+            const int l = __builtin_ctzll(past);
+            r.group = g0 + l;
+            r.begin = __builtin_amdgcn_readlane(begin, l);
+            r.rows = __builtin_amdgcn_readlane(end, l) - r.begin;
+            const int tiles_m = (r.rows + TILE - 1) / TILE;
+            const int first = before + __builtin_amdgcn_readlane(incl, l) - tiles_m;
+            const int local = logical - first * tiles_n;
+            const int gsize = group_m * tiles_n;
+            const int q = local / gsize, first_m = q * group_m;
+            const int gm = min(tiles_m - first_m, group_m);
+            const int in_q = local - q * gsize;
+            r.tm = first_m + in_q % gm;
+            r.tn = in_q / gm;
+            return r;
+        }
+        before += sum;
+    }
+    return r;
+}
+
+// The group's share of a product and its epilogue.
+__device__ __forceinline__ void enter_group(const GroupedArgs& a, const GroupRows& r, Gemm16Args* p, EpilogueArgs* e) {
+    p->M = e->M = r.rows;
+    p->A += (int64_t)r.begin * p->lda;
+    p->B += r.group * a.stride_b;
+    e->C = static_cast<char*>(e->C) + (e->c_type == 2 ? 4 : 2) * (r.begin * e->ldc);
+    if (e->residual != nullptr)
+        e->residual = static_cast<const char*>(e->residual) + (e->c_type == 2 ? 4 : 2) * (r.begin * e->ldr);
+    if (e->preact != nullptr) e->preact = static_cast<char*>(e->preact) + 2 * (r.begin * e->ldz);
+    if (e->bias != nullptr)
+        e->bias = static_cast<const char*>(e->bias) + (e->bias_type == 2 ? 4 : 2) * (r.group * a.ld_bias);
+}
+
+}  // namespace
+#endif
+
+// p: A, B, N, K and their leading dimensions (M is not used); e: M is not used.
+int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, int op_b);
+hipError_t launch_grouped(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
+                          int op_b, void* workspace);
+// The weights' gradient: p.M x p.N per group from A (rows x M) and B (rows x N), both
+// as stored; e: C, its type and leading dimension.
+int64_t grouped_grad_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e);
+hipError_t launch_grouped_grad(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                               int format, void* workspace);
+// dZ = dY act'(Z) over the groups' rows, and the groups' column sums (e.bias_grad: groups x N).
+int64_t grouped_activation_workspace(int64_t rows, int64_t groups, int64_t N);
+hipError_t launch_grouped_activation(const GroupedArgs& a, const EpilogueArgs& e, const uint16_t* dY, int64_t ld,
+                                     float* partials, hipStream_t s);
+
+}  // namespace gemmf32
