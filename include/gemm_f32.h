@@ -80,6 +80,7 @@ extern "C" {
 #define GEMM_F32_ERR_INVALID_ACTIVATION 14 /* activation unknown                       */
 #define GEMM_F32_ERR_INVALID_EPILOGUE 15 /* an epilogue field its mode does not take   */
 #define GEMM_F32_ERR_INVALID_SCALAR 16  /* eps, a coefficient or a step count out of range */
+#define GEMM_F32_ERR_OVERLAP        17  /* an output overlaps another tensor of its call  */
 
 /* Kernel ladder.  Each rung computes the same product; each is tested against
  * the oracle and against the rung below it.
@@ -635,6 +636,40 @@ int layer_norm_backward(int type, int64_t rows, int64_t cols, const void *dy, in
                         int64_t ldx, const float *mean, const float *rstd, int param_type, const void *gamma,
                         const void *residual_grad, int64_t ld_residual, void *dx, int64_t lddx, float *dgamma,
                         float *dbeta, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* The norm over all of a model's gradients, and their clipping.
+ *   norm = sqrt(sum over the tensors and their values of g^2)
+ *   out  = g min(1, max_norm / (norm + eps))
+ *   count     tensors; grads, out, sizes and types are HOST arrays of that
+ *             length, read before the call returns
+ *   grads     device pointers to sizes[i] values each, in one run of memory, of
+ *             types[i]: GEMM_MIXED_BF16, _F16 or _F32, mixed as they come;
+ *             aligned to the type's size.  A size of 0 is skipped, and its
+ *             pointer may be NULL
+ *   out       likewise; out[i] may be grads[i].  Outputs must overlap nothing
+ *             else in the lists (GEMM_F32_ERR_OVERLAP): a tensor listed twice
+ *             counts twice in grad_norm and is refused in place
+ *   norm      device pointer to one binary32 value: written by grad_norm and
+ *             grad_clip_norm, read by grad_clip (so that the norms of shards
+ *             can be joined in between)
+ *   max_norm  >= 0, finite;  eps > 0, finite
+ *   workspace of grad_norm_workspace_size() bytes, as for gemm_mixed_epilogue
+ * Squares are added in binary64 in a fixed order, so that no binary32 value is
+ * too large or too small to count; the norm is rounded to binary32, the factor
+ * is computed from it and rounded to binary32, and every value times the factor
+ * is rounded once more to its type.  In place with a factor of 1 nothing is
+ * written.  A norm that is infinite gives a factor of 0 (0, and NaN in place of
+ * infinities), a NaN gives NaN: look at the norm before the update.  Without
+ * tensors the norm is +0.  Statuses, streams and graphs as above; a captured
+ * graph holds the lists as they were. */
+int64_t grad_norm_workspace_size(int64_t count, const int64_t *sizes);   /* bytes; -1 if invalid */
+int grad_norm(int64_t count, const void *const *grads, const int64_t *sizes, const int *types, float *norm,
+              void *workspace, int64_t workspace_bytes, void *stream);
+int grad_clip(int64_t count, const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
+              const float *norm, float max_norm, float eps, void *stream);
+/* Both, in a launch less. */
+int grad_clip_norm(int64_t count, const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
+                   float max_norm, float eps, float *norm, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Orthogonalisation of `batch` rows x cols matrices by Newton-Schulz
  * products (the update step of the Muon optimiser).  Per matrix,

@@ -11,6 +11,7 @@ built, or a call returns a nonzero status, an exception is raised.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -155,6 +156,14 @@ def load_library():
         lib.layer_norm_backward.argtypes = [ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_int,
                                             _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]
         lib.layer_norm_backward.restype = ctypes.c_int
+        lib.grad_norm_workspace_size.argtypes = [_i64, _vp]
+        lib.grad_norm_workspace_size.restype = _i64
+        lib.grad_norm.argtypes = [_i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
+        lib.grad_norm.restype = ctypes.c_int
+        lib.grad_clip.argtypes = [_i64, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp]
+        lib.grad_clip.restype = ctypes.c_int
+        lib.grad_clip_norm.argtypes = [_i64, _vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp, _i64, _vp]
+        lib.grad_clip_norm.restype = ctypes.c_int
         lib.newton_schulz_workspace_size.argtypes = [ctypes.c_int, _i64, _i64, _i64]
         lib.newton_schulz_workspace_size.restype = _i64
         lib.newton_schulz.argtypes = [ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _i64, ctypes.c_int] + \
@@ -1021,6 +1030,121 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, residual_grad=None, out=
                                    _addr(dweight), _addr(dbias), addr, nbytes,
                                    torch._C._cuda_getCurrentRawStream(device)))
     return out, dweight, dbias
+
+
+# -------------------------------------------------- gradients of a model
+
+class _TensorList:
+    """Host arrays of a list of tensors for the entry points: addresses, sizes
+    and types of each, all of one GPU and dense in memory."""
+
+    def __init__(self, tensors, what="grads", like=None):
+        tensors = list(tensors)
+        self.tensors, self.count = tensors, len(tensors)
+        if like is not None and self.count != like.count:
+            raise ValueError(f"{self.count} tensors in {what} for {like.count} gradients")
+        self.device = _device_of(*tensors) if tensors else None
+        if like is None:
+            types = []
+            for t in tensors:
+                kind = _TYPE_OF_DTYPE.get(t.dtype)
+                if kind is None:
+                    raise TypeError(f"{what} must be bfloat16, float16 or float32, not {t.dtype}")
+                if not t.is_contiguous() and not _dense(t):
+                    raise ValueError(f"{what} must lie densely in memory")
+                types.append(kind)
+            self.types = array.array("i", types)
+            self.sizes = array.array("q", [t.numel() for t in tensors])
+        else:
+            for t, g in zip(tensors, like.tensors):
+                if t.dtype is not g.dtype or t.shape != g.shape:
+                    raise ValueError(f"a tensor of {what} differs from its gradient in shape or dtype")
+                if t.stride() != g.stride() and not (t.is_contiguous() and g.is_contiguous()):
+                    raise ValueError(f"a tensor of {what} is laid out otherwise than its gradient")
+        self.data = array.array("q", [t.data_ptr() for t in tensors])
+
+
+def _dense(t) -> bool:
+    """Whether t's values fill one run of memory, in whatever order."""
+    expected = 1
+    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n != 1), key=lambda p: p[1]):
+        if stride != expected:
+            return False
+        expected *= size
+    return True
+
+
+def _at(a: array.array) -> int | None:
+    return a.buffer_info()[0] if len(a) else None
+
+
+def grad_norm(grads, out=None, stream=None):
+    """A one-element float32 tensor with the 2-norm over all values of the
+    tensors (bfloat16, float16 or float32, mixed as they come; any shapes, dense
+    in memory); written to ``out`` if given.  A tensor that is listed twice
+    counts twice."""
+    g = _TensorList(grads)
+    if g.count == 0:
+        raise ValueError("the norm of no tensors has no device")
+    if _elsewhere(stream, g.device):
+        with _placed(stream, g.device):
+            return grad_norm(g.tensors, out)
+    lib = load_library()
+    out = _norm_of(out, g)
+    ws, addr, nbytes = _workspace(out, lib.grad_norm_workspace_size(g.count, _at(g.sizes)))
+    _check(lib.grad_norm(g.count, _at(g.data), _at(g.sizes), _at(g.types), out.data_ptr(), addr, nbytes,
+                         torch._C._cuda_getCurrentRawStream(g.device)))
+    return out
+
+
+def _norm_of(norm, g: _TensorList):
+    if norm is None:
+        return torch.empty(1, dtype=torch.float32, device=g.tensors[0].device)
+    if norm.numel() != 1 or norm.dtype is not torch.float32 or _device_of(norm) != g.device:
+        raise TypeError("the norm is one float32 value on the gradients' GPU")
+    return norm
+
+
+def clip_grads(grads, norm, max_norm, eps=1e-6, out=None, stream=None):
+    """Multiplies the tensors by min(1, max_norm / (norm + eps)), with ``norm`` on
+    the GPU (from ``grad_norm``, or joined from several shards'), in place or
+    into the tensors of ``out``; returns those written.  No tensor to be written
+    may overlap another."""
+    g = _TensorList(grads)
+    if g.count == 0:
+        return [] if out is None else out
+    if _elsewhere(stream, g.device):
+        with _placed(stream, g.device):
+            return clip_grads(g.tensors, norm, max_norm, eps, out)
+    if norm is None:
+        raise TypeError("clip_grads needs the norm")
+    o = g if out is None else _TensorList(out, "out", g)
+    if o.device != g.device:
+        raise ValueError(f"out on cuda:{o.device}, gradients on cuda:{g.device}")
+    _check(load_library().grad_clip(g.count, _at(g.data), _at(o.data), _at(g.sizes), _at(g.types),
+                                    _norm_of(norm, g).data_ptr(), max_norm, eps,
+                                    torch._C._cuda_getCurrentRawStream(g.device)))
+    return o.tensors
+
+
+def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
+    """``grad_norm`` and ``clip_grads`` in one call; returns the norm before
+    clipping (a one-element float32 tensor)."""
+    g = _TensorList(grads)
+    if g.count == 0:
+        raise ValueError("the norm of no tensors has no device")
+    if _elsewhere(stream, g.device):
+        with _placed(stream, g.device):
+            return clip_grad_norm(g.tensors, max_norm, eps, out)
+    lib = load_library()
+    o = g if out is None else _TensorList(out, "out", g)
+    if o.device != g.device:
+        raise ValueError(f"out on cuda:{o.device}, gradients on cuda:{g.device}")
+    norm = _norm_of(None, g)
+    ws, addr, nbytes = _workspace(norm, lib.grad_norm_workspace_size(g.count, _at(g.sizes)))
+    _check(lib.grad_clip_norm(g.count, _at(g.data), _at(o.data), _at(g.sizes), _at(g.types), max_norm, eps,
+                              norm.data_ptr(), addr, nbytes, torch._C._cuda_getCurrentRawStream(g.device)))
+    return norm
 
 
 # ---------------------------------------------------------- Newton-Schulz

@@ -181,6 +181,7 @@ extern "C" const char* gemm_f32_status_string(int status) {
         case GEMM_F32_ERR_INVALID_EPILOGUE:
             return "epilogue field not taken in this mode: bias goes with gradient 0, bias_grad with gradient 1";
         case GEMM_F32_ERR_INVALID_SCALAR: return "eps, a coefficient or a step count out of range";
+        case GEMM_F32_ERR_OVERLAP: return "an output overlaps another tensor";
         default: return "unknown status";
     }
 }
