@@ -535,6 +535,30 @@ int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, int64_t N, in
                         void *C, int64_t ldc, const gemm_epilogue *epilogue,
                         void *workspace, int64_t workspace_bytes, void *stream);
 
+/* The layer's forward pass with a weight held in 4 bits, for a decoder's few
+ * rows: the product of gemm_mixed_epilogue (op_b T) with
+ *   W[n][k] = scales[n][k / group] (q[n][k] - zeros[n][k / group])
+ * which is never formed: whole numbers meet A in the matrix units, and a group's
+ * binary32 sum meets the scale.
+ *   format     of A, scales and zeros (16-bit values)
+ *   Q          N rows of (K + 1) / 2 bytes: q[n][k], 0 .. 15, in the low half of
+ *              byte n*ldq + k / 2 for an even k, in the high half for an odd
+ *              one; any alignment, ldq >= max(1, (K + 1) / 2)
+ *   group      k per scale: 32, 64 or a multiple of 128 (a whole row's: any
+ *              multiple not below K); the last group may be cut off by K
+ *   scales     N rows of ceil(K / group), ld_scales >= max(1, that)
+ *   zeros      likewise, any values; or NULL: 8 throughout
+ *   epilogue   forward mode only
+ * Any number of rows is taken; the weight is expanded once for every 64 of
+ * them, so that past a few hundred a 16-bit weight is the better choice.  Sums
+ * are binary32, of x (16 + q) with 16 + zero times the sum of x taken off: their
+ * error is that of a sum whose terms are up to four times as large.  For the
+ * same reason an infinity in A gives NaN.  No workspace; the rest as for
+ * gemm_mixed_epilogue. */
+int gemm_w4_epilogue(int format, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint8_t* Q,
+                     int64_t ldq, int64_t group, const uint16_t* scales, int64_t ld_scales, const uint16_t* zeros,
+                     int64_t ld_zeros, void* C, int64_t ldc, const gemm_epilogue* epilogue, void* stream);
+
 /* The gradient mode without a product, for a gradient dY that is already
  * there: dZ = dY * act'(Z), and the bias gradient, dZ's column sums.
  *   format      GEMM_MIXED_BF16 or GEMM_MIXED_F16, of dY, preact and dZ

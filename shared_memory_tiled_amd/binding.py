@@ -128,6 +128,8 @@ def load_library():
         lib.gemm_mixed_epilogue_workspace_size.restype = _i64
         lib.gemm_mixed_epilogue.argtypes = esig + [_vp, _i64, ep, _vp, _i64, _vp]
         lib.gemm_mixed_epilogue.restype = ctypes.c_int
+        lib.gemm_w4_epilogue.argtypes = [ctypes.c_int] + [_i64] * 3 + [_vp, _i64] * 2 + [_i64] + [_vp, _i64] * 3 + [ep, _vp]
+        lib.gemm_w4_epilogue.restype = ctypes.c_int
         lib.activation_grad_workspace_size.argtypes = [_i64, _i64]
         lib.activation_grad_workspace_size.restype = _i64
         lib.activation_grad.argtypes = [ctypes.c_int, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
@@ -690,6 +692,56 @@ def linear(X, W, bias=None, activation="none", residual=None, out=None, out_dtyp
         ep.preact = preact.data_ptr()
         ep.ld_preact = N or 1
     _linear_call(fmt, oa, ob, M, N, K, X, lda, W, ldb, out, ldc, ep)
+    return (out, preact) if return_preact else out
+
+
+def linear_w4(X, Q, scales, zeros=None, group_size=128, bias=None, activation="none", residual=None, out=None,
+              out_dtype=None, return_preact=False, stream=None):
+    """act(X @ W.T + bias) + residual for a few rows X (bfloat16 or float16) and
+    a weight held in 4 bits, W[n, k] = scales[n, k // group_size] * (q[n, k] -
+    zeros[n, k // group_size]).
+
+    X is M x K; Q is uint8, N x ceil(K / 2), q[n, k] in the low half of a byte
+    for an even k and in the high half for the next one; ``scales`` and ``zeros``
+    have X's dtype, N x ceil(K / group_size); without ``zeros`` they are 8.
+    ``group_size`` is 32, 64 or a multiple of 128.  The rest as for
+    ``linear``."""
+    device = _device_of(X, Q, scales, zeros, bias, residual, out)
+    if _elsewhere(stream, device):
+        with _placed(stream, device):
+            return linear_w4(X, Q, scales, zeros, group_size, bias, activation, residual, out, out_dtype, return_preact)
+    fmt = _FORMAT_OF_DTYPE.get(X.dtype)
+    if fmt is None or X.dim() != 2:
+        raise TypeError("X must be a 2-D bfloat16 or float16 tensor")
+    if Q.dim() != 2 or Q.dtype is not torch.uint8:
+        raise TypeError("Q must be a 2-D tensor of uint8")
+    if group_size != 32 and group_size != 64 and (group_size < 128 or group_size % 128):
+        raise ValueError(f"group_size is 32, 64 or a multiple of 128, not {group_size}")
+    M, K = X.shape
+    N, ldx = Q.shape[0], _row_major(X, "X")
+    if Q.shape[1] != (K + 1) // 2:
+        raise ValueError(f"Q has {Q.shape[1]} bytes a row, not {(K + 1) // 2}")
+    groups = -(-K // group_size)
+    ldq, lds = _row_major(Q, "Q"), _matrix(scales, "scales", N, groups, X.dtype)
+    ldz = 0 if zeros is None else _matrix(zeros, "zeros", N, groups, X.dtype)
+    out, ldc = _output(out, out_dtype, X, M, N)
+    ep = Epilogue(_TYPE_OF_DTYPE[out.dtype], _activation(activation))
+    if bias is not None:
+        _vector(bias, "bias", N, (X.dtype, torch.float32))
+        ep.bias_type = _TYPE_OF_DTYPE[bias.dtype]
+        ep.bias = bias.data_ptr()
+    if residual is not None:
+        ep.ld_residual = _matrix(residual, "residual", M, N, out.dtype)
+        ep.residual = residual.data_ptr()
+    preact = None
+    if return_preact:
+        preact = X.new_empty((M, N))
+        ep.preact = preact.data_ptr()
+        ep.ld_preact = N or 1
+    _check(load_library().gemm_w4_epilogue(
+        fmt, M, N, K, X.data_ptr(), ldx, Q.data_ptr(), ldq, group_size, scales.data_ptr(), lds,
+        None if zeros is None else zeros.data_ptr(), ldz, out.data_ptr(), ldc, ctypes.byref(ep),
+        torch._C._cuda_getCurrentRawStream(device)))
     return (out, preact) if return_preact else out
 
 

@@ -5,6 +5,7 @@
 #include "gemm_f32.h"
 #include "api_checks.h"
 #include "launch.h"
+#include "linear_w4.h"
 
 #include <limits.h>
 #include <math.h>
@@ -52,6 +53,57 @@ extern "C" int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, in
     if (st != GEMM_F32_OK) return st;
     if ((st = check_device()) != GEMM_F32_OK) return st;
     return finish(launch_linear(p, e, s, format, op_a, op_b, workspace));
+}
+
+// ----------------------------------------- the product with a 4-bit weight
+
+namespace {
+
+int check_w4(int format, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint8_t* Q,
+             int64_t ldq, int64_t group, const uint16_t* scales, int64_t ld_scales, const uint16_t* zeros,
+             int64_t ld_zeros, int64_t ldc, const gemm_epilogue* ep) {
+    // the checks of a 16-bit product, whose weight is not looked at
+    const int st = check_linear(GEMM_F32_OP_N, GEMM_F32_OP_T, format, M, N, K, A, lda, A, at_least_one(K), ldc, ep);
+    if (st != GEMM_F32_OK) return st;
+    if (ep->gradient != 0) return GEMM_F32_ERR_INVALID_EPILOGUE;
+    if (group != 32 && group != 64 && (group < 128 || group % 128 != 0)) return GEMM_F32_ERR_INVALID_DIM;
+    if (group > INT_MAX) return GEMM_F32_ERR_TOO_LARGE;
+    const int64_t bytes = K / 2 + K % 2, groups = K / group + (K % group != 0);
+    if (ldq < at_least_one(bytes) || ld_scales < at_least_one(groups) ||
+        (zeros != nullptr && ld_zeros < at_least_one(groups)))
+        return GEMM_F32_ERR_INVALID_LD;
+    if (M == 0 || N == 0) return GEMM_F32_OK;
+    if (K > 0 && (Q == nullptr || scales == nullptr)) return GEMM_F32_ERR_NULL_PTR;
+    if ((((uintptr_t)scales | (uintptr_t)zeros) & 1u) != 0) return GEMM_F32_ERR_MISALIGNED;
+    if (!extent_fits(N, bytes, ldq) || !extent_fits(N, groups, ld_scales) ||
+        (zeros != nullptr && !extent_fits(N, groups, ld_zeros)))
+        return GEMM_F32_ERR_TOO_LARGE;
+    // blocks of 16 columns and up to 1024 threads, rows by 16 in the second coordinate
+    if (N > 1 << 25 || M > 65535 * 16) return GEMM_F32_ERR_TOO_LARGE;
+    return GEMM_F32_OK;
+}
+
+W4Args w4_args(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint8_t* Q, int64_t ldq,
+               int64_t group, const uint16_t* scales, int64_t ld_scales, const uint16_t* zeros, int64_t ld_zeros) {
+    return W4Args{(int)M, (int)N, (int)K, A, lda, Q, ldq, (int)group, scales, ld_scales, zeros, ld_zeros};
+}
+
+}  // namespace
+
+extern "C" int gemm_w4_epilogue(int format, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda,
+                                const uint8_t* Q, int64_t ldq, int64_t group, const uint16_t* scales,
+                                int64_t ld_scales, const uint16_t* zeros, int64_t ld_zeros, void* C, int64_t ldc,
+                                const gemm_epilogue* epilogue, void* stream) {
+    int st = check_w4(format, M, N, K, A, lda, Q, ldq, group, scales, ld_scales, zeros, ld_zeros, ldc, epilogue);
+    if (st != GEMM_F32_OK) return st;
+    if (M == 0 || N == 0) return GEMM_F32_OK;
+    if (C == nullptr) return GEMM_F32_ERR_NULL_PTR;
+    if (misaligned_type(C, epilogue->c_type)) return GEMM_F32_ERR_MISALIGNED;
+    if (other_matrix(C, ldc, epilogue->residual, epilogue->ld_residual, M)) return GEMM_F32_ERR_INVALID_LD;
+    if ((st = check_device()) != GEMM_F32_OK) return st;
+    return finish(launch_linear_w4(w4_args(M, N, K, A, lda, Q, ldq, group, scales, ld_scales, zeros, ld_zeros),
+                                   epilogue_args(format, M, N, C, ldc, epilogue), reinterpret_cast<hipStream_t>(stream),
+                                   format));
 }
 
 extern "C" int64_t activation_grad_workspace_size(int64_t M, int64_t N) {
