@@ -10,7 +10,7 @@
 #include "mfma16_common.h"
 #include "staged_tile.h"
 
-#include <limits.h>
+#include <math.h>
 
 namespace gemmf32 {
 
@@ -172,24 +172,117 @@ void grouped_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_n, in
     Core::finish(acc, e, BT * r.tm, BT * r.tn, lds);
 }
 
-// The weights' gradient: group blockIdx.x / tiles, whose tiles the XCDs share
-// (groups differ in their rows, so whole groups to an XCD would not balance).
 template <int FMT, int BT>
 __global__ __launch_bounds__(256)
 void grouped_grad_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, int group_m) {
     using Core = GroupedCore<FMT, false, false, BT>;
     __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
-    const int tiles = tiles_m * tiles_n, g = (int)blockIdx.x / tiles;
-    int tm, tn, begin, end;
-    grouped_tile((int)blockIdx.x - g * tiles, tiles_m, tiles_n, group_m, &tm, &tn);
-    group_range(a, g, &begin, &end);
-    p.A += (int64_t)begin * p.lda;
-    p.B += (int64_t)begin * p.ldb;
-    p.K = end - begin;
-    e.C = static_cast<char*>(e.C) + (e.c_type == 2 ? 4 : 2) * (g * a.stride_b);
+    const GroupRows r = locate_grad_tile(a, (int)blockIdx.x, tiles_m, tiles_n, group_m);
+    enter_grad_group(a, r, &p, &e);
     floatx4 acc[Core::F][Core::F];
-    Core::run(p, BT * tm, BT * tn, lds, acc);
-    Core::finish(acc, e, BT * tm, BT * tn, lds);
+    Core::run(p, BT * r.tm, BT * r.tn, lds, acc);
+    Core::finish(acc, e, BT * r.tm, BT * r.tn, lds);
+}
+
+template <int BT>
+hipError_t launch_any(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
+                      int op_b) {
+    const int tn = ceil_div(p.N, BT);
+    const dim3 grid((unsigned)(grouped_row_tiles(a.rows, a.groups, BT) * tn)), b(256);
+    if (format == 0 && op_b) hipLaunchKernelGGL((grouped_kernel<0, true, BT>), grid, b, 0, s, a, p, e, tn, 8);
+    else if (format == 0) hipLaunchKernelGGL((grouped_kernel<0, false, BT>), grid, b, 0, s, a, p, e, tn, 8);
+    else if (op_b) hipLaunchKernelGGL((grouped_kernel<1, true, BT>), grid, b, 0, s, a, p, e, tn, 8);
+    else hipLaunchKernelGGL((grouped_kernel<1, false, BT>), grid, b, 0, s, a, p, e, tn, 8);
+    return hipGetLastError();
+}
+
+template <int BT>
+hipError_t launch_grad_any(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format) {
+    const int tm = ceil_div(p.M, BT), tn = ceil_div(p.N, BT);
+    const dim3 grid((unsigned)(tm * tn * a.groups)), b(256);
+    if (format == 0) hipLaunchKernelGGL((grouped_grad_kernel<0, BT>), grid, b, 0, s, a, p, e, tm, tn, 8);
+    else hipLaunchKernelGGL((grouped_grad_kernel<1, BT>), grid, b, 0, s, a, p, e, tm, tn, 8);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------- choice of kernel
+
+// A factor of `rows` rows whose copies' 32-bit offsets hold, a tile's
+// overhang included.
+bool offsets_hold(int64_t rows, int64_t ld) { return ld < (1ll << 30) / (rows + 256); }
+bool even_base(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// Whether the scheduled tiles take the product.
+bool scheduled_fits(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
+    return p.K > 0 && p.K % 2 == 0 && p.lda % 2 == 0 && p.ldb % 2 == 0 && a.stride_b % 2 == 0 && (op_b || p.N % 2 == 0) &&
+           even_base(p.A) && even_base(p.B) && offsets_hold(256, p.lda) && offsets_hold(op_b ? p.N : p.K, p.ldb);
+}
+bool scheduled_grad_fits(const GroupedArgs& a, const Gemm16Args& p) {
+    return p.lda % 2 == 0 && p.ldb % 2 == 0 && p.M % 2 == 0 && p.N % 2 == 0 && even_base(p.A) && even_base(p.B) &&
+           offsets_hold(a.rows, p.lda) && offsets_hold(a.rows, p.ldb);
+}
+
+// Estimated time of a launch on `tile` x `tile` tiles, in us: `row_tiles` x
+// `col_tiles` of them, `phases` steps of 64 along K.  A round of 256 blocks takes
+// `slow` per phase once all CUs are busy (`fast` up to half of them) and `fixed`
+// for start and epilogue, as in the plain layer's estimate; how many rounds the
+// groups' sizes make is not known here, so past one round half a round is added
+// for the last one.  tile 0: the register-staged 128 x 128 tiles, two blocks to
+// a CU.
+double tile_time(int tile, double row_tiles, double col_tiles, double phases, bool known) {
+    static const struct { int tile; double fast, slow, fixed; } kCost[] = {
+        {256, 1.00, 1.38, 20.0}, {192, 0.78, 0.90, 14.0}, {160, 0.66, 0.78, 12.0},
+        {128, 0.40, 0.42, 16.0}, {64, 0.22, 0.24, 4.8},   {0, 1.40, 1.40, 9.0}};
+    for (const auto& c : kCost)
+        if (c.tile == tile) {
+            const double slots = tile == 0 ? 512.0 : 256.0, tiles = row_tiles * col_tiles;
+            const double rounds = known ? ceil(tiles / slots) : tiles <= 0.8 * slots ? 1.0 : tiles / slots + 0.5;
+            const double busy = fmin(1.0, fmax(0.0, 2.0 * tiles / slots - 1.0));
+            return rounds * ((c.fast + (c.slow - c.fast) * busy) * phases + c.fixed);
+        }
+    return 1e30;
+}
+
+// Row tiles that groups of `rows` rows on average make: each but the smallest
+// leaves half a tile on average.
+double expected_row_tiles(int groups, int rows, int tile) {
+    const double used = groups < rows ? groups : rows, each = rows / used;
+    if (groups == 1) return ceil_div(rows, tile);
+    return used * fmax(1.0, each / tile + 0.5);
+}
+
+// The tile of least estimated time, of those the problem fits; 0: any problem's.
+int pick_tile(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
+    if (!scheduled_fits(a, p, op_b)) return 0;
+    int best = 0;
+    double least = 1e30;
+    for (const int tile : {256, 192, 160, 128, 64}) {
+        if (tile <= 128 && p.K % 8 != 0) continue;
+        const double t = tile_time(tile, expected_row_tiles(a.groups, a.rows, tile), ceil_div(p.N, tile),
+                                   ceil_div(p.K, 64), a.groups == 1);
+        if (t < least) {
+            least = t;
+            best = tile;
+        }
+    }
+    return best;
+}
+
+// The same for the weights' gradient, whose depth is a group's rows.
+int pick_grad_tile(const GroupedArgs& a, const Gemm16Args& p) {
+    if (!scheduled_grad_fits(a, p)) return 0;
+    int best = 0;
+    double least = 1e30;
+    for (const int tile : {256, 192, 160, 128, 64, 0}) {
+        const int side = tile == 0 ? 128 : tile;
+        const double t = tile_time(tile, (double)a.groups * ceil_div(p.M, side), ceil_div(p.N, side),
+                                   fmax(1.0, a.rows / 64.0 / a.groups), true);
+        if (t < least) {
+            least = t;
+            best = tile;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -198,30 +291,28 @@ int64_t grouped_workspace(const GroupedArgs&, const Gemm16Args&, const EpilogueA
 
 hipError_t launch_grouped(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
                           int op_b, void*) {
-    constexpr int BT = 128;
-    const int tn = ceil_div(p.N, BT);
-    const int64_t blocks = grouped_row_tiles(a.rows, a.groups, BT) * tn;
-    if (blocks > 0x7FFFFFFFll / 256) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), b(256);
-    if (format == 0 && op_b) hipLaunchKernelGGL((grouped_kernel<0, true, BT>), grid, b, 0, s, a, p, e, tn, 8);
-    else if (format == 0) hipLaunchKernelGGL((grouped_kernel<0, false, BT>), grid, b, 0, s, a, p, e, tn, 8);
-    else if (op_b) hipLaunchKernelGGL((grouped_kernel<1, true, BT>), grid, b, 0, s, a, p, e, tn, 8);
-    else hipLaunchKernelGGL((grouped_kernel<1, false, BT>), grid, b, 0, s, a, p, e, tn, 8);
-    return hipGetLastError();
+    switch (pick_tile(a, p, op_b)) {
+        case 256: return launch_grouped_wide256(a, p, e, s, format, op_b);
+        case 192: return launch_grouped_wide192(a, p, e, s, format, op_b);
+        case 160: return launch_grouped_wide160(a, p, e, s, format, op_b);
+        case 128: return launch_grouped_ksplit128(a, p, e, s, format, op_b);
+        case 64: return launch_grouped_ksplit(a, p, e, s, format, op_b);
+        default: return launch_any<128>(a, p, e, s, format, op_b);
+    }
 }
 
 int64_t grouped_grad_workspace(const GroupedArgs&, const Gemm16Args&, const EpilogueArgs&) { return 0; }
 
 hipError_t launch_grouped_grad(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
                                int format, void*) {
-    constexpr int BT = 128;
-    const int tm = ceil_div(p.M, BT), tn = ceil_div(p.N, BT);
-    const int64_t blocks = (int64_t)tm * tn * a.groups;
-    if ((int64_t)tm * tn > 0x7FFFFFFFll / 256 || blocks > 0x7FFFFFFFll / 256) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), b(256);
-    if (format == 0) hipLaunchKernelGGL((grouped_grad_kernel<0, BT>), grid, b, 0, s, a, p, e, tm, tn, 8);
-    else hipLaunchKernelGGL((grouped_grad_kernel<1, BT>), grid, b, 0, s, a, p, e, tm, tn, 8);
-    return hipGetLastError();
+    switch (pick_grad_tile(a, p)) {
+        case 256: return launch_grouped_grad_wide256(a, p, e, s, format);
+        case 192: return launch_grouped_grad_wide192(a, p, e, s, format);
+        case 160: return launch_grouped_grad_wide160(a, p, e, s, format);
+        case 128: return launch_grouped_grad_ksplit128(a, p, e, s, format);
+        case 64: return launch_grouped_grad_ksplit(a, p, e, s, format);
+        default: return launch_grad_any<128>(a, p, e, s, format);
+    }
 }
 
 // --------------------------------------------- the activation's gradient

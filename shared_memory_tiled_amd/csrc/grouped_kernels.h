@@ -8,7 +8,7 @@
 // clamps: whatever they hold, no row outside the matrices is touched.
 #pragma once
 
-#include "launch.h"
+#include "mfma16_common.h"
 
 namespace gemmf32 {
 
@@ -119,8 +119,53 @@ __device__ __forceinline__ void enter_group(const GroupedArgs& a, const GroupRow
         e->bias = static_cast<const char*>(e->bias) + (e->bias_type == 2 ? 4 : 2) * (r.group * a.ld_bias);
 }
 
+// The weights' gradient: block b's group and tile.  The tiles of a group are
+// shared by the XCDs: groups differ in their rows, so whole groups to an XCD
+// would not balance.
+__device__ __forceinline__ GroupRows locate_grad_tile(const GroupedArgs& a, int b, int tiles_m, int tiles_n, int group_m) {
+    const int tiles = tiles_m * tiles_n;
+    GroupRows r;
+    r.group = b / tiles;
+    grouped_tile(b - r.group * tiles, tiles_m, tiles_n, group_m, &r.tm, &r.tn);
+    int end;
+    group_range(a, r.group, &r.begin, &end);
+    r.rows = end - r.begin;
+    return r;
+}
+__device__ __forceinline__ void enter_grad_group(const GroupedArgs& a, const GroupRows& r, Gemm16Args* p, EpilogueArgs* e) {
+    p->A += (int64_t)r.begin * p->lda;
+    p->B += (int64_t)r.begin * p->ldb;
+    p->K = r.rows;
+    e->C = static_cast<char*>(e->C) + (e->c_type == 2 ? 4 : 2) * (r.group * a.stride_b);
+}
+
 }  // namespace
 #endif
+
+// The tiles on the scheduled K loops: 256, 192 and 160 (any even K; for the
+// gradient any rows), 128 and 64 whose waves split K (K a multiple of 8; any
+// rows).  Widths, leading dimensions and strides even, bases on 4 bytes, a
+// group's operands within the copies' offsets; the caller checks.
+hipError_t launch_grouped_wide256(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                  int format, int op_b);
+hipError_t launch_grouped_wide192(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                  int format, int op_b);
+hipError_t launch_grouped_wide160(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                  int format, int op_b);
+hipError_t launch_grouped_ksplit128(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                    int format, int op_b);
+hipError_t launch_grouped_ksplit(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                 int format, int op_b);
+hipError_t launch_grouped_grad_wide256(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                       int format);
+hipError_t launch_grouped_grad_wide192(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                       int format);
+hipError_t launch_grouped_grad_wide160(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                       int format);
+hipError_t launch_grouped_grad_ksplit128(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e,
+                                         hipStream_t s, int format);
+hipError_t launch_grouped_grad_ksplit(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                      int format);
 
 // p: A, B, N, K and their leading dimensions (M is not used); e: M is not used.
 int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, int op_b);
