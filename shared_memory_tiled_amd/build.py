@@ -33,7 +33,7 @@ FLAGS = ["-O3", f"--offload-arch={ARCH}", "-std=c++17", "-fPIC", "-Wall",
 # allocator copied every accumulator before each matrix instruction of that
 # kernel.
 EXTRA_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]
-               for src in ("mfma16_ksplit.hip", "newton_schulz_ksplit.hip", "linear_ksplit.hip", "grouped_ksplit.hip")}
+               for src in ("mfma16_ksplit.hip", "newton_schulz_ksplit.hip", "linear_ksplit.hip")}
 
 
 def _compile(src: str, resource_usage: bool) -> str:

@@ -17,6 +17,9 @@ namespace gemmf32 {
 namespace {
 
 // ------------------------------------------------------ tiles for any problem
+//
+// For what the copied tiles do not take: odd widths, leading dimensions or
+// bases, K no multiple of 8, operands past 2 GiB.
 
 // A tile of T rows of a factor, 64 deep, as 16-bit values in LDS: loaded by
 // 256 threads in runs of 8 that go through registers, so any alignment and
@@ -212,107 +215,218 @@ hipError_t launch_grad_any(const GroupedArgs& a, const Gemm16Args& p, const Epil
 bool offsets_hold(int64_t rows, int64_t ld) { return ld < (1ll << 30) / (rows + 256); }
 bool even_base(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-// Whether the scheduled tiles take the product.
-bool scheduled_fits(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
-    return p.K > 0 && p.K % 2 == 0 && p.lda % 2 == 0 && p.ldb % 2 == 0 && a.stride_b % 2 == 0 && (op_b || p.N % 2 == 0) &&
+// Whether the copied tiles (grouped_shared.hip) take the product.
+bool shared_fits(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
+    return p.K > 0 && p.K % 8 == 0 && p.lda % 2 == 0 && p.ldb % 2 == 0 && a.stride_b % 2 == 0 && (op_b || p.N % 2 == 0) &&
            even_base(p.A) && even_base(p.B) && offsets_hold(256, p.lda) && offsets_hold(op_b ? p.N : p.K, p.ldb);
 }
-bool scheduled_grad_fits(const GroupedArgs& a, const Gemm16Args& p) {
+bool shared_grad_fits(const GroupedArgs& a, const Gemm16Args& p) {
     return p.lda % 2 == 0 && p.ldb % 2 == 0 && p.M % 2 == 0 && p.N % 2 == 0 && even_base(p.A) && even_base(p.B) &&
            offsets_hold(a.rows, p.lda) && offsets_hold(a.rows, p.ldb);
 }
 
-// Estimated time of a launch on `tile` x `tile` tiles, in us: `row_tiles` x
-// `col_tiles` of them, `phases` steps of 64 along K.  A round of 256 blocks takes
-// `slow` per phase once all CUs are busy (`fast` up to half of them) and `fixed`
-// for start and epilogue, as in the plain layer's estimate; how many rounds the
-// groups' sizes make is not known here, so past one round half a round is added
-// for the last one.  tile 0: the register-staged 128 x 128 tiles, two blocks to
-// a CU.
-double tile_time(int tile, double row_tiles, double col_tiles, double phases, bool known) {
-    static const struct { int tile; double fast, slow, fixed; } kCost[] = {
-        {256, 1.00, 1.38, 20.0}, {192, 0.78, 0.90, 14.0}, {160, 0.66, 0.78, 12.0},
-        {128, 0.40, 0.42, 16.0}, {64, 0.22, 0.24, 4.8},   {0, 1.40, 1.40, 9.0}};
-    for (const auto& c : kCost)
-        if (c.tile == tile) {
-            const double slots = tile == 0 ? 512.0 : 256.0, tiles = row_tiles * col_tiles;
-            const double rounds = known ? ceil(tiles / slots) : tiles <= 0.8 * slots ? 1.0 : tiles / slots + 0.5;
-            const double busy = fmin(1.0, fmax(0.0, 2.0 * tiles / slots - 1.0));
-            return rounds * ((c.fast + (c.slow - c.fast) * busy) * phases + c.fixed);
-        }
-    return 1e30;
-}
+// Groups that have a row, if every row chooses one with the same chance.
+double used_groups(int groups, int rows) { return groups * (1.0 - pow(1.0 - 1.0 / groups, rows)); }
 
-// Row tiles that groups of `rows` rows on average make: each but the smallest
-// leaves half a tile on average.
+// Row tiles that the groups make on average: each group leaves half a tile.
 double expected_row_tiles(int groups, int rows, int tile) {
-    const double used = groups < rows ? groups : rows, each = rows / used;
     if (groups == 1) return ceil_div(rows, tile);
-    return used * fmax(1.0, each / tile + 0.5);
+    const double used = used_groups(groups, rows);
+    return used * fmax(1.0, rows / used / tile + 0.5);
 }
 
-// The tile of least estimated time, of those the problem fits; 0: any problem's.
-int pick_tile(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
-    if (!scheduled_fits(a, p, op_b)) return 0;
-    int best = 0;
-    double least = 1e30;
-    for (const int tile : {256, 192, 160, 128, 64}) {
-        if (tile <= 128 && p.K % 8 != 0) continue;
-        const double t = tile_time(tile, expected_row_tiles(a.groups, a.rows, tile), ceil_div(p.N, tile),
-                                   ceil_div(p.K, 64), a.groups == 1);
-        if (t < least) {
-            least = t;
-            best = tile;
-        }
-    }
-    return best;
+// Estimated time of `tiles` tiles of `phases` steps of 32 k, in us.  A block
+// alone on a CU takes `alone` per phase, which is the memory's latency over the
+// stages in flight; with `slots` of them on the chip (two or three to a CU) a
+// round of them takes `full` per phase; and `fixed` for start and epilogue.  How
+// many rounds the groups' rows make is not known here: past one, half a round
+// more for the last.  (4096^3 in one group: 121 us on 128 x 256 tiles, 157 on 128
+// x 128, 157 on 64 x 256, 185 on 64 x 128; 1024 x 1024 x 1024 in 16 groups: 28 /
+// 19 / 19 / 15.)
+struct Shape {
+    int bm, bn, slots;
+    double alone, full, fixed;
+};
+constexpr Shape kShapes[] = {
+    {128, 256, 512, 0.45, 0.84, 13.5}, {128, 128, 768, 0.43, 0.875, 5.1}, {64, 256, 512, 0.45, 0.575, 5.0},
+    {64, 128, 768, 0.305, 0.50, 5.0}};
+double tiles_time(const Shape& c, double tiles, double phases) {
+    if (tiles > c.slots) return (tiles / c.slots + 0.5) * (c.full * phases + c.fixed);
+    const double busy = fmax(0.0, (tiles - 256.0) / (c.slots - 256.0));
+    return (c.alone + (c.full - c.alone) * busy) * phases + c.fixed;
 }
 
-// The same for the weights' gradient, whose depth is a group's rows.
-int pick_grad_tile(const GroupedArgs& a, const Gemm16Args& p) {
-    if (!scheduled_grad_fits(a, p)) return 0;
-    int best = 0;
+// The pass over `splits` planes of `values`, from 4 us, at 3 TB/s.
+double pass_time(int splits, double values) { return 4.0 + 4.0 * splits * values / 3e6; }
+
+struct Plan {
+    bool shared;
+    int bm, bn;
+    int splits, k_share;               // blocks along K; k of each
+    int64_t bytes;                     // of planes, if split
+};
+
+Plan make_plan(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
+    Plan q{};
+    q.splits = 1;
+    q.k_share = p.K;
+    if (!shared_fits(a, p, op_b)) return q;
+    q.shared = true;
+    const int phases = ceil_div(p.K, 32);
     double least = 1e30;
-    for (const int tile : {256, 192, 160, 128, 64, 0}) {
-        const int side = tile == 0 ? 128 : tile;
-        const double t = tile_time(tile, (double)a.groups * ceil_div(p.M, side), ceil_div(p.N, side),
-                                   fmax(1.0, a.rows / 64.0 / a.groups), true);
-        if (t < least) {
-            least = t;
-            best = tile;
+    for (const Shape& c : kShapes) {
+        const double tiles = expected_row_tiles(a.groups, a.rows, c.bm) * ceil_div(p.N, c.bn);
+        for (int splits = 1; splits <= 16 && (splits == 1 || (tiles * splits <= c.slots && phases >= 8 * splits)); splits *= 2) {
+            const double t = tiles_time(c, tiles * splits, (double)phases / splits) +
+                             (splits > 1 ? pass_time(splits, (double)a.rows * p.N) : 0.0);
+            if (t < least) {
+                least = t;
+                q.bm = c.bm;
+                q.bn = c.bn;
+                q.k_share = splits > 1 ? 32 * ceil_div(phases, splits) : p.K;
+                q.splits = ceil_div(p.K, q.k_share);
+            }
         }
     }
-    return best;
+    if (q.splits > 1) q.bytes = 4 * (int64_t)q.splits * a.rows * p.N;
+    return q;
+}
+
+// The weights' gradient: 128 x 256 tiles from two rounds of them on (8192 x 2048
+// x 4096 over 16 groups 196 us against 208; 16384 x 4096 x 4096 over 8 498 against
+// 553), 128 x 128 below; few tiles with long groups split the rows.
+Plan make_grad_plan(const GroupedArgs& a, const Gemm16Args& p) {
+    Plan q{};
+    q.splits = 1;
+    if (!shared_grad_fits(a, p)) return q;
+    q.shared = true;
+    q.bm = 128;
+    const int64_t wide = (int64_t)a.groups * ceil_div(p.M, 128) * ceil_div(p.N, 256);
+    q.bn = wide >= 1024 ? 256 : 128;
+    if (q.bn == 256) return q;
+    const double tiles = (double)a.groups * ceil_div(p.M, 128) * ceil_div(p.N, 128);
+    const double phases = ceil(a.rows / used_groups(a.groups, a.rows > 0 ? a.rows : 1) / 32.0);
+    double least = 1e30;
+    for (int splits = 1; splits <= 32 && (splits == 1 || (tiles * splits <= 768 && phases >= 8 * splits)); splits *= 2) {
+        const double t = tiles_time(kShapes[1], tiles * splits, phases / splits) +
+                         (splits > 1 ? pass_time(splits, (double)a.groups * p.M * p.N) : 0.0);
+        if (t < least) {
+            least = t;
+            q.splits = splits;
+        }
+    }
+    if (q.splits > 1) q.bytes = 4 * (int64_t)q.splits * a.groups * p.M * p.N;
+    return q;
+}
+
+// ------------------------------------------- passes over a split K's planes
+
+// W values at `at` of each plane, added in order, four loads in flight.
+template <int W>
+__device__ __forceinline__ void add_planes(const float* planes, int count, int64_t plane, int64_t at, int valid, float (&v)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = 0.0f;
+    for (int q = 0; q < count; q += 4) {
+        float u[4][W];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (q + k < count) load_values<2>(planes + (q + k) * plane, at, valid, u[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (q + k < count) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[i] += u[k][i];
+            }
+    }
+}
+
+// The layer's epilogue over the planes' sums: 16 rows of one group x 128 columns
+// to a block, a run of 4 columns of two rows to a thread.
+constexpr int kPassRows = 16;
+__global__ __launch_bounds__(256)
+void grouped_pass_kernel(GroupedArgs a, EpilogueArgs e, int tiles_n, const float* planes, int count, int64_t plane) {
+    const GroupRows r = locate_group_tile<kPassRows>(a, (int)blockIdx.x, tiles_n, 1);
+    if (r.rows < 0) return;
+    Gemm16Args p{};
+    enter_group(a, r, &p, &e);
+    const int col = 128 * r.tn + 4 * (threadIdx.x & 31);
+    if (col >= e.N) return;
+    float bias[4];
+    load_bias(e, col, bias);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = kPassRows * r.tm + (threadIdx.x >> 5) + 8 * h;
+        if (row >= e.M) return;
+        EpilogueRun<4, false> run;
+        run.load(e, row, col);
+        float v[4];
+        add_planes(planes, count, plane, (int64_t)(r.begin + row) * e.N + col, e.N - col, v);
+        run.finish(e, row, col, bias, v);
+    }
+}
+
+// The gradients of all groups: rows are groups x M, 8 of them x 128 columns to a
+// block.
+__global__ __launch_bounds__(256)
+void grouped_grad_pass_kernel(EpilogueArgs e, int64_t stride_c, int64_t rows, const float* planes, int count, int64_t plane) {
+    const int64_t i = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int col = 128 * blockIdx.x + 4 * (threadIdx.x & 31);
+    if (i >= rows || col >= e.N) return;
+    float v[4];
+    add_planes(planes, count, plane, i * e.N + col, e.N - col, v);
+    const int64_t g = i / e.M;
+    store_values(e.c_type, e.C, g * stride_c + (i - g * e.M) * e.ldc + col, e.N - col, v);
 }
 
 }  // namespace
 
-int64_t grouped_workspace(const GroupedArgs&, const Gemm16Args&, const EpilogueArgs&, int) { return 0; }
-
-hipError_t launch_grouped(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
-                          int op_b, void*) {
-    switch (pick_tile(a, p, op_b)) {
-        case 256: return launch_grouped_wide256(a, p, e, s, format, op_b);
-        case 192: return launch_grouped_wide192(a, p, e, s, format, op_b);
-        case 160: return launch_grouped_wide160(a, p, e, s, format, op_b);
-        case 128: return launch_grouped_ksplit128(a, p, e, s, format, op_b);
-        case 64: return launch_grouped_ksplit(a, p, e, s, format, op_b);
-        default: return launch_any<128>(a, p, e, s, format, op_b);
-    }
+int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs&, int op_b) {
+    return make_plan(a, p, op_b).bytes;
 }
 
-int64_t grouped_grad_workspace(const GroupedArgs&, const Gemm16Args&, const EpilogueArgs&) { return 0; }
+hipError_t launch_grouped(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
+                          int op_b, void* workspace) {
+    const Plan q = make_plan(a, p, op_b);
+    if (!q.shared) return launch_any<128>(a, p, e, s, format, op_b);
+    if (q.splits == 1) return launch_grouped_shared(a, p, e, s, format, op_b, q.bm, q.bn, q.k_share, 0);
+    const int64_t plane = (int64_t)a.rows * p.N;
+    EpilogueArgs sums{};
+    sums.N = e.N;
+    sums.c_type = 2;
+    sums.C = workspace;
+    sums.ldc = p.N;
+    const hipError_t err = launch_grouped_shared(a, p, sums, s, format, op_b, q.bm, q.bn, q.k_share, plane);
+    if (err != hipSuccess) return err;
+    const int tn = ceil_div(e.N, 128);
+    hipLaunchKernelGGL(grouped_pass_kernel, dim3((unsigned)(grouped_row_tiles(a.rows, a.groups, kPassRows) * tn)), dim3(256),
+                       0, s, a, e, tn, static_cast<const float*>(workspace), q.splits, plane);
+    return hipGetLastError();
+}
+
+int64_t grouped_grad_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs&) {
+    return make_grad_plan(a, p).bytes;
+}
 
 hipError_t launch_grouped_grad(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                               int format, void*) {
-    switch (pick_grad_tile(a, p)) {
-        case 256: return launch_grouped_grad_wide256(a, p, e, s, format);
-        case 192: return launch_grouped_grad_wide192(a, p, e, s, format);
-        case 160: return launch_grouped_grad_wide160(a, p, e, s, format);
-        case 128: return launch_grouped_grad_ksplit128(a, p, e, s, format);
-        case 64: return launch_grouped_grad_ksplit(a, p, e, s, format);
-        default: return launch_grad_any<128>(a, p, e, s, format);
-    }
+                               int format, void* workspace) {
+    const Plan q = make_grad_plan(a, p);
+    if (!q.shared) return launch_grad_any<128>(a, p, e, s, format);
+    if (q.splits == 1) return launch_grouped_grad_shared(a, p, e, s, format, q.bn, 1, 0);
+    const int64_t plane = (int64_t)a.groups * p.M * p.N;
+    GroupedArgs whole = a;
+    whole.stride_b = (int64_t)p.M * p.N;
+    EpilogueArgs sums{};
+    sums.M = p.M;
+    sums.N = p.N;
+    sums.c_type = 2;
+    sums.C = workspace;
+    sums.ldc = p.N;
+    const hipError_t err = launch_grouped_grad_shared(whole, p, sums, s, format, q.bn, q.splits, plane);
+    if (err != hipSuccess) return err;
+    const int64_t rows = (int64_t)a.groups * p.M;
+    hipLaunchKernelGGL(grouped_grad_pass_kernel, dim3(ceil_div(p.N, 128), (unsigned)((rows + 7) / 8)), dim3(256), 0, s, e,
+                       a.stride_b, rows, static_cast<const float*>(workspace), q.splits, plane);
+    return hipGetLastError();
 }
 
 // --------------------------------------------- the activation's gradient

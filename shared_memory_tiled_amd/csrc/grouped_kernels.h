@@ -142,30 +142,17 @@ __device__ __forceinline__ void enter_grad_group(const GroupedArgs& a, const Gro
 }  // namespace
 #endif
 
-// The tiles on the scheduled K loops: 256, 192 and 160 (any even K; for the
-// gradient any rows), 128 and 64 whose waves split K (K a multiple of 8; any
-// rows).  Widths, leading dimensions and strides even, bases on 4 bytes, a
-// group's operands within the copies' offsets; the caller checks.
-hipError_t launch_grouped_wide256(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                  int format, int op_b);
-hipError_t launch_grouped_wide192(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                  int format, int op_b);
-hipError_t launch_grouped_wide160(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                  int format, int op_b);
-hipError_t launch_grouped_ksplit128(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                    int format, int op_b);
-hipError_t launch_grouped_ksplit(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                 int format, int op_b);
-hipError_t launch_grouped_grad_wide256(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                       int format);
-hipError_t launch_grouped_grad_wide192(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                       int format);
-hipError_t launch_grouped_grad_wide160(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                       int format);
-hipError_t launch_grouped_grad_ksplit128(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e,
-                                         hipStream_t s, int format);
-hipError_t launch_grouped_grad_ksplit(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                      int format);
+// Tiles of bm x bn (grouped_shared.hip): 128 x 256, 128 x 128, 64 x 256, 64 x
+// 128; the gradient's of 128 rows.  For bases on 4 bytes, even leading dimensions
+// and strides, even widths of the factors that are not k-contiguous, K a multiple
+// of 8 otherwise (the gradient: any rows), and operands within the copies'
+// offsets; the caller checks.  K split over blocks (k_share a multiple of 32
+// below K; splits above 1): each stores its sums as a plane of binary32 values,
+// `plane` of them after the one before, e then being the first plane.
+hipError_t launch_grouped_shared(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                 int format, int op_b, int bm, int bn, int k_share, int64_t plane);
+hipError_t launch_grouped_grad_shared(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                      int format, int bn, int splits, int64_t plane);
 
 // p: A, B, N, K and their leading dimensions (M is not used); e: M is not used.
 int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, int op_b);

@@ -1,0 +1,335 @@
+// grouped_shared.hip -- the grouped layer on tiles that share a CU with other
+// blocks: 128 x 256 and 128 x 128, 64 x 256 and 64 x 128 (GroupedSharedCore).
+//
+// The scheduled tiles own a CU: their start (the first copies' latency) and
+// their epilogue (12 to 20 us) pass with the matrix units idle, which is the
+// most of a tile's time where K is short -- a weight's gradient over an expert's
+// few hundred rows above all -- and groups of unequal rows leave their last
+// round badly filled.  Here a block takes a half, a third or a quarter of a CU's
+// LDS and registers, so that one block computes while another starts or stores.
+//
+// K goes in phases of 32 through a ring of LDS stages: while one is computed the
+// copies of the next are in flight, about 96 KB on a CU whatever the tile, which
+// is what the memory's latency takes.  Per phase a wave issues its share of the
+// 1 KB copies straight into LDS and its matrix instructions, and passes one
+// barrier.  The stages have the layouts of the 128-wide k-split tiles
+// (KsplitTile128): one for A's 128 rows or half of one for 64, one or two side
+// by side for B's columns.
+#include "epilogue.h"
+#include "grouped_kernels.h"
+#include "mfma16_ksplit128_core.h"
+#include "staged_tile.h"
+
+namespace gemmf32 {
+
+namespace {
+
+// Zeros over the block's BM x BN tile at (m0, n0): the gradient of a weight
+// that no row chose.
+template <int BM, int BN>
+__device__ __forceinline__ void zero_tile(const EpilogueArgs& e, int m0, int n0) {
+    const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i = threadIdx.x; i < BM * BN / 8; i += 256) {
+        const int row = m0 + i / (BN / 8), col = n0 + 8 * (i % (BN / 8));
+        if (row < e.M && col < e.N) store_values(e.c_type, e.C, (int64_t)row * e.ldc + col, e.N - col, v);
+    }
+}
+
+// Waits until at most N of this wave's copies are in flight and its LDS reads are
+// done.
+template <int N>
+__device__ __forceinline__ void wait_ring() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// The same for `ahead` phases of C copies each beyond the one waited for, at
+// most N of them in flight.
+template <int N, int C>
+__device__ __forceinline__ void wait_phase(int ahead) {
+    if (N == 0 || ahead >= N) wait_ring<N * C>();
+    else wait_phase<(N > 0 ? N - 1 : 0), C>(ahead);
+}
+
+// BM rows (64 only with A k-contiguous) x 128 NB columns, BLOCKS to a CU.
+template <int FMT, bool KCA, bool KCB, int BM_, int NB, int STAGES, int BLOCKS>
+struct GroupedSharedCore {
+    using TA = KsplitTile128<KCA>;
+    using TB = KsplitTile128<KCB>;
+    static constexpr int BM = BM_, BN = 128 * NB, BK = 32;
+    static_assert(BM == 128 || (BM == 64 && KCA), "tile");
+    // 64 x 256: four waves side by side; else two by two
+    static constexpr int WROWS = BM == 64 && NB == 2 ? 1 : 2, WCOLS = 4 / WROWS;
+    static constexpr int FM = BM / 16 / WROWS, FN = BN / 16 / WCOLS;
+    static constexpr int A_BYTES = TA::BYTES * BM / 128, STAGE = A_BYTES + NB * TB::BYTES;
+    static constexpr int CA = BM / 64, CB = 2 * NB, COPIES = CA + CB;            // per wave and phase
+    using Staged = StagedTile<FM, FN>;
+    using Run = EpilogueRun<8, false>;
+    static constexpr int PATCHES = 4 * Staged::PATCH * 4;
+    static constexpr int BIAS = STAGES * STAGE > PATCHES ? STAGES * STAGE : PATCHES;   // its place in LDS
+    static constexpr int LDS_BYTES = BIAS + 4 * BN;
+    static_assert(BLOCKS * LDS_BYTES <= 163840, "blocks to a CU");
+
+    // The tile at (m0, n0) of the product; K > 0.
+    __device__ static __forceinline__ void run(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
+                                               floatx4 (&acc)[FM][FN]) {
+        const int lane = threadIdx.x & 63;
+        const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        // This wave's copies: CA of A's, CB of those of one 128-wide half of B's
+        // columns.  Offsets are past the end by themselves wherever zeros are
+        // wanted: rows past the last one, k past K of a k-contiguous factor (the
+        // last phase), rows k past K of the other kind.
+        constexpr uint32_t kPastEnd = 0x80000000u;
+        const int half = CB * w / 8, b0 = CB * w % 8;
+        uint32_t offset[COPIES];
+#pragma unroll
+        for (int j = 0; j < CA; ++j) offset[j] = (uint32_t)TA::copy_src(CA * w + j, lane, m0, p.lda);
+#pragma unroll
+        for (int j = 0; j < CB; ++j) offset[CA + j] = (uint32_t)TB::copy_src(b0 + j, lane, n0 + 128 * half, p.ldb);
+        constexpr int kRawBufferWord3 = 0x00020000;
+        const int64_t a_rows = KCA ? p.M : p.K, a_cols = KCA ? p.K : p.M;
+        const int64_t b_rows = KCB ? p.N : p.K, b_cols = KCB ? p.K : p.N;
+        const __amdgpu_buffer_rsrc_t rsrc_a = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t*>(p.A), (short)0, (int)(2 * ((a_rows - 1) * p.lda + a_cols)), kRawBufferWord3);
+        const __amdgpu_buffer_rsrc_t rsrc_b = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t*>(p.B), (short)0, (int)(2 * ((b_rows - 1) * p.ldb + b_cols)), kRawBufferWord3);
+        auto copies = [&](int ph, int stage) __attribute__((always_inline)) {
+            const int k0 = BK * ph;
+            const bool last = k0 + BK > p.K;
+            unsigned char* const at = lds + stage * STAGE;
+            const uint32_t pa = (uint32_t)TA::phase_bytes(k0, p.lda), pb = (uint32_t)TB::phase_bytes(k0, p.ldb);
+#pragma unroll
+            for (int j = 0; j < CA; ++j) {
+                uint32_t v = offset[j] + pa;
+                if (KCA && last && k0 + TA::copy_k(CA * w + j, lane) >= p.K) v = kPastEnd;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc_a, (__attribute__((address_space(3))) void*)(at + TA::copy_dst(CA * w + j)), 16, (int)v, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < CB; ++j) {
+                uint32_t v = offset[CA + j] + pb;
+                if (KCB && last && k0 + TB::copy_k(b0 + j, lane) >= p.K) v = kPastEnd;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc_b,
+                    (__attribute__((address_space(3))) void*)(at + A_BYTES + half * TB::BYTES + TB::copy_dst(b0 + j)), 16,
+                    (int)v, 0, 0, 0);
+            }
+        };
+        // Read bases in stage 0: the wave's FM blocks of 16 rows and FN of 16
+        // columns (of one half, which holds 8 of them).
+        const int fa = FM * (w / WCOLS), fb = FN * (w % WCOLS);
+        const uint32_t a_at = lds_addr(lds) + TA::read_base(lane) + TA::read_imm(1, 0) * (uint32_t)fa;
+        const uint32_t b_at = lds_addr(lds) + A_BYTES + (uint32_t)(fb / 8) * TB::BYTES + TB::read_base(lane) +
+                              TB::read_imm(1, 0) * (uint32_t)(fb % 8);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+        const int phases = ceil_div(p.K, BK);
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (s < phases) copies(s, s);
+        int stage = 0;
+        for (int ph = 0; ph < phases; ++ph) {
+            // This phase's copies of this wave have landed (those of the next ones
+            // may be in flight) and its reads of the phase before are done; then
+            // everyone's are, and the stage before is free.
+            wait_phase<STAGES - 2, COPIES>(phases - 1 - ph);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (ph + STAGES - 1 < phases) copies(ph + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+            const uint32_t sa = a_at + (uint32_t)(stage * STAGE), sb = b_at + (uint32_t)(stage * STAGE);
+            u32x4 aq[FM], bq[FN];
+            u32x2 ah[FM][2], bh[FN][2];
+            if constexpr (KCA) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i) aq[i] = lds_read128(sa + TA::read_imm(i, 0));
+            } else {
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) ah[i][h] = read_tr16_off(sa, (int)TA::read_imm(i, h));
+            }
+            if constexpr (KCB) {
+#pragma unroll
+                for (int i = 0; i < FN; ++i) bq[i] = lds_read128(sb + TB::read_imm(i, 0));
+            } else {
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) bh[i][h] = read_tr16_off(sb, (int)TB::read_imm(i, h));
+            }
+            if constexpr (!KCA) {
+                wait_halves(ah);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) aq[i] = u32x4{ah[i][0][0], ah[i][0][1], ah[i][1][0], ah[i][1][1]};
+            }
+            if constexpr (!KCB) {
+                wait_halves(bh);
+#pragma unroll
+                for (int i = 0; i < FN; ++i) bq[i] = u32x4{bh[i][0][0], bh[i][0][1], bh[i][1][0], bh[i][1][1]};
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma16x16<FMT>(aq[i], bq[j], acc[i][j]);
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        }
+        __syncthreads();                               // the stages are free
+    }
+    __device__ static __forceinline__ void wait_halves(u32x2 (&h)[8][2]) { wait_tied(h); }
+    __device__ static __forceinline__ void wait_halves(u32x2 (&h)[4][2]) {
+        asm volatile("s_waitcnt lgkmcnt(0)"
+                     : "+v"(h[0][0]), "+v"(h[0][1]), "+v"(h[1][0]), "+v"(h[1][1]), "+v"(h[2][0]), "+v"(h[2][1]),
+                       "+v"(h[3][0]), "+v"(h[3][1])
+                     :
+                     : "memory");
+    }
+
+    // The forward epilogue; thread t holds bias value n0 + t.
+    __device__ static __forceinline__ void finish(const floatx4 (&acc)[FM][FN], const EpilogueArgs& e, int m0, int n0,
+                                                  float bias, unsigned char* lds) {
+        const int lane = threadIdx.x & 63;
+        const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        float* const shared = reinterpret_cast<float*>(lds + BIAS);
+        if ((int)threadIdx.x < BN) shared[threadIdx.x] = bias;
+        __syncthreads();
+        float* const patch = reinterpret_cast<float*>(lds) + w * Staged::PATCH;
+        const int row0 = m0 + 16 * FM * (w / WCOLS), wcol = 16 * FN * (w % WCOLS), col0 = n0 + wcol;
+        auto bias_of = [&](int col, float (&b)[8]) __attribute__((always_inline)) {
+            const floatx4 lo = *reinterpret_cast<const floatx4*>(shared + wcol + col);
+            const floatx4 hi = *reinterpret_cast<const floatx4*>(shared + wcol + col + 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                b[c] = lo[c];
+                b[4 + c] = hi[c];
+            }
+        };
+        // Whole runs at places of 32 bits from the wave's corner; else value by
+        // value where a run crosses N, with what the epilogue reads.
+        constexpr int64_t kMaxLd = 1 << 22;
+        if ((n0 + BN <= e.N || e.N % 8 == 0) && e.residual == nullptr && e.ldc < kMaxLd &&
+            (e.preact == nullptr || e.ldz < kMaxLd)) {
+            char* const c_base = static_cast<char*>(e.C) + (e.c_type == 2 ? 4 : 2) * ((int64_t)row0 * e.ldc + col0);
+            char* const z_base = static_cast<char*>(e.preact) + 2 * ((int64_t)row0 * e.ldz + col0);
+            const unsigned ldc = (unsigned)e.ldc, ldz = (unsigned)e.ldz;
+            Staged::template rows<false, 0>(
+                acc, patch, nullptr, lane, false, [](int, int, u32x4 (&)[1]) {},
+                [&](int row, int col, float (&v)[8], const u32x4 (&)[1]) __attribute__((always_inline)) {
+                    if (row0 + row >= e.M || col0 + col >= e.N) return;
+                    float b[8];
+                    bias_of(col, b);
+                    const Run run{};
+                    run.finish_at(e, c_base, __umul24(row, ldc) + col, z_base, __umul24(row, ldz) + col, b, v);
+                },
+                [](int, int) {});
+        } else {
+            Staged::template rows<false, 0>(
+                acc, patch, nullptr, lane, false, [](int, int, u32x4 (&)[1]) {},
+                [&](int row, int col, float (&v)[8], const u32x4 (&)[1]) __attribute__((always_inline)) {
+                    if (row0 + row >= e.M || col0 + col >= e.N) return;
+                    float b[8];
+                    bias_of(col, b);
+                    Run run;
+                    run.load(e, row0 + row, col0 + col);
+                    run.finish(e, row0 + row, col0 + col, b, v);
+                },
+                [](int, int) {});
+        }
+    }
+};
+
+// Blocks (x, y) of one x split K: y takes k from y k_share on (a multiple of 32)
+// and stores its sums as plane y, `plane` floats after the one before (then e is
+// that matrix, without a layer's epilogue); k_share = K: not split.
+template <int FMT, bool KCB, int BM, int NB, int STAGES, int BLOCKS>
+__global__ __launch_bounds__(256, BLOCKS)
+void grouped_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_n, int group_m, int k_share,
+                           int64_t plane) {
+    using Core = GroupedSharedCore<FMT, true, KCB, BM, NB, STAGES, BLOCKS>;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
+    const GroupRows r = locate_group_tile<BM>(a, (int)blockIdx.x, tiles_n, group_m);
+    if (r.rows < 0) return;
+    enter_group(a, r, &p, &e);
+    const int m0 = BM * r.tm, n0 = Core::BN * r.tn;
+    p.A += (int64_t)m0 * p.lda;
+    p.M = min(r.rows - m0, BM);
+    const int k0 = (int)blockIdx.y * k_share;
+    p.A += k0;
+    p.B += KCB ? (int64_t)k0 : k0 * p.ldb;
+    p.K = min(p.K - k0, k_share);
+    e.C = static_cast<char*>(e.C) + 4 * (blockIdx.y * plane);
+    float bias[1] = {0.0f};
+    if ((int)threadIdx.x < Core::BN) load_bias(e, n0 + (int)threadIdx.x, bias);
+    floatx4 acc[Core::FM][Core::FN];
+    Core::run(p, 0, n0, lds, acc);
+    Core::finish(acc, e, m0, n0, bias[0], lds);
+}
+
+// The same for the gradient: the group's rows in gridDim.y shares.
+template <int FMT, int NB, int STAGES, int BLOCKS>
+__global__ __launch_bounds__(256, BLOCKS)
+void grouped_grad_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, int group_m,
+                                int64_t plane) {
+    using Core = GroupedSharedCore<FMT, false, false, 128, NB, STAGES, BLOCKS>;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
+    GroupRows r = locate_grad_tile(a, (int)blockIdx.x, tiles_m, tiles_n, group_m);
+    const int splits = (int)gridDim.y, share = (r.rows + 32 * splits - 1) / (32 * splits) * 32;
+    const int skip = min((int)blockIdx.y * share, r.rows);
+    r.begin += skip;
+    r.rows = min(r.rows - skip, share);
+    enter_grad_group(a, r, &p, &e);
+    e.C = static_cast<char*>(e.C) + 4 * (blockIdx.y * plane);
+    const int m0 = Core::BM * r.tm, n0 = Core::BN * r.tn;
+    if (r.rows == 0) return zero_tile<Core::BM, Core::BN>(e, m0, n0);
+    floatx4 acc[Core::FM][Core::FN];
+    Core::run(p, m0, n0, lds, acc);
+    Core::finish(acc, e, m0, n0, 0.0f, lds);
+}
+
+template <int BM, int NB, int STAGES, int BLOCKS>
+void launch(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_b,
+            int k_share, int64_t plane) {
+    constexpr int kGroupM = 1024 / BM;
+    const int tn = ceil_div(p.N, 128 * NB);
+    const dim3 g((unsigned)(grouped_row_tiles(a.rows, a.groups, BM) * tn), (unsigned)ceil_div(p.K, k_share)), b(256);
+    auto run = [&](auto fmt, auto kcb) {
+        hipLaunchKernelGGL((grouped_shared_kernel<decltype(fmt)::value, decltype(kcb)::value, BM, NB, STAGES, BLOCKS>), g,
+                           b, 0, s, a, p, e, tn, kGroupM, k_share, plane);
+    };
+    if (format == 0 && op_b) run(std::integral_constant<int, 0>{}, std::true_type{});
+    else if (format == 0) run(std::integral_constant<int, 0>{}, std::false_type{});
+    else if (op_b) run(std::integral_constant<int, 1>{}, std::true_type{});
+    else run(std::integral_constant<int, 1>{}, std::false_type{});
+}
+
+template <int NB, int STAGES, int BLOCKS>
+void launch_grad(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
+                 int splits, int64_t plane) {
+    constexpr int kGroupM = 8;
+    const int tm = ceil_div(p.M, 128), tn = ceil_div(p.N, 128 * NB);
+    const dim3 g((unsigned)(tm * tn * a.groups), (unsigned)splits), b(256);
+    if (format == 0)
+        hipLaunchKernelGGL((grouped_grad_shared_kernel<0, NB, STAGES, BLOCKS>), g, b, 0, s, a, p, e, tm, tn, kGroupM, plane);
+    else
+        hipLaunchKernelGGL((grouped_grad_shared_kernel<1, NB, STAGES, BLOCKS>), g, b, 0, s, a, p, e, tm, tn, kGroupM, plane);
+}
+
+}  // namespace
+
+hipError_t launch_grouped_shared(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                 int format, int op_b, int bm, int bn, int k_share, int64_t plane) {
+    if (bm == 128 && bn == 256) launch<128, 2, 3, 2>(a, p, e, s, format, op_b, k_share, plane);
+    else if (bm == 128) launch<128, 1, 3, 3>(a, p, e, s, format, op_b, k_share, plane);
+    else if (bn == 256) launch<64, 2, 3, 2>(a, p, e, s, format, op_b, k_share, plane);
+    else launch<64, 1, 4, 3>(a, p, e, s, format, op_b, k_share, plane);
+    return hipGetLastError();
+}
+
+hipError_t launch_grouped_grad_shared(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
+                                      int format, int bn, int splits, int64_t plane) {
+    if (bn == 256) launch_grad<2, 3, 2>(a, p, e, s, format, splits, plane);
+    else launch_grad<1, 3, 3>(a, p, e, s, format, splits, plane);
+    return hipGetLastError();
+}
+
+}  // namespace gemmf32
