@@ -1,212 +1,18 @@
 // grouped.hip -- the layer whose rows belong to groups (experts) with a weight
-// each: choice of kernel, the tiles for any sizes and alignment, and the
-// activation's gradient with the groups' bias gradients.
+// each: choice of tile, the passes over a split K's planes, and the activation's
+// gradient with the groups' bias gradients.
 //
 // For the rows i of group g: Z_i = X_i W_g + b_g, Y_i = act(Z_i); backward,
 // dZ = dY act'(Z), dX_i = dZ_i W_g^T (the same product with the weight's other
 // orientation), dW_g = X_g^T dZ_g, db_g = the sum of dZ's rows of g.
 #include "epilogue.h"
 #include "grouped_kernels.h"
-#include "mfma16_common.h"
-#include "staged_tile.h"
 
 #include <math.h>
 
 namespace gemmf32 {
 
 namespace {
-
-// ------------------------------------------------------ tiles for any problem
-//
-// For what the copied tiles do not take: odd widths, leading dimensions or
-// bases, K no multiple of 8, operands past 2 GiB.
-
-// A tile of T rows of a factor, 64 deep, as 16-bit values in LDS: loaded by
-// 256 threads in runs of 8 that go through registers, so any alignment and
-// size will do (whole runs as one 16-byte load, runs across an edge value by
-// value, zeros past it), with 64-bit places.
-//   KC (k runs along the rows): T rows of 64, fragments read as 16 bytes of k
-//   else: 64 rows of T, fragments through the transposed read
-// Rows are padded by 16 bytes, which spreads them over the banks.
-template <bool KC, int T>
-struct GroupedTile {
-    static constexpr int BK = 64, PITCH = (KC ? BK : T) + 8, ELEMS = (KC ? T : BK) * PITCH;
-    static constexpr int RUNS = T * BK / 8 / 256;           // per thread
-    static constexpr int PER_ROW = (KC ? BK : T) / 8;
-    u32x4 held[RUNS];
-
-    // Rows (mn) mn0 .. of `mn`, k0 .. of `k`.
-    __device__ __forceinline__ void load(const uint16_t* base, int64_t ld, int mn0, int mn, int k0, int k) {
-#pragma unroll
-        for (int i = 0; i < RUNS; ++i) {
-            const int c = i * 256 + threadIdx.x, r = c / PER_ROW, at = 8 * (c % PER_ROW);
-            const int row = (KC ? mn0 : k0) + r, col = (KC ? k0 : mn0) + at;
-            const int valid = row < (KC ? mn : k) ? (KC ? k : mn) - col : 0;
-            const uint16_t* const q = base + (int64_t)row * ld + col;
-            u32x4 v = {0, 0, 0, 0};
-            if (valid >= 8) {
-                __builtin_memcpy(&v, q, 16);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < valid) v[e / 2] |= (unsigned)q[e] << (16 * (e % 2));
-            }
-            held[i] = v;
-        }
-    }
-    __device__ __forceinline__ void store(uint16_t* lds) const {
-#pragma unroll
-        for (int i = 0; i < RUNS; ++i) {
-            const int c = i * 256 + threadIdx.x;
-            *reinterpret_cast<u32x4*>(lds + c / PER_ROW * PITCH + 8 * (c % PER_ROW)) = held[i];
-        }
-    }
-    // Fragments of rows mn + 16 f, k 32 s + 8 (lane / 16) .. + 7.
-    template <int F>
-    __device__ static __forceinline__ void fragments(const uint16_t* lds, int mn, int s, int lane, u32x4 (&q)[F]) {
-        if constexpr (KC) {
-#pragma unroll
-            for (int f = 0; f < F; ++f)
-                q[f] = *reinterpret_cast<const u32x4*>(lds + (mn + 16 * f + lane % 16) * PITCH + 32 * s + 8 * (lane / 16));
-        } else {
-            const int j = lane % 16;
-            const uint32_t at = lds_addr(lds + (32 * s + 8 * (lane / 16) + j / 4) * PITCH + mn + 4 * (j % 4));
-            u32x2 h[F][2];
-#pragma unroll
-            for (int f = 0; f < F; ++f)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) h[f][i] = read_tr16(at + 2 * (4 * i * PITCH + 16 * f));
-            wait_halves(h);
-#pragma unroll
-            for (int f = 0; f < F; ++f) q[f] = u32x4{h[f][0][0], h[f][0][1], h[f][1][0], h[f][1][1]};
-        }
-    }
-    __device__ static __forceinline__ void wait_halves(u32x2 (&h)[4][2]) {
-        asm volatile("s_waitcnt lgkmcnt(0)"
-                     : "+v"(h[0][0]), "+v"(h[0][1]), "+v"(h[1][0]), "+v"(h[1][1]), "+v"(h[2][0]), "+v"(h[2][1]),
-                       "+v"(h[3][0]), "+v"(h[3][1])
-                     :
-                     : "memory");
-    }
-    __device__ static __forceinline__ void wait_halves(u32x2 (&h)[2][2]) {
-        asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(h[0][0]), "+v"(h[0][1]), "+v"(h[1][0]), "+v"(h[1][1]) : : "memory");
-    }
-};
-
-// The BT x BT tile at (m0, n0) of a product: four waves of BT / 2 x BT / 2, two
-// stages of LDS, the next phase's loads in registers while one is computed.
-template <int FMT, bool KCA, bool KCB, int BT>
-struct GroupedCore {
-    using TA = GroupedTile<KCA, BT>;
-    using TB = GroupedTile<KCB, BT>;
-    static constexpr int F = BT / 32;
-    using Staged = StagedTile<F, F>;
-    static constexpr int STAGE = TA::ELEMS + TB::ELEMS;
-    static constexpr int PATCHES = 4 * Staged::PATCH * 4;
-    static constexpr int LDS_BYTES = 4 * STAGE > PATCHES ? 4 * STAGE : PATCHES;
-
-    __device__ static __forceinline__ void run(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
-                                               floatx4 (&acc)[F][F]) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        uint16_t* const stage = reinterpret_cast<uint16_t*>(lds);
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-#pragma unroll
-            for (int j = 0; j < F; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-        TA a;
-        TB b;
-        const int phases = ceil_div(p.K, 64);
-        if (phases > 0) {
-            a.load(p.A, p.lda, m0, p.M, 0, p.K);
-            b.load(p.B, p.ldb, n0, p.N, 0, p.K);
-        }
-        for (int ph = 0; ph < phases; ++ph) {
-            uint16_t* const cur = stage + (ph & 1) * STAGE;
-            a.store(cur);
-            b.store(cur + TA::ELEMS);
-            __syncthreads();               // the other stage's readers passed the barrier before this one
-            if (ph + 1 < phases) {
-                a.load(p.A, p.lda, m0, p.M, 64 * (ph + 1), p.K);
-                b.load(p.B, p.ldb, n0, p.N, 64 * (ph + 1), p.K);
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                u32x4 fa[F], fb[F];
-                TA::template fragments<F>(cur, wave / 2 * (BT / 2), s, lane, fa);
-                TB::template fragments<F>(cur + TA::ELEMS, wave % 2 * (BT / 2), s, lane, fb);
-#pragma unroll
-                for (int i = 0; i < F; ++i)
-#pragma unroll
-                    for (int j = 0; j < F; ++j) acc[i][j] = mfma16x16<FMT>(fa[i], fb[j], acc[i][j]);
-            }
-        }
-        __syncthreads();
-    }
-
-    __device__ static __forceinline__ void finish(const floatx4 (&acc)[F][F], const EpilogueArgs& e, int m0, int n0,
-                                                  unsigned char* lds) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        float* const patch = reinterpret_cast<float*>(lds) + wave * Staged::PATCH;
-        const int row0 = m0 + wave / 2 * (BT / 2), col0 = n0 + wave % 2 * (BT / 2);
-        Staged::template rows<false, 0>(
-            acc, patch, nullptr, lane, false, [](int, int, u32x4 (&)[1]) {},
-            [&](int row, int col, float (&v)[8], const u32x4 (&)[1]) __attribute__((always_inline)) {
-                if (row0 + row >= e.M || col0 + col >= e.N) return;
-                float b[8];
-                load_bias(e, col0 + col, b);
-                EpilogueRun<8, false> run;
-                run.load(e, row0 + row, col0 + col);
-                run.finish(e, row0 + row, col0 + col, b, v);
-            },
-            [](int, int) {});
-    }
-};
-
-template <int FMT, bool KCB, int BT>
-__global__ __launch_bounds__(256)
-void grouped_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_n, int group_m) {
-    using Core = GroupedCore<FMT, true, KCB, BT>;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
-    const GroupRows r = locate_group_tile<BT>(a, (int)blockIdx.x, tiles_n, group_m);
-    if (r.rows < 0) return;
-    enter_group(a, r, &p, &e);
-    floatx4 acc[Core::F][Core::F];
-    Core::run(p, BT * r.tm, BT * r.tn, lds, acc);
-    Core::finish(acc, e, BT * r.tm, BT * r.tn, lds);
-}
-
-template <int FMT, int BT>
-__global__ __launch_bounds__(256)
-void grouped_grad_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, int group_m) {
-    using Core = GroupedCore<FMT, false, false, BT>;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
-    const GroupRows r = locate_grad_tile(a, (int)blockIdx.x, tiles_m, tiles_n, group_m);
-    enter_grad_group(a, r, &p, &e);
-    floatx4 acc[Core::F][Core::F];
-    Core::run(p, BT * r.tm, BT * r.tn, lds, acc);
-    Core::finish(acc, e, BT * r.tm, BT * r.tn, lds);
-}
-
-template <int BT>
-hipError_t launch_any(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
-                      int op_b) {
-    const int tn = ceil_div(p.N, BT);
-    const dim3 grid((unsigned)(grouped_row_tiles(a.rows, a.groups, BT) * tn)), b(256);
-    if (format == 0 && op_b) hipLaunchKernelGGL((grouped_kernel<0, true, BT>), grid, b, 0, s, a, p, e, tn, 8);
-    else if (format == 0) hipLaunchKernelGGL((grouped_kernel<0, false, BT>), grid, b, 0, s, a, p, e, tn, 8);
-    else if (op_b) hipLaunchKernelGGL((grouped_kernel<1, true, BT>), grid, b, 0, s, a, p, e, tn, 8);
-    else hipLaunchKernelGGL((grouped_kernel<1, false, BT>), grid, b, 0, s, a, p, e, tn, 8);
-    return hipGetLastError();
-}
-
-template <int BT>
-hipError_t launch_grad_any(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format) {
-    const int tm = ceil_div(p.M, BT), tn = ceil_div(p.N, BT);
-    const dim3 grid((unsigned)(tm * tn * a.groups)), b(256);
-    if (format == 0) hipLaunchKernelGGL((grouped_grad_kernel<0, BT>), grid, b, 0, s, a, p, e, tm, tn, 8);
-    else hipLaunchKernelGGL((grouped_grad_kernel<1, BT>), grid, b, 0, s, a, p, e, tm, tn, 8);
-    return hipGetLastError();
-}
 
 // ------------------------------------------------------- choice of kernel
 
@@ -215,12 +21,12 @@ hipError_t launch_grad_any(const GroupedArgs& a, const Gemm16Args& p, const Epil
 bool offsets_hold(int64_t rows, int64_t ld) { return ld < (1ll << 30) / (rows + 256); }
 bool even_base(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-// Whether the copied tiles (grouped_shared.hip) take the product.
-bool shared_fits(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
+// Whether the operands can be copied straight into LDS.
+bool direct_fits(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
     return p.K > 0 && p.K % 8 == 0 && p.lda % 2 == 0 && p.ldb % 2 == 0 && a.stride_b % 2 == 0 && (op_b || p.N % 2 == 0) &&
            even_base(p.A) && even_base(p.B) && offsets_hold(256, p.lda) && offsets_hold(op_b ? p.N : p.K, p.ldb);
 }
-bool shared_grad_fits(const GroupedArgs& a, const Gemm16Args& p) {
+bool direct_grad_fits(const GroupedArgs& a, const Gemm16Args& p) {
     return p.lda % 2 == 0 && p.ldb % 2 == 0 && p.M % 2 == 0 && p.N % 2 == 0 && even_base(p.A) && even_base(p.B) &&
            offsets_hold(a.rows, p.lda) && offsets_hold(a.rows, p.ldb);
 }
@@ -260,7 +66,7 @@ double tiles_time(const Shape& c, double tiles, double phases) {
 double pass_time(int splits, double values) { return 4.0 + 4.0 * splits * values / 3e6; }
 
 struct Plan {
-    bool shared;
+    bool direct;
     int bm, bn;
     int splits, k_share;               // blocks along K; k of each
     int64_t bytes;                     // of planes, if split
@@ -270,11 +76,17 @@ Plan make_plan(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
     Plan q{};
     q.splits = 1;
     q.k_share = p.K;
-    if (!shared_fits(a, p, op_b)) return q;
-    q.shared = true;
+    q.direct = direct_fits(a, p, op_b);
+    if (p.K == 0) {                    // the epilogue alone
+        q.bm = 64;
+        q.bn = 128;
+        q.k_share = 1;
+        return q;
+    }
     const int phases = ceil_div(p.K, 32);
     double least = 1e30;
     for (const Shape& c : kShapes) {
+        if (!q.direct && c.bn != 128) continue;
         const double tiles = expected_row_tiles(a.groups, a.rows, c.bm) * ceil_div(p.N, c.bn);
         for (int splits = 1; splits <= 16 && (splits == 1 || (tiles * splits <= c.slots && phases >= 8 * splits)); splits *= 2) {
             const double t = tiles_time(c, tiles * splits, (double)phases / splits) +
@@ -298,11 +110,10 @@ Plan make_plan(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
 Plan make_grad_plan(const GroupedArgs& a, const Gemm16Args& p) {
     Plan q{};
     q.splits = 1;
-    if (!shared_grad_fits(a, p)) return q;
-    q.shared = true;
+    q.direct = direct_grad_fits(a, p);
     q.bm = 128;
     const int64_t wide = (int64_t)a.groups * ceil_div(p.M, 128) * ceil_div(p.N, 256);
-    q.bn = wide >= 1024 ? 256 : 128;
+    q.bn = q.direct && wide >= 1024 ? 256 : 128;
     if (q.bn == 256) return q;
     const double tiles = (double)a.groups * ceil_div(p.M, 128) * ceil_div(p.N, 128);
     const double phases = ceil(a.rows / used_groups(a.groups, a.rows > 0 ? a.rows : 1) / 32.0);
@@ -387,15 +198,14 @@ int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, const Epilo
 hipError_t launch_grouped(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
                           int op_b, void* workspace) {
     const Plan q = make_plan(a, p, op_b);
-    if (!q.shared) return launch_any<128>(a, p, e, s, format, op_b);
-    if (q.splits == 1) return launch_grouped_shared(a, p, e, s, format, op_b, q.bm, q.bn, q.k_share, 0);
+    if (q.splits == 1) return launch_grouped_shared(a, p, e, s, format, op_b, q.direct, q.bm, q.bn, q.k_share, 0);
     const int64_t plane = (int64_t)a.rows * p.N;
     EpilogueArgs sums{};
     sums.N = e.N;
     sums.c_type = 2;
     sums.C = workspace;
     sums.ldc = p.N;
-    const hipError_t err = launch_grouped_shared(a, p, sums, s, format, op_b, q.bm, q.bn, q.k_share, plane);
+    const hipError_t err = launch_grouped_shared(a, p, sums, s, format, op_b, q.direct, q.bm, q.bn, q.k_share, plane);
     if (err != hipSuccess) return err;
     const int tn = ceil_div(e.N, 128);
     hipLaunchKernelGGL(grouped_pass_kernel, dim3((unsigned)(grouped_row_tiles(a.rows, a.groups, kPassRows) * tn)), dim3(256),
@@ -410,8 +220,7 @@ int64_t grouped_grad_workspace(const GroupedArgs& a, const Gemm16Args& p, const 
 hipError_t launch_grouped_grad(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
                                int format, void* workspace) {
     const Plan q = make_grad_plan(a, p);
-    if (!q.shared) return launch_grad_any<128>(a, p, e, s, format);
-    if (q.splits == 1) return launch_grouped_grad_shared(a, p, e, s, format, q.bn, 1, 0);
+    if (q.splits == 1) return launch_grouped_grad_shared(a, p, e, s, format, q.direct, q.bn, 1, 0);
     const int64_t plane = (int64_t)a.groups * p.M * p.N;
     GroupedArgs whole = a;
     whole.stride_b = (int64_t)p.M * p.N;
@@ -421,7 +230,7 @@ hipError_t launch_grouped_grad(const GroupedArgs& a, const Gemm16Args& p, const 
     sums.c_type = 2;
     sums.C = workspace;
     sums.ldc = p.N;
-    const hipError_t err = launch_grouped_grad_shared(whole, p, sums, s, format, q.bn, q.splits, plane);
+    const hipError_t err = launch_grouped_grad_shared(whole, p, sums, s, format, q.direct, q.bn, q.splits, plane);
     if (err != hipSuccess) return err;
     const int64_t rows = (int64_t)a.groups * p.M;
     hipLaunchKernelGGL(grouped_grad_pass_kernel, dim3(ceil_div(p.N, 128), (unsigned)((rows + 7) / 8)), dim3(256), 0, s, e,

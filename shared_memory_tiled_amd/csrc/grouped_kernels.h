@@ -143,16 +143,18 @@ __device__ __forceinline__ void enter_grad_group(const GroupedArgs& a, const Gro
 #endif
 
 // Tiles of bm x bn (grouped_shared.hip): 128 x 256, 128 x 128, 64 x 256, 64 x
-// 128; the gradient's of 128 rows.  For bases on 4 bytes, even leading dimensions
-// and strides, even widths of the factors that are not k-contiguous, K a multiple
-// of 8 otherwise (the gradient: any rows), and operands within the copies'
-// offsets; the caller checks.  K split over blocks (k_share a multiple of 32
-// below K; splits above 1): each stores its sums as a plane of binary32 values,
-// `plane` of them after the one before, e then being the first plane.
+// 128; the gradient's of 128 rows.  direct: the operands are copied straight into
+// LDS, for bases on 4 bytes, even leading dimensions and strides, even widths of
+// the factors that are not k-contiguous, K a multiple of 8 otherwise (the
+// gradient: any rows), and operands within the copies' offsets; the caller
+// checks.  Otherwise any problem, on 128 columns.  K split over blocks (k_share a
+// multiple of 32 below K; splits above 1): each stores its sums as a plane of
+// binary32 values, `plane` of them after the one before, e then being the first
+// plane.
 hipError_t launch_grouped_shared(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                 int format, int op_b, int bm, int bn, int k_share, int64_t plane);
+                                 int format, int op_b, bool direct, int bm, int bn, int k_share, int64_t plane);
 hipError_t launch_grouped_grad_shared(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                      int format, int bn, int splits, int64_t plane);
+                                      int format, bool direct, int bn, int splits, int64_t plane);
 
 // p: A, B, N, K and their leading dimensions (M is not used); e: M is not used.
 int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, int op_b);

@@ -12,7 +12,11 @@
 // copies of the next are in flight, about 96 KB on a CU whatever the tile, which
 // is what the memory's latency takes.  Per phase a wave issues its share of the
 // 1 KB copies straight into LDS and its matrix instructions, and passes one
-// barrier.  The stages have the layouts of the 128-wide k-split tiles
+// barrier.  Problems that the copies do not take (DIRECT false: odd widths,
+// leading dimensions or bases, K no multiple of 8, operands past 2 GiB) go
+// through registers instead: runs of 8 values loaded wherever they lie, three
+// phases ahead, then written to the same places of one of two stages.  The stages
+// have the layouts of the 128-wide k-split tiles
 // (KsplitTile128): one for A's 128 rows or half of one for 64, one or two side
 // by side for B's columns.
 #include "epilogue.h"
@@ -51,7 +55,7 @@ __device__ __forceinline__ void wait_phase(int ahead) {
 }
 
 // BM rows (64 only with A k-contiguous) x 128 NB columns, BLOCKS to a CU.
-template <int FMT, bool KCA, bool KCB, int BM_, int NB, int STAGES, int BLOCKS>
+template <int FMT, bool KCA, bool KCB, int BM_, int NB, int STAGES, int BLOCKS, bool DIRECT>
 struct GroupedSharedCore {
     using TA = KsplitTile128<KCA>;
     using TB = KsplitTile128<KCB>;
@@ -69,9 +73,71 @@ struct GroupedSharedCore {
     static constexpr int LDS_BYTES = BIAS + 4 * BN;
     static_assert(BLOCKS * LDS_BYTES <= 163840, "blocks to a CU");
 
-    // The tile at (m0, n0) of the product; K > 0.
+    // Where a wave reads its fragments in stage 0: its FM blocks of 16 rows and FN
+    // of 16 columns (of one half, which holds 8 of them).
+    struct Fragments {
+        uint32_t a_at, b_at;
+        __device__ __forceinline__ Fragments(const unsigned char* lds, int lane, int w) {
+            const int fa = FM * (w / WCOLS), fb = FN * (w % WCOLS);
+            a_at = lds_addr(lds) + TA::read_base(lane) + TA::read_imm(1, 0) * (uint32_t)fa;
+            b_at = lds_addr(lds) + A_BYTES + (uint32_t)(fb / 8) * TB::BYTES + TB::read_base(lane) +
+                   TB::read_imm(1, 0) * (uint32_t)(fb % 8);
+        }
+        // A phase's matrix instructions, from `stage`.
+        __device__ __forceinline__ void multiply(int stage, floatx4 (&acc)[FM][FN]) const {
+            const uint32_t sa = a_at + (uint32_t)(stage * STAGE), sb = b_at + (uint32_t)(stage * STAGE);
+            u32x4 aq[FM], bq[FN];
+            u32x2 ah[FM][2], bh[FN][2];
+            if constexpr (KCA) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i) aq[i] = lds_read128(sa + TA::read_imm(i, 0));
+            } else {
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) ah[i][h] = read_tr16_off(sa, (int)TA::read_imm(i, h));
+            }
+            if constexpr (KCB) {
+#pragma unroll
+                for (int i = 0; i < FN; ++i) bq[i] = lds_read128(sb + TB::read_imm(i, 0));
+            } else {
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) bh[i][h] = read_tr16_off(sb, (int)TB::read_imm(i, h));
+            }
+            if constexpr (!KCA) {
+                wait_halves(ah);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) aq[i] = u32x4{ah[i][0][0], ah[i][0][1], ah[i][1][0], ah[i][1][1]};
+            }
+            if constexpr (!KCB) {
+                wait_halves(bh);
+#pragma unroll
+                for (int i = 0; i < FN; ++i) bq[i] = u32x4{bh[i][0][0], bh[i][0][1], bh[i][1][0], bh[i][1][1]};
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma16x16<FMT>(aq[i], bq[j], acc[i][j]);
+        }
+    };
+    __device__ static __forceinline__ void clear(floatx4 (&acc)[FM][FN]) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // The tile at (m0, n0) of the product; K > 0 if DIRECT.
     __device__ static __forceinline__ void run(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
                                                floatx4 (&acc)[FM][FN]) {
+        if constexpr (DIRECT) run_direct(p, m0, n0, lds, acc);
+        else run_staged(p, m0, n0, lds, acc);
+    }
+
+    __device__ static __forceinline__ void run_direct(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
+                                                      floatx4 (&acc)[FM][FN]) {
         const int lane = threadIdx.x & 63;
         const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         // This wave's copies: CA of A's, CB of those of one 128-wide half of B's
@@ -114,16 +180,8 @@ struct GroupedSharedCore {
                     (int)v, 0, 0, 0);
             }
         };
-        // Read bases in stage 0: the wave's FM blocks of 16 rows and FN of 16
-        // columns (of one half, which holds 8 of them).
-        const int fa = FM * (w / WCOLS), fb = FN * (w % WCOLS);
-        const uint32_t a_at = lds_addr(lds) + TA::read_base(lane) + TA::read_imm(1, 0) * (uint32_t)fa;
-        const uint32_t b_at = lds_addr(lds) + A_BYTES + (uint32_t)(fb / 8) * TB::BYTES + TB::read_base(lane) +
-                              TB::read_imm(1, 0) * (uint32_t)(fb % 8);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+        const Fragments fragments(lds, lane, w);
+        clear(acc);
         const int phases = ceil_div(p.K, BK);
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s)
@@ -137,44 +195,99 @@ struct GroupedSharedCore {
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             if (ph + STAGES - 1 < phases) copies(ph + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-            const uint32_t sa = a_at + (uint32_t)(stage * STAGE), sb = b_at + (uint32_t)(stage * STAGE);
-            u32x4 aq[FM], bq[FN];
-            u32x2 ah[FM][2], bh[FN][2];
-            if constexpr (KCA) {
-#pragma unroll
-                for (int i = 0; i < FM; ++i) aq[i] = lds_read128(sa + TA::read_imm(i, 0));
-            } else {
-#pragma unroll
-                for (int i = 0; i < FM; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) ah[i][h] = read_tr16_off(sa, (int)TA::read_imm(i, h));
-            }
-            if constexpr (KCB) {
-#pragma unroll
-                for (int i = 0; i < FN; ++i) bq[i] = lds_read128(sb + TB::read_imm(i, 0));
-            } else {
-#pragma unroll
-                for (int i = 0; i < FN; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) bh[i][h] = read_tr16_off(sb, (int)TB::read_imm(i, h));
-            }
-            if constexpr (!KCA) {
-                wait_halves(ah);
-#pragma unroll
-                for (int i = 0; i < FM; ++i) aq[i] = u32x4{ah[i][0][0], ah[i][0][1], ah[i][1][0], ah[i][1][1]};
-            }
-            if constexpr (!KCB) {
-                wait_halves(bh);
-#pragma unroll
-                for (int i = 0; i < FN; ++i) bq[i] = u32x4{bh[i][0][0], bh[i][0][1], bh[i][1][0], bh[i][1][1]};
-            }
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mfma16x16<FMT>(aq[i], bq[j], acc[i][j]);
+            fragments.multiply(stage, acc);
             stage = stage == STAGES - 1 ? 0 : stage + 1;
         }
         __syncthreads();                               // the stages are free
+    }
+
+    // Through registers, for operands anywhere in memory.  A run is one load of 16
+    // bytes without a branch: rows past the last one repeat it and columns past
+    // the last one repeat the first (both end in results that are not stored), and
+    // a run across the last column reads on into the next row.  Only the last
+    // phase, which holds the last row and K's edge, takes its values one by one
+    // with zeros past K; it is computed first.  Rows shorter than a run (of an
+    // operand whose k runs along its columns) always go one by one.
+    __device__ static __forceinline__ void run_staged(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
+                                                      floatx4 (&acc)[FM][FN]) {
+        const int lane = threadIdx.x & 63;
+        const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        const int half = CB * w / 8, b0 = CB * w % 8;
+        const Fragments fragments(lds, lane, w);
+        clear(acc);
+        const int phases = ceil_div(p.K, BK);
+        if (phases == 0) return __syncthreads();
+        constexpr int AHEAD = 3;
+        u32x4 held[AHEAD][COPIES];
+        // Copy j's first value at phase 0, the first of its k and how many values
+        // of a run of the other kind exist.
+        const uint16_t* at[COPIES];
+        int k_of[COPIES], width[COPIES];
+        auto place = [&](int j, bool kc, const uint16_t* base, int64_t ld, int size, int mn, int k) __attribute__((always_inline)) {
+            const int row = min(mn, size - 1), col = mn < size ? mn : 0;
+            at[j] = base + (kc ? (int64_t)row * ld + k : (int64_t)k * ld + col);
+            k_of[j] = k;
+            width[j] = kc ? 8 : min(size - col, 8);
+        };
+#pragma unroll
+        for (int j = 0; j < CA; ++j)
+            place(j, KCA, p.A, p.lda, p.M, m0 + TA::copy_mn(CA * w + j, lane), TA::copy_k(CA * w + j, lane));
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+            place(CA + j, KCB, p.B, p.ldb, p.N, n0 + 128 * half + TB::copy_mn(b0 + j, lane), TB::copy_k(b0 + j, lane));
+        const int64_t step_a = BK * (KCA ? 1 : p.lda), step_b = BK * (KCB ? 1 : p.ldb);
+        const bool short_a = !KCA && p.lda < 8, short_b = !KCB && p.ldb < 8;
+        // The values of copy j's run in phase ph, one by one.
+        auto single = [&](int j, int ph) __attribute__((always_inline)) -> u32x4 {
+            const bool kc = j < CA ? KCA : KCB;
+            const int left = p.K - BK * ph - k_of[j];                     // of k, from the run's first
+            const int valid = kc ? min(left, 8) : left > 0 ? width[j] : 0;
+            const uint16_t* const q = valid > 0 ? at[j] + ph * (j < CA ? step_a : step_b) : j < CA ? p.A : p.B;
+            unsigned u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = q[max(min(e, valid - 1), 0)];
+            u32x4 v;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                v[d] = (2 * d < valid ? u[2 * d] : 0u) | (2 * d + 1 < valid ? u[2 * d + 1] << 16 : 0u);
+            return v;
+        };
+        auto load = [&](int ph, u32x4 (&v)[COPIES]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < COPIES; ++j) {
+                if (j < CA ? short_a : short_b) v[j] = single(j, ph);
+                else __builtin_memcpy(&v[j], at[j] + ph * (j < CA ? step_a : step_b), 16);
+            }
+        };
+        auto store = [&](const u32x4 (&v)[COPIES], int stage) __attribute__((always_inline)) {
+            unsigned char* const to = lds + stage * STAGE + 16 * lane;
+#pragma unroll
+            for (int j = 0; j < CA; ++j) *reinterpret_cast<u32x4*>(to + TA::copy_dst(CA * w + j)) = v[j];
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+                *reinterpret_cast<u32x4*>(to + A_BYTES + half * TB::BYTES + TB::copy_dst(b0 + j)) = v[CA + j];
+        };
+        // Position 0 is the last phase, position i phase i - 1.
+#pragma unroll
+        for (int s = 1; s < AHEAD; ++s)
+            if (s < phases) load(s - 1, held[s]);
+#pragma unroll
+        for (int j = 0; j < COPIES; ++j) held[0][j] = single(j, phases - 1);
+        for (int i = 0; i < phases; i += AHEAD) {
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s) {
+                if (i + s >= phases) break;
+                const int stage = (i + s) & 1;
+                // The stage's readers, two phases ago, passed the last barrier.
+                store(held[s], stage);
+                if (i + s + AHEAD < phases) load(i + s + AHEAD - 1, held[s]);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                fragments.multiply(stage, acc);
+            }
+        }
+        __syncthreads();
     }
     __device__ static __forceinline__ void wait_halves(u32x2 (&h)[8][2]) { wait_tied(h); }
     __device__ static __forceinline__ void wait_halves(u32x2 (&h)[4][2]) {
@@ -241,11 +354,11 @@ struct GroupedSharedCore {
 // Blocks (x, y) of one x split K: y takes k from y k_share on (a multiple of 32)
 // and stores its sums as plane y, `plane` floats after the one before (then e is
 // that matrix, without a layer's epilogue); k_share = K: not split.
-template <int FMT, bool KCB, int BM, int NB, int STAGES, int BLOCKS>
+template <int FMT, bool KCB, int BM, int NB, int STAGES, int BLOCKS, bool DIRECT>
 __global__ __launch_bounds__(256, BLOCKS)
 void grouped_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_n, int group_m, int k_share,
                            int64_t plane) {
-    using Core = GroupedSharedCore<FMT, true, KCB, BM, NB, STAGES, BLOCKS>;
+    using Core = GroupedSharedCore<FMT, true, KCB, BM, NB, STAGES, BLOCKS, DIRECT>;
     __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
     const GroupRows r = locate_group_tile<BM>(a, (int)blockIdx.x, tiles_n, group_m);
     if (r.rows < 0) return;
@@ -266,11 +379,11 @@ void grouped_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tile
 }
 
 // The same for the gradient: the group's rows in gridDim.y shares.
-template <int FMT, int NB, int STAGES, int BLOCKS>
+template <int FMT, int NB, int STAGES, int BLOCKS, bool DIRECT>
 __global__ __launch_bounds__(256, BLOCKS)
 void grouped_grad_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, int group_m,
                                 int64_t plane) {
-    using Core = GroupedSharedCore<FMT, false, false, 128, NB, STAGES, BLOCKS>;
+    using Core = GroupedSharedCore<FMT, false, false, 128, NB, STAGES, BLOCKS, DIRECT>;
     __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
     GroupRows r = locate_grad_tile(a, (int)blockIdx.x, tiles_m, tiles_n, group_m);
     const int splits = (int)gridDim.y, share = (r.rows + 32 * splits - 1) / (32 * splits) * 32;
@@ -286,15 +399,15 @@ void grouped_grad_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int
     Core::finish(acc, e, m0, n0, 0.0f, lds);
 }
 
-template <int BM, int NB, int STAGES, int BLOCKS>
+template <int BM, int NB, int STAGES, int BLOCKS, bool DIRECT>
 void launch(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_b,
             int k_share, int64_t plane) {
     constexpr int kGroupM = 1024 / BM;
     const int tn = ceil_div(p.N, 128 * NB);
-    const dim3 g((unsigned)(grouped_row_tiles(a.rows, a.groups, BM) * tn), (unsigned)ceil_div(p.K, k_share)), b(256);
+    const dim3 g((unsigned)(grouped_row_tiles(a.rows, a.groups, BM) * tn), p.K > 0 ? (unsigned)ceil_div(p.K, k_share) : 1u), b(256);
     auto run = [&](auto fmt, auto kcb) {
-        hipLaunchKernelGGL((grouped_shared_kernel<decltype(fmt)::value, decltype(kcb)::value, BM, NB, STAGES, BLOCKS>), g,
-                           b, 0, s, a, p, e, tn, kGroupM, k_share, plane);
+        hipLaunchKernelGGL((grouped_shared_kernel<decltype(fmt)::value, decltype(kcb)::value, BM, NB, STAGES, BLOCKS,
+                                                  DIRECT>), g, b, 0, s, a, p, e, tn, kGroupM, k_share, plane);
     };
     if (format == 0 && op_b) run(std::integral_constant<int, 0>{}, std::true_type{});
     else if (format == 0) run(std::integral_constant<int, 0>{}, std::false_type{});
@@ -302,33 +415,37 @@ void launch(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hi
     else run(std::integral_constant<int, 1>{}, std::false_type{});
 }
 
-template <int NB, int STAGES, int BLOCKS>
+template <int NB, int STAGES, int BLOCKS, bool DIRECT>
 void launch_grad(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
                  int splits, int64_t plane) {
     constexpr int kGroupM = 8;
     const int tm = ceil_div(p.M, 128), tn = ceil_div(p.N, 128 * NB);
     const dim3 g((unsigned)(tm * tn * a.groups), (unsigned)splits), b(256);
     if (format == 0)
-        hipLaunchKernelGGL((grouped_grad_shared_kernel<0, NB, STAGES, BLOCKS>), g, b, 0, s, a, p, e, tm, tn, kGroupM, plane);
+        hipLaunchKernelGGL((grouped_grad_shared_kernel<0, NB, STAGES, BLOCKS, DIRECT>), g, b, 0, s, a, p, e, tm, tn, kGroupM, plane);
     else
-        hipLaunchKernelGGL((grouped_grad_shared_kernel<1, NB, STAGES, BLOCKS>), g, b, 0, s, a, p, e, tm, tn, kGroupM, plane);
+        hipLaunchKernelGGL((grouped_grad_shared_kernel<1, NB, STAGES, BLOCKS, DIRECT>), g, b, 0, s, a, p, e, tm, tn, kGroupM, plane);
 }
 
 }  // namespace
 
 hipError_t launch_grouped_shared(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                 int format, int op_b, int bm, int bn, int k_share, int64_t plane) {
-    if (bm == 128 && bn == 256) launch<128, 2, 3, 2>(a, p, e, s, format, op_b, k_share, plane);
-    else if (bm == 128) launch<128, 1, 3, 3>(a, p, e, s, format, op_b, k_share, plane);
-    else if (bn == 256) launch<64, 2, 3, 2>(a, p, e, s, format, op_b, k_share, plane);
-    else launch<64, 1, 4, 3>(a, p, e, s, format, op_b, k_share, plane);
+                                 int format, int op_b, bool direct, int bm, int bn, int k_share, int64_t plane) {
+    if (!direct) {
+        if (bm == 128) launch<128, 1, 2, 2, false>(a, p, e, s, format, op_b, k_share, plane);
+        else launch<64, 1, 2, 3, false>(a, p, e, s, format, op_b, k_share, plane);
+    } else if (bm == 128 && bn == 256) launch<128, 2, 3, 2, true>(a, p, e, s, format, op_b, k_share, plane);
+    else if (bm == 128) launch<128, 1, 3, 3, true>(a, p, e, s, format, op_b, k_share, plane);
+    else if (bn == 256) launch<64, 2, 3, 2, true>(a, p, e, s, format, op_b, k_share, plane);
+    else launch<64, 1, 4, 3, true>(a, p, e, s, format, op_b, k_share, plane);
     return hipGetLastError();
 }
 
 hipError_t launch_grouped_grad_shared(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
-                                      int format, int bn, int splits, int64_t plane) {
-    if (bn == 256) launch_grad<2, 3, 2>(a, p, e, s, format, splits, plane);
-    else launch_grad<1, 3, 3>(a, p, e, s, format, splits, plane);
+                                      int format, bool direct, int bn, int splits, int64_t plane) {
+    if (!direct) launch_grad<1, 2, 2, false>(a, p, e, s, format, splits, plane);
+    else if (bn == 256) launch_grad<2, 3, 2, true>(a, p, e, s, format, splits, plane);
+    else launch_grad<1, 3, 3, true>(a, p, e, s, format, splits, plane);
     return hipGetLastError();
 }
 
