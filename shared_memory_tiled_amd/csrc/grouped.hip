@@ -23,7 +23,7 @@ bool even_base(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0
 
 // Whether the operands can be copied straight into LDS.
 bool direct_fits(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
-    return p.K > 0 && p.K % 8 == 0 && p.lda % 2 == 0 && p.ldb % 2 == 0 && a.stride_b % 2 == 0 && (op_b || p.N % 2 == 0) &&
+    return p.K > 0 && p.K % 2 == 0 && p.lda % 2 == 0 && p.ldb % 2 == 0 && a.stride_b % 2 == 0 && (op_b || p.N % 2 == 0) &&
            even_base(p.A) && even_base(p.B) && offsets_hold(256, p.lda) && offsets_hold(op_b ? p.N : p.K, p.ldb);
 }
 bool direct_grad_fits(const GroupedArgs& a, const Gemm16Args& p) {

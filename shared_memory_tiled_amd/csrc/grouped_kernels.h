@@ -145,8 +145,8 @@ __device__ __forceinline__ void enter_grad_group(const GroupedArgs& a, const Gro
 // Tiles of bm x bn (grouped_shared.hip): 128 x 256, 128 x 128, 64 x 256, 64 x
 // 128; the gradient's of 128 rows.  direct: the operands are copied straight into
 // LDS, for bases on 4 bytes, even leading dimensions and strides, even widths of
-// the factors that are not k-contiguous, K a multiple of 8 otherwise (the
-// gradient: any rows), and operands within the copies' offsets; the caller
+// the factors that are not k-contiguous, an even K otherwise (the gradient: any
+// rows), and operands within the copies' offsets; the caller
 // checks.  Otherwise any problem, on 128 columns.  K split over blocks (k_share a
 // multiple of 32 below K; splits above 1): each stores its sums as a plane of
 // binary32 values, `plane` of them after the one before, e then being the first

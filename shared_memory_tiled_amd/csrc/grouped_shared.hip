@@ -13,7 +13,7 @@
 // is what the memory's latency takes.  Per phase a wave issues its share of the
 // 1 KB copies straight into LDS and its matrix instructions, and passes one
 // barrier.  Problems that the copies do not take (DIRECT false: odd widths,
-// leading dimensions or bases, K no multiple of 8, operands past 2 GiB) go
+// leading dimensions or bases, an odd K, operands past 2 GiB) go
 // through registers instead: runs of 8 values loaded wherever they lie, three
 // phases ahead, then written to the same places of one of two stages.  The stages
 // have the layouts of the 128-wide k-split tiles
@@ -136,6 +136,22 @@ struct GroupedSharedCore {
         else run_staged(p, m0, n0, lds, acc);
     }
 
+    // Zeros over the values from k on in the runs that hold the last phase's k (not
+    // a multiple of 8) of k-contiguous factors: what was copied there lies past K.
+    __device__ static __forceinline__ void cut_runs(unsigned char* stage, int k) {
+        u32x4 mask;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            mask[d] = (2 * d < k % 8 ? 0x0000FFFFu : 0u) | (2 * d + 1 < k % 8 ? 0xFFFF0000u : 0u);
+        auto cut = [&](unsigned char* tile, int rows) __attribute__((always_inline)) {
+            for (int r = threadIdx.x; r < rows; r += 256)
+                *reinterpret_cast<u32x4*>(tile + 64 * r + 16 * ((k / 8) ^ (((r >> 3) & 1) << 1))) &= mask;
+        };
+        if constexpr (KCA) cut(stage, BM);
+        if constexpr (KCB) cut(stage + A_BYTES, BN);
+        __syncthreads();
+    }
+
     __device__ static __forceinline__ void run_direct(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
                                                       floatx4 (&acc)[FM][FN]) {
         const int lane = threadIdx.x & 63;
@@ -195,6 +211,7 @@ struct GroupedSharedCore {
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             if (ph + STAGES - 1 < phases) copies(ph + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+            if ((KCA || KCB) && ph == phases - 1 && p.K % 8 != 0) cut_runs(lds + stage * STAGE, p.K % 32);
             fragments.multiply(stage, acc);
             stage = stage == STAGES - 1 ? 0 : stage + 1;
         }
