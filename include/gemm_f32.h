@@ -553,11 +553,14 @@ int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, int64_t N, in
  * them, so that past a few hundred a 16-bit weight is the better choice.  Sums
  * are binary32, of x (16 + q) with 16 + zero times the sum of x taken off: their
  * error is that of a sum whose terms are up to four times as large.  For the
- * same reason an infinity in A gives NaN.  No workspace; the rest as for
- * gemm_mixed_epilogue. */
+ * same reason an infinity in A gives NaN.  The workspace, of
+ * gemm_w4_epilogue_workspace_size() bytes, and the rest as for
+ * gemm_mixed_epilogue; M at most 65535 * 64, N at most 2^25. */
+int64_t gemm_w4_epilogue_workspace_size(int64_t M, int64_t N, int64_t K);   /* bytes; -1 if invalid */
 int gemm_w4_epilogue(int format, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint8_t* Q,
                      int64_t ldq, int64_t group, const uint16_t* scales, int64_t ld_scales, const uint16_t* zeros,
-                     int64_t ld_zeros, void* C, int64_t ldc, const gemm_epilogue* epilogue, void* stream);
+                     int64_t ld_zeros, void* C, int64_t ldc, const gemm_epilogue* epilogue, void* workspace,
+                     int64_t workspace_bytes, void* stream);
 
 /* The gradient mode without a product, for a gradient dY that is already
  * there: dZ = dY * act'(Z), and the bias gradient, dZ's column sums.

@@ -128,8 +128,11 @@ def load_library():
         lib.gemm_mixed_epilogue_workspace_size.restype = _i64
         lib.gemm_mixed_epilogue.argtypes = esig + [_vp, _i64, ep, _vp, _i64, _vp]
         lib.gemm_mixed_epilogue.restype = ctypes.c_int
-        lib.gemm_w4_epilogue.argtypes = [ctypes.c_int] + [_i64] * 3 + [_vp, _i64] * 2 + [_i64] + [_vp, _i64] * 3 + [ep, _vp]
+        lib.gemm_w4_epilogue.argtypes = [ctypes.c_int] + [_i64] * 3 + [_vp, _i64] * 2 + [_i64] + [_vp, _i64] * 3 + \
+            [ep, _vp, _i64, _vp]
         lib.gemm_w4_epilogue.restype = ctypes.c_int
+        lib.gemm_w4_epilogue_workspace_size.argtypes = [_i64] * 3
+        lib.gemm_w4_epilogue_workspace_size.restype = _i64
         lib.activation_grad_workspace_size.argtypes = [_i64, _i64]
         lib.activation_grad_workspace_size.restype = _i64
         lib.activation_grad.argtypes = [ctypes.c_int, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
@@ -738,10 +741,11 @@ def linear_w4(X, Q, scales, zeros=None, group_size=128, bias=None, activation="n
         preact = X.new_empty((M, N))
         ep.preact = preact.data_ptr()
         ep.ld_preact = N or 1
-    _check(load_library().gemm_w4_epilogue(
-        fmt, M, N, K, X.data_ptr(), ldx, Q.data_ptr(), ldq, group_size, scales.data_ptr(), lds,
-        None if zeros is None else zeros.data_ptr(), ldz, out.data_ptr(), ldc, ctypes.byref(ep),
-        torch._C._cuda_getCurrentRawStream(device)))
+    lib = load_library()
+    ws, addr, nbytes = _workspace(X, lib.gemm_w4_epilogue_workspace_size(M, N, K))
+    _check(lib.gemm_w4_epilogue(fmt, M, N, K, X.data_ptr(), ldx, Q.data_ptr(), ldq, group_size, scales.data_ptr(), lds,
+                                None if zeros is None else zeros.data_ptr(), ldz, out.data_ptr(), ldc, ctypes.byref(ep),
+                                addr, nbytes, torch._C._cuda_getCurrentRawStream(device)))
     return (out, preact) if return_preact else out
 
 

@@ -31,9 +31,10 @@ FLAGS = ["-O3", f"--offload-arch={ARCH}", "-std=c++17", "-fPIC", "-Wall",
 # Per-source extra flags.  The k-split sources: matrix instructions in their
 # vector-register form -- with the accumulators in AGPRs the register
 # allocator copied every accumulator before each matrix instruction of that
-# kernel.
+# kernel.  The 4-bit weight's: its sums are read by vector instructions after
+# every group of k.
 EXTRA_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]
-               for src in ("mfma16_ksplit.hip", "newton_schulz_ksplit.hip", "linear_ksplit.hip")}
+               for src in ("mfma16_ksplit.hip", "newton_schulz_ksplit.hip", "linear_ksplit.hip", "linear_w4.hip")}
 
 
 def _compile(src: str, resource_usage: bool) -> str:

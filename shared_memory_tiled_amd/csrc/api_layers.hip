@@ -59,6 +59,10 @@ extern "C" int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, in
 
 namespace {
 
+// Blocks of 16 columns and up to 1024 threads, rows by 64 in the second
+// coordinate.
+constexpr int64_t kMaxW4Cols = 1 << 25, kMaxW4Rows = 65535 * 64;
+
 int check_w4(int format, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint8_t* Q,
              int64_t ldq, int64_t group, const uint16_t* scales, int64_t ld_scales, const uint16_t* zeros,
              int64_t ld_zeros, int64_t ldc, const gemm_epilogue* ep) {
@@ -78,8 +82,7 @@ int check_w4(int format, int64_t M, int64_t N, int64_t K, const uint16_t* A, int
     if (!extent_fits(N, bytes, ldq) || !extent_fits(N, groups, ld_scales) ||
         (zeros != nullptr && !extent_fits(N, groups, ld_zeros)))
         return GEMM_F32_ERR_TOO_LARGE;
-    // blocks of 16 columns and up to 1024 threads, rows by 16 in the second coordinate
-    if (N > 1 << 25 || M > 65535 * 16) return GEMM_F32_ERR_TOO_LARGE;
+    if (N > kMaxW4Cols || M > kMaxW4Rows) return GEMM_F32_ERR_TOO_LARGE;
     return GEMM_F32_OK;
 }
 
@@ -90,20 +93,28 @@ W4Args w4_args(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, 
 
 }  // namespace
 
+extern "C" int64_t gemm_w4_epilogue_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxW4Rows || N > kMaxW4Cols || K > INT_MAX) return -1;
+    return M == 0 || N == 0 ? 0 : linear_w4_workspace((int)M, (int)N, (int)K);
+}
+
 extern "C" int gemm_w4_epilogue(int format, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda,
                                 const uint8_t* Q, int64_t ldq, int64_t group, const uint16_t* scales,
                                 int64_t ld_scales, const uint16_t* zeros, int64_t ld_zeros, void* C, int64_t ldc,
-                                const gemm_epilogue* epilogue, void* stream) {
+                                const gemm_epilogue* epilogue, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
     int st = check_w4(format, M, N, K, A, lda, Q, ldq, group, scales, ld_scales, zeros, ld_zeros, ldc, epilogue);
     if (st != GEMM_F32_OK) return st;
     if (M == 0 || N == 0) return GEMM_F32_OK;
     if (C == nullptr) return GEMM_F32_ERR_NULL_PTR;
     if (misaligned_type(C, epilogue->c_type)) return GEMM_F32_ERR_MISALIGNED;
     if (other_matrix(C, ldc, epilogue->residual, epilogue->ld_residual, M)) return GEMM_F32_ERR_INVALID_LD;
+    st = check_workspace(linear_w4_workspace((int)M, (int)N, (int)K), workspace, workspace_bytes);
+    if (st != GEMM_F32_OK) return st;
     if ((st = check_device()) != GEMM_F32_OK) return st;
     return finish(launch_linear_w4(w4_args(M, N, K, A, lda, Q, ldq, group, scales, ld_scales, zeros, ld_zeros),
                                    epilogue_args(format, M, N, C, ldc, epilogue), reinterpret_cast<hipStream_t>(stream),
-                                   format));
+                                   format, workspace));
 }
 
 extern "C" int64_t activation_grad_workspace_size(int64_t M, int64_t N) {

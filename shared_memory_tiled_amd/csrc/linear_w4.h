@@ -14,6 +14,7 @@ struct W4Args {
     const uint16_t* scales; int64_t ld_scales;        // N rows of ceil(K / group)
     const uint16_t* zeros; int64_t ld_zeros;          // likewise, or null: 8
 };
-hipError_t launch_linear_w4(const W4Args& p, const EpilogueArgs& e, hipStream_t s, int format);
+int64_t linear_w4_workspace(int M, int N, int K);
+hipError_t launch_linear_w4(const W4Args& p, const EpilogueArgs& e, hipStream_t s, int format, void* workspace);
 
 }  // namespace gemmf32

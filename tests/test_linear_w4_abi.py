@@ -22,10 +22,11 @@ def lib():
 def call(lib, **kw):
     a = dict(fmt=0, M=8, N=16, K=200, A=FAKE, lda=200, Q=FAKE, ldq=100, group=64, scales=FAKE, lds=4, zeros=FAKE, ldz=4,
              C=FAKE, ldc=16)
+    w = dict(ws=FAKE, ws_bytes=1 << 60)
     e = dict(c_type=0)
     for k, v in kw.items():
-        (a if k in a else e)[k] = v
-    return lib.gemm_w4_epilogue(*a.values(), ctypes.byref(binding.epilogue(**e)), None)
+        (a if k in a else w if k in w else e)[k] = v
+    return lib.gemm_w4_epilogue(*a.values(), ctypes.byref(binding.epilogue(**e)), w["ws"], w["ws_bytes"], None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -42,10 +43,23 @@ def call(lib, **kw):
     (dict(C=FAKE + 1), "MISALIGNED"), (dict(C=FAKE + 2, c_type=2), "MISALIGNED"),
     (dict(M=2 ** 31), "TOO_LARGE"), (dict(ldq=2 ** 62), "TOO_LARGE"), (dict(lds=2 ** 62), "TOO_LARGE"),
     (dict(group=2 ** 40), "TOO_LARGE"), (dict(N=2 ** 26, ldc=2 ** 26), "TOO_LARGE"), (dict(M=2 ** 22, N=1), "TOO_LARGE"),
+    (dict(ws_bytes=-1), "INVALID_DIM"),
     (dict(M=0, A=None, C=None), "OK"), (dict(N=0, ldc=1, Q=None, scales=None, C=None), "OK"),
 ])
 def test_refusals(lib, kw, want):
     assert call(lib, **kw) == CODES["GEMM_F32_OK" if want == "OK" else f"GEMM_F32_ERR_{want}"]
+
+
+def test_workspace(lib):
+    assert lib.gemm_w4_epilogue_workspace_size(1, 0, 64) == 0 and lib.gemm_w4_epilogue_workspace_size(0, 8, 64) == 0
+    for bad in ((-1, 8, 64), (1, -8, 64), (1, 8, -64), (2 ** 22, 8, 64), (1, 2 ** 26, 64), (1, 8, 2 ** 31)):
+        assert lib.gemm_w4_epilogue_workspace_size(*bad) == -1
+    need = lib.gemm_w4_epilogue_workspace_size(40, 256, 16384)           # few columns, a long K
+    assert need > 0 and need % (4 * 40 * 256) == 0
+    big = dict(M=40, N=256, K=16384, lda=16384, ldq=8192, lds=256, ldz=256, ldc=256)
+    assert call(lib, **big, ws_bytes=need - 1) == CODES["GEMM_F32_ERR_WORKSPACE"]
+    assert call(lib, **big, ws=None) == CODES["GEMM_F32_ERR_NULL_PTR"]
+    assert call(lib, **big, ws=FAKE + 4) == CODES["GEMM_F32_ERR_MISALIGNED"]
 
 
 def test_binding_refuses_cpu_tensors():
