@@ -256,21 +256,49 @@ void grouped_activation_kernel(GroupedArgs a, EpilogueArgs e, const uint16_t* dY
     const int c = 8 * (threadIdx.x & 31), w = threadIdx.x >> 5, col = r.tn * kActCols + c;
     const int first = r.tm * kActRows, last = min(first + kActRows, r.rows);
     float sums[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // Four rows' loads in flight: one row after the other, a small layer's pass is
+    // eight times the memory's latency (90 x 171 13 us).  A run across N is loaded
+    // from further down in its row and moved; rows shorter than a run go one by
+    // one.
+    const bool z = e.act != kActNone;
+    const uint16_t* const pre = static_cast<const uint16_t*>(e.preact);
     if (col < e.N) {
-        for (int i = first + w; i < last; i += 8) {
-            const int64_t row = r.begin + i;
-            RawRun<8> y, z;
-            y.load(e.z_type, dY, row * ld + col, e.N - col);
-            float v[8], zv[8];
-            if (e.act != kActNone) z.load(e.z_type, e.preact, row * e.ldz + col, e.N - col);
-            y.values(e.z_type, v);
-            if (e.act != kActNone) {
-                z.values(e.z_type, zv);
-                times_derivative(e.act, zv, v);
-            }
-            if (e.C != nullptr) store_values(e.c_type, e.C, row * e.ldc + col, e.N - col, v);
+        const int from = max(min(col, e.N - 8), 0), by = col - from;
+        auto load = [&](const uint16_t* row) __attribute__((always_inline)) -> u32x4 {
+            u32x4 v = {0, 0, 0, 0};
+            if (e.N >= 8) __builtin_memcpy(&v, row + from, 16);
+            else
+                for (int k = 0; k < e.N; ++k) v[k / 2] |= (unsigned)row[k] << (16 * (k % 2));
+            return v;
+        };
+        auto values = [&](u32x4 v, float (&f)[8]) __attribute__((always_inline)) {
+            RawRun<8> run;
+            v = move_down(v, by);
+            __builtin_memcpy(run.w, &v, 16);
+            run.values(e.z_type, f);
+        };
+        for (int i = first + w; i < last; i += 32) {
+            u32x4 yr[4], zr[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sums[k] += v[k];
+            for (int u = 0; u < 4; ++u) {                  // past the last row: that one again
+                const int64_t row = r.begin + min(i + 8 * u, last - 1);
+                yr[u] = load(dY + row * ld);
+                if (z) zr[u] = load(pre + row * e.ldz);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + 8 * u < last) {
+                    const int64_t row = r.begin + i + 8 * u;
+                    float v[8], zv[8];
+                    values(yr[u], v);
+                    if (z) {
+                        values(zr[u], zv);
+                        times_derivative(e.act, zv, v);
+                    }
+                    if (e.C != nullptr) store_values(e.c_type, e.C, row * e.ldc + col, e.N - col, v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sums[k] += v[k];
+                }
         }
     }
     if (partials == nullptr) return;
@@ -300,7 +328,13 @@ void grouped_sum_kernel(GroupedArgs a, int N, const float* partials, float* out)
     const float* const q = partials + ((int64_t)begin / kActRows + g) * N;
     float s = 0.f;
     if (col < N)
-        for (int i = w; i < tiles; i += 4) s += q[(int64_t)i * N + col];
+        for (int i = w; i < tiles; i += 32) {              // eight loads in flight, added in order
+            float u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = i + 4 * k < tiles ? q[(int64_t)(i + 4 * k) * N + col] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += u[k];
+        }
     part[w][threadIdx.x & 63] = s;
     __syncthreads();
     if (w == 0 && col < N)

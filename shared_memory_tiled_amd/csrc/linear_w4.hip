@@ -90,15 +90,9 @@ __device__ __forceinline__ u32x4 load_edge(const uint16_t* row, int k, int count
         }
         return v;
     }
-    const int from = min(k, count - 8), by = k - from;     // values to move down by
+    const int from = min(k, count - 8);
     __builtin_memcpy(&v, row + from, 16);
-    if (by & 1)
-        v = u32x4{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
-                  __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
-    if (by & 2) v = u32x4{v[1], v[2], v[3], 0};
-    if (by & 4) v = u32x4{v[2], v[3], 0, 0};
-    if (by >= 8) v = u32x4{0, 0, 0, 0};
-    return v;
+    return move_down(v, k - from);
 }
 
 // The scales or zero points of COLS columns for GROUPS groups, in LDS: read from

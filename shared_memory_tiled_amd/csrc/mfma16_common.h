@@ -117,6 +117,18 @@ __device__ __forceinline__ u32x2 read_tr16_off(uint32_t lds_byte_addr, int off) 
     return v;
 }
 
+// Eight 16-bit values moved down by `by` (0 and more) places, zeros above: what a
+// load that was moved down to stay inside a row brought, at its place.
+__device__ __forceinline__ u32x4 move_down(u32x4 v, int by) {
+    if (by & 1)
+        v = u32x4{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
+                  __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
+    if (by & 2) v = u32x4{v[1], v[2], v[3], 0};
+    if (by & 4) v = u32x4{v[2], v[3], 0, 0};
+    if (by >= 8) v = u32x4{0, 0, 0, 0};
+    return v;
+}
+
 // D = A B + C on one 16 x 16 x 32 block (format 0 bfloat16, 1 binary16):
 // lane l supplies A[l % 16][8 (l / 16) .. + 7] and B[8 (l / 16) .. + 7][l %
 // 16]; accumulator register r holds D[4 (l / 16) + r][l % 16].
