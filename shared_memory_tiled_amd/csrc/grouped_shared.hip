@@ -54,6 +54,13 @@ __device__ __forceinline__ void wait_phase(int ahead) {
     else wait_phase<(N > 0 ? N - 1 : 0), C>(ahead);
 }
 
+// 16 bytes at any address that a 16-bit value may have, past the caches: what
+// no one reads soon need not push out what the other blocks read.
+__device__ __forceinline__ void store_streamed(char* p, u32x4 v) {
+    typedef u32x4 Bytes __attribute__((aligned(2)));
+    __builtin_nontemporal_store(v, reinterpret_cast<Bytes*>(p));
+}
+
 // BM rows (64 only with A k-contiguous) x 128 NB columns, BLOCKS to a CU.
 template <int FMT, bool KCA, bool KCB, int BM_, int NB, int STAGES, int BLOCKS, bool DIRECT>
 struct GroupedSharedCore {
@@ -119,7 +126,8 @@ struct GroupedSharedCore {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mfma16x16<FMT>(aq[i], bq[j], acc[i][j]);
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = KCA ? mfma16x16<FMT>(aq[i], bq[j], acc[i][j]) : mfma16x16<FMT>(bq[j], aq[i], acc[i][j]);
         }
     };
     __device__ static __forceinline__ void clear(floatx4 (&acc)[FM][FN]) {
@@ -315,9 +323,20 @@ struct GroupedSharedCore {
                      : "memory");
     }
 
-    // The forward epilogue; thread t holds bias value n0 + t.
+    __device__ static __forceinline__ u32x4 pack(const float (&v)[8]) {
+        using T = typename Stored<FMT>::T;
+        T raw[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw[i] = (T)v[i];
+        u32x4 d;
+        __builtin_memcpy(&d, raw, 16);
+        return d;
+    }
+
+    // The forward epilogue; thread t holds bias value n0 + t.  streamed: C's whole
+    // runs go past the caches.
     __device__ static __forceinline__ void finish(const floatx4 (&acc)[FM][FN], const EpilogueArgs& e, int m0, int n0,
-                                                  float bias, unsigned char* lds) {
+                                                  float bias, bool streamed, unsigned char* lds) {
         const int lane = threadIdx.x & 63;
         const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         float* const shared = reinterpret_cast<float*>(lds + BIAS);
@@ -349,7 +368,16 @@ struct GroupedSharedCore {
                     float b[8];
                     bias_of(col, b);
                     const Run run{};
-                    run.finish_at(e, c_base, __umul24(row, ldc) + col, z_base, __umul24(row, ldz) + col, b, v);
+                    const uint32_t c_at = __umul24(row, ldc) + col, z_at = __umul24(row, ldz) + col;
+                    if (!streamed) return run.finish_at(e, c_base, c_at, z_base, z_at, b, v);
+                    run.apply(
+                        e, b, v,
+                        [&](const float (&z)[8]) __attribute__((always_inline)) {
+                            Run::template store_whole<FMT>(z_base, 2 * z_at, z);
+                        },
+                        [&](const float (&q)[8]) __attribute__((always_inline)) {
+                            store_streamed(c_base + 2 * c_at, pack(q));
+                        });
                 },
                 [](int, int) {});
         } else {
@@ -366,6 +394,79 @@ struct GroupedSharedCore {
                 [](int, int) {});
         }
     }
+
+    // The gradient's, which stores its sums.  Register r of acc[i][j] of lane (c =
+    // l % 16, g = l / 16) is row 16 i + c, column 16 j + 4 g + r of the wave's
+    // span (the matrix instruction gets B's fragment first): a lane's 4 values of
+    // two blocks j, j + 1 become 8 consecutive ones of one by a swap of the lane
+    // groups' halves, and a store of 16 bytes a lane writes 64 bytes of 16 rows.
+    // planes: into binary32 planes of a sum still to be joined.  Whole lines of the
+    // gradient go past the caches, which hold what the other blocks read: 8192 x
+    // 2048 x 4096 over 16 groups 150 us against 204 with ordinary stores (4096 x
+    // 1024 x 2048 over 64 68 against 117); through LDS, as runs of 256 bytes, 158
+    // and 75.  Parts of lines do not: 2000 x 1000 x 1000 over 4 15.3 us against 16.
+    __device__ static __forceinline__ void finish_gradient(const floatx4 (&acc)[FM][FN], const EpilogueArgs& e, int m0,
+                                                           int n0, bool planes, unsigned char* lds) {
+        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+        const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        const int row0 = m0 + 16 * FM * (w / WCOLS), col0 = n0 + 16 * FN * (w % WCOLS);
+        if (row0 >= e.M || col0 >= e.N) return;
+        const int size = e.c_type == 2 ? 4 : 2;
+        if (e.N % 8 != 0 || (size * e.ldc | (int64_t)(uintptr_t)e.C) % 16 != 0)
+            return gradient_runs(acc, e, row0, col0, planes, lds);
+        const bool streamed = !planes && (size * e.ldc | (int64_t)(uintptr_t)e.C) % 64 == 0;
+        const int to = 16 * (g & 1) + 8 * (g >> 1);        // the 8 columns of a pair of blocks a lane stores
+        auto put = [&](int row, int col, u32x4 v) __attribute__((always_inline)) {
+            if (row >= e.M || col >= e.N) return;
+            char* const p = static_cast<char*>(e.C) + size * (row * e.ldc + col);
+            if (streamed) store_streamed(p, v);
+            else __builtin_memcpy(p, &v, 16);
+        };
+#pragma unroll
+        for (int j = 0; j < FN; j += 2) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int row = row0 + 16 * i + c, col = col0 + 16 * j;
+                if (e.c_type == 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) put(row, col + 16 * h + 4 * g, __builtin_bit_cast(u32x4, acc[i][j + h]));
+                    continue;
+                }
+                const floatx4 a = acc[i][j], b = acc[i][j + 1];
+                const u32x4 d = pack({a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+                const auto lo = __builtin_amdgcn_permlane16_swap(d[0], d[2], false, false);
+                const auto hi = __builtin_amdgcn_permlane16_swap(d[1], d[3], false, false);
+                put(row, col + to, u32x4{lo[0], hi[0], lo[1], hi[1]});
+            }
+        }
+    }
+
+    // The same where rows do not begin at 16 bytes: 16 rows at a time through the
+    // wave's patch of LDS, as runs of 8 columns, a wave's span of a row at once
+    // (8192 x 2001 x 2003 over 16 groups 154 us against 188 from the registers).
+    __device__ static __forceinline__ void gradient_runs(const floatx4 (&acc)[FM][FN], const EpilogueArgs& e, int row0,
+                                                         int col0, bool planes, unsigned char* lds) {
+        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+        float* const patch = reinterpret_cast<float*>(lds) + (threadIdx.x >> 6) * Staged::PATCH;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) *reinterpret_cast<floatx4*>(patch + c * Staged::PITCH + 16 * j + 4 * g) = acc[i][j];
+            wave_lds_fence();
+#pragma unroll
+            for (int t = 0; t < FN / 2; ++t) {
+                const int k = 64 * t + lane, row = row0 + 16 * i + k / (2 * FN), at = 8 * (k % (2 * FN)), col = col0 + at;
+                const floatx4* const q = reinterpret_cast<const floatx4*>(patch + k / (2 * FN) * Staged::PITCH + at);
+                const floatx4 lo = q[0], hi = q[1];
+                const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                if (row >= e.M || col >= e.N) continue;
+                const int64_t index = row * e.ldc + col;
+                if (e.c_type == FMT && !planes && col + 8 <= e.N) store_streamed(static_cast<char*>(e.C) + 2 * index, pack(v));
+                else store_values(e.c_type, e.C, index, e.N - col, v);
+            }
+            wave_lds_fence();
+        }
+    }
 };
 
 // Blocks (x, y) of one x split K: y takes k from y k_share on (a multiple of 32)
@@ -374,7 +475,7 @@ struct GroupedSharedCore {
 template <int FMT, bool KCB, int BM, int NB, int STAGES, int BLOCKS, bool DIRECT>
 __global__ __launch_bounds__(256, BLOCKS)
 void grouped_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_n, int group_m, int k_share,
-                           int64_t plane) {
+                           int64_t plane, bool streamed) {
     using Core = GroupedSharedCore<FMT, true, KCB, BM, NB, STAGES, BLOCKS, DIRECT>;
     __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
     const GroupRows r = locate_group_tile<BM>(a, (int)blockIdx.x, tiles_n, group_m);
@@ -392,7 +493,7 @@ void grouped_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tile
     if ((int)threadIdx.x < Core::BN) load_bias(e, n0 + (int)threadIdx.x, bias);
     floatx4 acc[Core::FM][Core::FN];
     Core::run(p, 0, n0, lds, acc);
-    Core::finish(acc, e, m0, n0, bias[0], lds);
+    Core::finish(acc, e, m0, n0, bias[0], streamed, lds);
 }
 
 // The same for the gradient: the group's rows in gridDim.y shares.
@@ -413,18 +514,25 @@ void grouped_grad_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int
     if (r.rows == 0) return zero_tile<Core::BM, Core::BN>(e, m0, n0);
     floatx4 acc[Core::FM][Core::FN];
     Core::run(p, m0, n0, lds, acc);
-    Core::finish(acc, e, m0, n0, 0.0f, lds);
+    Core::finish_gradient(acc, e, m0, n0, splits > 1, lds);
 }
+
+// Outputs from here on go past the caches (a quarter of the 32 MB of the L2s: they
+// would push the operands out).  4096 x 2044 x 2044 over 8 groups 65 us against 78
+// with ordinary stores, 16384 x 4096 x 4096 over 8 558 against 567; 16 x 2048 x
+// 4096 over 16 42 against 41.
+constexpr int64_t kStreamedValues = 4 << 20;
 
 template <int BM, int NB, int STAGES, int BLOCKS, bool DIRECT>
 void launch(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format, int op_b,
             int k_share, int64_t plane) {
     constexpr int kGroupM = 1024 / BM;
+    const bool streamed = DIRECT && e.c_type == format && (int64_t)a.rows * p.N >= kStreamedValues;
     const int tn = ceil_div(p.N, 128 * NB);
     const dim3 g((unsigned)(grouped_row_tiles(a.rows, a.groups, BM) * tn), p.K > 0 ? (unsigned)ceil_div(p.K, k_share) : 1u), b(256);
     auto run = [&](auto fmt, auto kcb) {
         hipLaunchKernelGGL((grouped_shared_kernel<decltype(fmt)::value, decltype(kcb)::value, BM, NB, STAGES, BLOCKS,
-                                                  DIRECT>), g, b, 0, s, a, p, e, tn, kGroupM, k_share, plane);
+                                                  DIRECT>), g, b, 0, s, a, p, e, tn, kGroupM, k_share, plane, streamed);
     };
     if (format == 0 && op_b) run(std::integral_constant<int, 0>{}, std::true_type{});
     else if (format == 0) run(std::integral_constant<int, 0>{}, std::false_type{});
