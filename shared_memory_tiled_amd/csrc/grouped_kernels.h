@@ -38,6 +38,7 @@ namespace {
 struct GroupRows {
     int group, begin, rows;            // of the group; rows < 0: none for this block
     int tm, tn;                        // the tile within the group
+    int quarter;                       // of the tile; -1: all of it
 };
 
 __device__ __forceinline__ void group_range(const GroupedArgs& a, int g, int* begin, int* end) {
@@ -59,8 +60,9 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
 // Block b's tile among the groups' tiles of TILE rows x tiles_n columns, in the
 // order of the groups, within one as grouped_tile orders them, each XCD walking
 // a contiguous run.  Every wave computes it for itself: 64 groups at a time, a
-// lane each.
-template <int TILE>
+// lane each.  ROUND > 0: the tiles past a whole number of rounds of ROUND, if they
+// are a quarter of one or less, go to four blocks each, which follow the others.
+template <int TILE, int ROUND = 0>
 __device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int b, int tiles_n, int group_m) {
     const int lane = threadIdx.x & 63;
     int begin = 0, end = 0, incl = 0, total = 0;
@@ -71,10 +73,22 @@ __device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int
         incl = wave_inclusive_sum((end - begin + TILE - 1) / TILE);
         total += __builtin_amdgcn_readlane(incl, 63);
     }
-    GroupRows r{0, 0, -1, 0, 0};
-    const int blocks = total * tiles_n;
-    if (b >= blocks) return r;
-    const int logical = xcd_contiguous(b, blocks);
+    GroupRows r{0, 0, -1, 0, 0, -1};
+    int blocks = total * tiles_n, rest = 0;
+    if constexpr (ROUND > 0) {
+        rest = blocks % ROUND;
+        if (rest > ROUND / 4) rest = 0;
+        blocks -= rest;
+    }
+    if (b >= blocks + 4 * rest) return r;
+    int logical;
+    if (b < blocks) {
+        logical = xcd_contiguous(b, blocks);
+    } else {
+        const int q = xcd_contiguous(b - blocks, 4 * rest);
+        logical = blocks + q / 4;
+        r.quarter = q % 4;
+    }
     const int row = logical / tiles_n;                      // row tile if the tiles went row by row
     int before = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {

@@ -472,16 +472,42 @@ struct GroupedSharedCore {
 // Blocks (x, y) of one x split K: y takes k from y k_share on (a multiple of 32)
 // and stores its sums as plane y, `plane` floats after the one before (then e is
 // that matrix, without a layer's epilogue); k_share = K: not split.
+// The 128 x 256 tiles past whole rounds of the 512 that the chip holds would run
+// alone on their CUs, at half its rate; a quarter of a round or less of them goes
+// to four times the blocks of 64 x 128, whose six stages take no more LDS: 8192 x
+// 2048 x 4096 over 16 groups with transposed weights 192 us against 221, 16384 x
+// 4096 x 4096 over 8 544 against 560 (up to half a round: 12000 x 4096 x 4096 over
+// 8 388 us against 404, but 5000 213 against 199 and 9000 323 against 311).
+constexpr bool quarters(int bm, int nb, bool direct) { return direct && bm == 128 && nb == 2; }
+constexpr int kRound = 512;
+
 template <int FMT, bool KCB, int BM, int NB, int STAGES, int BLOCKS, bool DIRECT>
 __global__ __launch_bounds__(256, BLOCKS)
 void grouped_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_n, int group_m, int k_share,
                            int64_t plane, bool streamed) {
     using Core = GroupedSharedCore<FMT, true, KCB, BM, NB, STAGES, BLOCKS, DIRECT>;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
-    const GroupRows r = locate_group_tile<BM>(a, (int)blockIdx.x, tiles_n, group_m);
+    constexpr bool QUARTERS = quarters(BM, NB, DIRECT);
+    using Quarter = GroupedSharedCore<FMT, true, KCB, 64, 1, QUARTERS ? 6 : 2, 2, DIRECT>;
+    constexpr int LDS_BYTES = QUARTERS && Quarter::LDS_BYTES > Core::LDS_BYTES ? Quarter::LDS_BYTES : Core::LDS_BYTES;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[LDS_BYTES];
+    const GroupRows r = locate_group_tile<BM, QUARTERS ? kRound : 0>(a, (int)blockIdx.x, tiles_n, group_m);
     if (r.rows < 0) return;
     enter_group(a, r, &p, &e);
-    const int m0 = BM * r.tm, n0 = Core::BN * r.tn;
+    int m0 = BM * r.tm, n0 = Core::BN * r.tn;
+    if constexpr (QUARTERS) {
+        if (r.quarter >= 0) {
+            m0 += 64 * (r.quarter >> 1);
+            n0 += 128 * (r.quarter & 1);
+            if (m0 >= r.rows || n0 >= p.N) return;
+            p.A += (int64_t)m0 * p.lda;
+            p.M = min(r.rows - m0, 64);
+            float bias[1] = {0.0f};
+            if ((int)threadIdx.x < Quarter::BN) load_bias(e, n0 + (int)threadIdx.x, bias);
+            floatx4 acc[Quarter::FM][Quarter::FN];
+            Quarter::run(p, 0, n0, lds, acc);
+            return Quarter::finish(acc, e, m0, n0, bias[0], streamed, lds);
+        }
+    }
     p.A += (int64_t)m0 * p.lda;
     p.M = min(r.rows - m0, BM);
     const int k0 = (int)blockIdx.y * k_share;
@@ -529,7 +555,9 @@ void launch(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hi
     constexpr int kGroupM = 1024 / BM;
     const bool streamed = DIRECT && e.c_type == format && (int64_t)a.rows * p.N >= kStreamedValues;
     const int tn = ceil_div(p.N, 128 * NB);
-    const dim3 g((unsigned)(grouped_row_tiles(a.rows, a.groups, BM) * tn), p.K > 0 ? (unsigned)ceil_div(p.K, k_share) : 1u), b(256);
+    const int64_t tiles = grouped_row_tiles(a.rows, a.groups, BM) * tn;
+    const int64_t more = quarters(BM, NB, DIRECT) ? 3 * std::min<int64_t>(tiles, kRound / 4) : 0;
+    const dim3 g((unsigned)(tiles + more), p.K > 0 ? (unsigned)ceil_div(p.K, k_share) : 1u), b(256);
     auto run = [&](auto fmt, auto kcb) {
         hipLaunchKernelGGL((grouped_shared_kernel<decltype(fmt)::value, decltype(kcb)::value, BM, NB, STAGES, BLOCKS,
                                                   DIRECT>), g, b, 0, s, a, p, e, tn, kGroupM, k_share, plane, streamed);
