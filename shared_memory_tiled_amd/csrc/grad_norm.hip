@@ -16,7 +16,13 @@
 // binary32 result.  Each block leaves one partial sum; partials are added in a
 // fixed order, without atomics, by one block for the norm alone and by every
 // block of the second pass for itself when both are asked for (16 KB from the
-// L2 against a launch of its own).
+// L2 against a launch of its own).  The scaled values are the one rounding.
+//
+// Measured: 0.81e9 bf16 values in 161 tensors, into other tensors, 902 us: the
+// norm 300 (5.4 TB/s), the second pass 638 alone (5.1 TB/s; a copy reaches 5.2).
+// Read and stored through the caches as ordinary accesses do, the pass took 667
+// and the call 976 (0.11e9 values in 121 tensors 131 us against 168).  Taking the
+// values in the reverse order, the last read first, gained nothing.
 #include "epilogue.h"
 #include "grad_norm.h"
 
@@ -121,6 +127,9 @@ void grad_norm_kernel(const double* partials, int count, float* norm) {
     if (threadIdx.x == 0) *norm = n;
 }
 
+// 16 bytes that no one reads again soon.
+typedef unsigned int Streamed __attribute__((ext_vector_type(4), aligned(2)));
+
 template <int TYPE>
 __device__ __forceinline__ void scale(const void* in, void* out, int64_t from, int64_t n, float factor) {
     using T = typename Stored<TYPE>::T;
@@ -137,13 +146,18 @@ __device__ __forceinline__ void scale(const void* in, void* out, int64_t from, i
         T v[U][V];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (j + u * kThreads < vectors) __builtin_memcpy(v[u], p + (j + u * kThreads) * V, 16);
+            if (j + u * kThreads < vectors) {
+                const Streamed d = __builtin_nontemporal_load(reinterpret_cast<const Streamed*>(p + (j + u * kThreads) * V));
+                __builtin_memcpy(v[u], &d, 16);
+            }
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (j + u * kThreads < vectors) {
 #pragma unroll
                 for (int k = 0; k < V; ++k) v[u][k] = (T)((float)v[u][k] * factor);
-                __builtin_memcpy(q + (j + u * kThreads) * V, v[u], 16);
+                Streamed d;
+                __builtin_memcpy(&d, v[u], 16);
+                __builtin_nontemporal_store(d, reinterpret_cast<Streamed*>(q + (j + u * kThreads) * V));
             }
     }
     const int64_t at = vectors * V + threadIdx.x;
