@@ -104,19 +104,23 @@ Plan make_plan(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
     return q;
 }
 
-// The weights' gradient: 128 x 256 tiles from two rounds of them on (8192 x 2048
-// x 4096 over 16 groups 196 us against 208; 16384 x 4096 x 4096 over 8 498 against
-// 553), 128 x 128 below; few tiles with long groups split the rows.
+// The weights' gradient: 128 x 256 tiles for groups of 384 rows and more that make
+// about one whole round of the 512 on the chip or two and more (16384 x 2048 x 4096
+// over 2 groups 249 us against 294 on 128 x 128, 8192 x 2048 x 4096 over 16 147
+// against 161), else 128 x 128, which store sooner (4096 x 1024 x 2048 over 64 63
+// us against 70, 2000 x 1000 x 1000 over 4 15 against 20); few tiles with long
+// groups split the rows.
 Plan make_grad_plan(const GroupedArgs& a, const Gemm16Args& p) {
     Plan q{};
     q.splits = 1;
     q.direct = direct_grad_fits(a, p);
     q.bm = 128;
     const int64_t wide = (int64_t)a.groups * ceil_div(p.M, 128) * ceil_div(p.N, 256);
-    q.bn = q.direct && wide >= 1024 ? 256 : 128;
+    const double rows = a.rows / used_groups(a.groups, a.rows > 0 ? a.rows : 1);
+    q.bn = q.direct && rows >= 384 && ((wide >= 448 && wide <= 512) || wide >= 1024) ? 256 : 128;
     if (q.bn == 256) return q;
     const double tiles = (double)a.groups * ceil_div(p.M, 128) * ceil_div(p.N, 128);
-    const double phases = ceil(a.rows / used_groups(a.groups, a.rows > 0 ? a.rows : 1) / 32.0);
+    const double phases = ceil(rows / 32.0);
     double least = 1e30;
     for (int splits = 1; splits <= 32 && (splits == 1 || (tiles * splits <= 768 && phases >= 8 * splits)); splits *= 2) {
         const double t = tiles_time(kShapes[1], tiles * splits, phases / splits) +

@@ -21,10 +21,11 @@ def test_tiles_left_over(counts, N, K, op_b):
     check_forward(counts, N, K, torch.float16, "relu", op_b, bias=False, preact=False, strides=True)
 
 
-# weights' gradients of 1024 tiles and more; rows of whole lines, of 16 bytes, of neither
+# weights' gradients of many tiles, of groups of few rows and of many; rows of whole lines, of 16 bytes, of neither
 @pytest.mark.parametrize("counts,N,K", [([40] * 63 + [0], 512, 1024), ([3, 100, 0, 61] * 16, 520, 1000),
-                                        ([33] * 70, 514, 998), ([50] * 65, 333, 1003)],
-                         ids=["lines", "runs", "even", "odd"])
+                                        ([33] * 70, 514, 998), ([50] * 65, 333, 1003), ([900, 0, 700], 2048, 4096),
+                                        ([420, 380], 2056, 3600), ([385], 3850, 4090)],
+                         ids=["lines", "runs", "even", "odd", "few", "few_runs", "one"])
 @pytest.mark.parametrize("op_b", ["N", "T"])
 def test_gradients_of_many_groups(counts, N, K, op_b):
     check_backward(counts, N, K, torch.bfloat16, "gelu_tanh", op_b)
