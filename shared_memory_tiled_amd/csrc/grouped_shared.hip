@@ -207,9 +207,11 @@ struct GroupedSharedCore {
         const Fragments fragments(lds, lane, w);
         clear(acc);
         const int phases = ceil_div(p.K, BK);
+        const int turn = KCA ? 0 : (int)((m0 / BM + n0 / BN) % phases);
+        auto turned = [&](int ph) __attribute__((always_inline)) { return KCA ? ph : ph + turn < phases ? ph + turn : ph + turn - phases; };
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s)
-            if (s < phases) copies(s, s);
+            if (s < phases) copies(turned(s), s);
         int stage = 0;
         for (int ph = 0; ph < phases; ++ph) {
             // This phase's copies of this wave have landed (those of the next ones
@@ -218,7 +220,7 @@ struct GroupedSharedCore {
             wait_phase<STAGES - 2, COPIES>(phases - 1 - ph);
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            if (ph + STAGES - 1 < phases) copies(ph + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+            if (ph + STAGES - 1 < phases) copies(turned(ph + STAGES - 1), stage == 0 ? STAGES - 1 : stage - 1);
             if ((KCA || KCB) && ph == phases - 1 && p.K % 8 != 0) cut_runs(lds + stage * STAGE, p.K % 32);
             fragments.multiply(stage, acc);
             stage = stage == STAGES - 1 ? 0 : stage + 1;
@@ -404,7 +406,11 @@ struct GroupedSharedCore {
     // gradient go past the caches, which hold what the other blocks read: 8192 x
     // 2048 x 4096 over 16 groups 150 us against 204 with ordinary stores (4096 x
     // 1024 x 2048 over 64 68 against 117); through LDS, as runs of 256 bytes, 158
-    // and 75.  Parts of lines do not: 2000 x 1000 x 1000 over 4 15.3 us against 16.
+    // and 75.  That is with its factors in the last-level cache; within a backward
+    // pass they come from memory, and it gains less: the pass over 2048 x 512 x
+    // 1024 and 64 groups 47 us against 57, 1024 x 4096 x 4096 and 8 215 against 232,
+    // 8192 x 2048 x 4096 and 16 391 against 400.  Parts of lines go through the
+    // caches: 2000 x 1000 x 1000 over 4 15.3 us against 16.
     __device__ static __forceinline__ void finish_gradient(const floatx4 (&acc)[FM][FN], const EpilogueArgs& e, int m0,
                                                            int n0, bool planes, unsigned char* lds) {
         const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
