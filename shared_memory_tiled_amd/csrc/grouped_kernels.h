@@ -100,19 +100,22 @@ __device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int
         const int sum = __builtin_amdgcn_readlane(incl, 63);
         if (row < before + sum) {
             const uint64_t past = __builtin_amdgcn_ballot_w64(before + incl > row);
+            if (past == 0) return r;
             const int l = __builtin_ctzll(past);
             r.group = g0 + l;
             r.begin = __builtin_amdgcn_readlane(begin, l);
-            r.rows = __builtin_amdgcn_readlane(end, l) - r.begin;
-            const int tiles_m = (r.rows + TILE - 1) / TILE;
+            const int rows = __builtin_amdgcn_readlane(end, l) - r.begin;
+            const int tiles_m = (rows + TILE - 1) / TILE;
             const int first = before + __builtin_amdgcn_readlane(incl, l) - tiles_m;
             const int local = logical - first * tiles_n;
-            const int gsize = group_m * tiles_n;
+            const int gsize = min(group_m, tiles_m) * tiles_n;
             const int q = local / gsize, first_m = q * group_m;
             const int gm = min(tiles_m - first_m, group_m);
             const int in_q = local - q * gsize;
             r.tm = first_m + in_q % gm;
             r.tn = in_q / gm;
+            // offsets that decrease can make more tiles than an int counts
+            if ((unsigned)r.tm < (unsigned)tiles_m && (unsigned)r.tn < (unsigned)tiles_n) r.rows = rows;
             return r;
         }
         before += sum;

@@ -6,7 +6,10 @@ from __future__ import annotations
 import pytest
 import torch
 
-from test_gpu_grouped import check_backward, check_forward
+import layer_refs as R
+from gpu_support import say
+from shared_memory_tiled_amd import binding
+from test_gpu_grouped import check_backward, check_forward, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +34,56 @@ def test_gradients_of_many_groups(counts, N, K, op_b):
     check_backward(counts, N, K, torch.bfloat16, "gelu_tanh", op_b)
     check_backward(counts, N, K, torch.float16, "none", op_b, wdt=torch.float32)
     check_backward(counts, N, K, torch.bfloat16, "none", op_b, strides=True)
+
+
+@pytest.mark.parametrize("M,N", [(3, (1 << 20) + 3), (70, 1 << 21), (1, 600001)], ids=str)
+def test_activation_of_wide_rows(M, N):
+    """More tiles side by side than a run of tiles down a group holds."""
+    say(f"grouped activation of wide rows {M} {N}")
+    dY, z = normal(1, M, N), normal(2, M, N)
+    ends = [0, M // 2, M]
+    dZ, db = binding.grouped_activation_backward(dY, torch.tensor(ends, dtype=torch.int32, device="cuda"), z, "silu")
+    torch.cuda.synchronize()
+    d = dY.double() * R.act_derivative(z.double(), "silu")
+    R.within(dZ, d, R.HALF[dY.dtype] * d.abs() + 32 * R.U * dY.double().abs(), "dZ")
+    for g, (a, e) in enumerate(zip(ends, ends[1:])):
+        tol = 32 * R.U * dY[a:e].double().abs().sum(0) + (e - a + 8) * R.U * d[a:e].abs().sum(0)
+        R.within(db[g], d[a:e].sum(0), tol, f"db of group {g}")
+
+
+@pytest.mark.parametrize("M,ld", [(4500, 1 << 20), (1100, 1 << 22)], ids=str)
+@pytest.mark.parametrize("op_b", ["N", "T"])
+def test_far_apart(M, ld, op_b):
+    """Rows and weights whose places pass 2^32 bytes and 2^32 elements."""
+    say(f"grouped far apart {M} {ld} {op_b}")
+    K, N, stride = 64, 72, (1 << 31) + 8
+    cuts = [0, M // 3, M // 3 + 5, M]
+    offsets = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+
+    def far(t):
+        view = torch.empty(M * ld, dtype=t.dtype, device="cuda").view(M, ld)[:, :t.shape[1]]
+        return view.copy_(t)
+
+    X, W, dY = normal(1, M, K), normal(2, 3, K, N, scale=K ** -0.5), normal(3, M, N)
+    Wd = W.transpose(1, 2).contiguous() if op_b == "T" else W
+    Wf = torch.empty(2 * stride + K * N, dtype=W.dtype, device="cuda").as_strided(Wd.shape, (stride, Wd.shape[2], 1))
+    Wf.copy_(Wd)
+    Xf, dYf, out = far(X), far(dY), far(torch.zeros_like(dY))
+    y = binding.grouped_linear(Xf, Wf, offsets, activation="silu", out=out, op_b=op_b)
+    dX, dW, db = binding.grouped_linear_backward(dYf, Xf, Wf, offsets, preact=out, activation="silu", op_b=op_b)
+    assert y is out
+    dt = X.dtype
+    for g, (a, e) in enumerate(zip(cuts, cuts[1:])):
+        Y, Z, S = R.linear_ref(X[a:e], W[g], None, "silu", None)
+        R.within(y[a:e], Y, R.linear_tol(Y, Z, S, K, "silu", None, dt), f"group {g}")
+        d = dY[a:e].double() * R.act_derivative(out[a:e].double(), "silu")
+        ed = R.HALF[dt] * d.abs() + 32 * R.U * dY[a:e].double().abs()
+        Wg, Xg = W[g].double(), X[a:e].double()
+        ref = d @ Wg.t().contiguous()
+        tol = R.HALF[dt] * ref.abs() + (ed + (N + 2) * R.U * d.abs()) @ Wg.abs().t().contiguous() * 1.01
+        R.within(dX[a:e], ref, tol, f"dX of group {g}")
+        ref = Xg.t().contiguous() @ d
+        tol = R.HALF[dt] * ref.abs() + Xg.abs().t().contiguous() @ (ed + (e - a + 2) * R.U * d.abs()) * 1.01
+        R.within(dW[g].t() if op_b == "T" else dW[g], ref, tol, f"dW of group {g}")
+        tol = 32 * R.U * dY[a:e].double().abs().sum(0) + (e - a + 8) * R.U * d.abs().sum(0)
+        R.within(db[g], d.sum(0), tol, f"db of group {g}")

@@ -216,3 +216,23 @@ def test_streams_and_graph_replay():
         torch.cuda.synchronize()
         for o in outs:
             assert torch.equal(o, eager)
+
+
+def test_far_apart():
+    """Rows of the weight, its scales and the result whose places pass 2^32 bytes."""
+    M, N, K, ld = 3, 70000, 256, 1 << 16
+    say(f"linear_w4 far apart {N} {ld}")
+    q, Q, scales, z = weight(N, K, 64, torch.bfloat16, True)
+    X = torch.randn(M, K, generator=generator(5), device="cuda").bfloat16()
+    want = binding.linear_w4(X, Q, scales, zeros=z, group_size=64)
+
+    def far(t, ld):
+        return torch.empty(t.shape[0] * ld, dtype=t.dtype, device="cuda").view(-1, ld)[:, :t.shape[1]].copy_(t)
+
+    out = far(torch.zeros_like(want), 1 << 31)
+    got = binding.linear_w4(X, far(Q, ld), far(scales, ld // 2), zeros=far(z, ld), group_size=64, out=out)
+    assert got is out and torch.equal(got, want)
+    W = scales.double().repeat_interleave(64, 1) * (q.double() - z.double().repeat_interleave(64, 1))
+    big = scales.double().repeat_interleave(64, 1) * (32 + q.double() + z.double().repeat_interleave(64, 1))
+    Y = X.double() @ W.t().contiguous()
+    R.within(want, Y, R.HALF[X.dtype] * Y.abs() + 94 * R.U * (X.double().abs() @ big.t().contiguous()), "out")
