@@ -18,10 +18,10 @@
 // block of the second pass for itself when both are asked for (16 KB from the
 // L2 against a launch of its own).  The scaled values are the one rounding.
 //
-// Measured: 0.81e9 bf16 values in 161 tensors, into other tensors, 902 us: the
+// Measured: 0.82e9 bf16 values in 161 tensors, into other tensors, 902 us: the
 // norm 300 (5.4 TB/s), the second pass 638 alone (5.1 TB/s; a copy reaches 5.2).
 // Read and stored through the caches as ordinary accesses do, the pass took 667
-// and the call 976 (0.11e9 values in 121 tensors 131 us against 168).  Taking the
+// and the call 976 (0.13e9 values in 121 tensors 131 us against 168).  Taking the
 // values in the reverse order, the last read first, gained nothing.
 #include "epilogue.h"
 #include "grad_norm.h"

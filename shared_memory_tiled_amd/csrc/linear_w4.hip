@@ -30,6 +30,12 @@
 // each stores its plane of sums and the epilogue pass adds them in order.
 // Columns past N and rows past M repeat the last one and are not stored; values
 // of x past K are zero, whatever the weight's bytes hold there.
+//
+// Measured in a graph, 128 k to a scale: 1 x 4096 x 4096 bf16 6.9 us (7.3 with the
+// weight in memory; a launch, one load's latency and a block's sum), 1 x 8192 x
+// 8192 11.6 (15.3, 2.3 TB/s), 16 x 8192 x 8192 16.5, 64 x 4096 x 4096 13.4, 256 x
+// 4096 x 4096 29: past a few rows the expansion bounds it, two operations for every
+// pair of values and 64 rows.
 #include "epilogue.h"
 #include "linear_w4.h"
 #include "mfma16_common.h"
