@@ -60,10 +60,11 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
 // Block b's tile among the groups' tiles of TILE rows x tiles_n columns, in the
 // order of the groups, within one as grouped_tile orders them, each XCD walking
 // a contiguous run.  Every wave computes it for itself: 64 groups at a time, a
-// lane each.  ROUND > 0: the tiles past a whole number of rounds of ROUND, if they
+// lane each.  round > 0: the tiles past a whole number of rounds of `round`, if they
 // are a quarter of one or less, go to four blocks each, which follow the others.
-template <int TILE, int ROUND = 0>
-__device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int b, int tiles_n, int group_m) {
+template <int TILE>
+__device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int b, int tiles_n, int group_m,
+                                                       int round = 0) {
     const int lane = threadIdx.x & 63;
     int begin = 0, end = 0, incl = 0, total = 0;
     const bool one = a.groups <= 64;
@@ -75,9 +76,9 @@ __device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int
     }
     GroupRows r{0, 0, -1, 0, 0, -1};
     int blocks = total * tiles_n, rest = 0;
-    if constexpr (ROUND > 0) {
-        rest = blocks % ROUND;
-        if (rest > ROUND / 4) rest = 0;
+    if (round > 0) {
+        rest = blocks % round;
+        if (rest > round / 4) rest = 0;
         blocks -= rest;
     }
     if (b >= blocks + 4 * rest) return r;

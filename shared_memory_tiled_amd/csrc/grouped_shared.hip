@@ -490,7 +490,8 @@ struct GroupedSharedCore {
 // to four times the blocks of 64 x 128, whose six stages take no more LDS: 8192 x
 // 2048 x 4096 over 16 groups with transposed weights 192 us against 221, 16384 x
 // 4096 x 4096 over 8 544 against 560 (up to half a round: 12000 x 4096 x 4096 over
-// 8 388 us against 404, but 5000 213 against 199 and 9000 323 against 311).
+// 8 388 us against 404, but 5000 213 against 199 and 9000 323 against 311).  Not
+// where K is split: there one round holds every block.
 constexpr bool quarters(int bm, int nb, bool direct) { return direct && bm == 128 && nb == 2; }
 constexpr int kRound = 512;
 
@@ -503,7 +504,7 @@ void grouped_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tile
     using Quarter = GroupedSharedCore<FMT, true, KCB, 64, 1, QUARTERS ? 6 : 2, 2, DIRECT>;
     constexpr int LDS_BYTES = QUARTERS && Quarter::LDS_BYTES > Core::LDS_BYTES ? Quarter::LDS_BYTES : Core::LDS_BYTES;
     __shared__ __attribute__((aligned(16))) unsigned char lds[LDS_BYTES];
-    const GroupRows r = locate_group_tile<BM, QUARTERS ? kRound : 0>(a, (int)blockIdx.x, tiles_n, group_m);
+    const GroupRows r = locate_group_tile<BM>(a, (int)blockIdx.x, tiles_n, group_m, QUARTERS && gridDim.y == 1 ? kRound : 0);
     if (r.rows < 0) return;
     enter_group(a, r, &p, &e);
     int m0 = BM * r.tm, n0 = Core::BN * r.tn;
@@ -569,8 +570,9 @@ void launch(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hi
     const bool streamed = DIRECT && e.c_type == format && (int64_t)a.rows * p.N >= kStreamedValues;
     const int tn = ceil_div(p.N, 128 * NB);
     const int64_t tiles = grouped_row_tiles(a.rows, a.groups, BM) * tn;
-    const int64_t more = quarters(BM, NB, DIRECT) ? 3 * std::min<int64_t>(tiles, kRound / 4) : 0;
-    const dim3 g((unsigned)(tiles + more), p.K > 0 ? (unsigned)ceil_div(p.K, k_share) : 1u), b(256);
+    const int shares = p.K > 0 ? ceil_div(p.K, k_share) : 1;
+    const int64_t more = quarters(BM, NB, DIRECT) && shares == 1 ? 3 * std::min<int64_t>(tiles, kRound / 4) : 0;
+    const dim3 g((unsigned)(tiles + more), (unsigned)shares), b(256);
     auto run = [&](auto fmt, auto kcb) {
         hipLaunchKernelGGL((grouped_shared_kernel<decltype(fmt)::value, decltype(kcb)::value, BM, NB, STAGES, BLOCKS,
                                                   DIRECT>), g, b, 0, s, a, p, e, tn, kGroupM, k_share, plane, streamed);

@@ -87,3 +87,43 @@ def test_far_apart(M, ld, op_b):
         R.within(dW[g].t() if op_b == "T" else dW[g], ref, tol, f"dW of group {g}")
         tol = 32 * R.U * dY[a:e].double().abs().sum(0) + (e - a + 8) * R.U * d.abs().sum(0)
         R.within(db[g], d.sum(0), tol, f"db of group {g}")
+
+
+def uneven(M, groups):
+    """M rows over groups of unequal sizes, one of them empty if there are several."""
+    if groups == 1:
+        return [M]
+    weights = [1 + (5 * g) % 7 for g in range(groups)]
+    weights[groups // 2] = 0
+    counts = [M * w // sum(weights) for w in weights]
+    counts[-1] += M - sum(counts)
+    return counts
+
+
+# rows, widths and depths at which the choice of tile and of the split of K changes
+CHOICES = [(1, 300, 1000, 1000), (1, 300, 500, 2102), (1, 300, 166, 4096), (1, 1000, 2000, 1000), (1, 1000, 1000, 6432),
+           (1, 1000, 2000, 4096), (1, 2000, 166, 8192), (1, 2000, 2000, 4096), (1, 4000, 1000, 6432),
+           (1, 4000, 2000, 2102), (1, 4000, 2000, 4096), (1, 9000, 166, 4096), (1, 9000, 166, 6432), (1, 9000, 1000, 1000),
+           (3, 300, 500, 2102), (3, 300, 166, 6432), (3, 300, 2000, 6432), (3, 2000, 1000, 4096), (3, 1000, 2000, 6432),
+           (3, 2000, 2000, 6432), (3, 4000, 500, 4096), (3, 4000, 1000, 4096), (3, 4000, 2000, 6432), (3, 9000, 166, 4096),
+           (22, 300, 500, 1000), (22, 300, 166, 8192), (22, 300, 2000, 2102), (22, 1000, 166, 6432), (22, 1000, 500, 4096),
+           (22, 1000, 1000, 2102), (22, 1000, 2000, 4096), (22, 4000, 500, 6432), (22, 9189, 166, 6432),
+           (22, 4000, 1000, 6432), (22, 4000, 2000, 1000), (22, 4000, 2000, 2102), (22, 9000, 2000, 1000)]
+
+
+@pytest.mark.parametrize("case", CHOICES, ids=str)
+@pytest.mark.parametrize("op_b", ["N", "T"])
+def test_choices(case, op_b):
+    groups, M, N, K = case
+    check_forward(uneven(M, groups), N, K, torch.bfloat16, "none", op_b, residual=False, preact=False)
+    check_forward(uneven(M, groups), N, K + 2, torch.float16, "gelu", op_b, lead=3, tail=1)
+
+
+@pytest.mark.parametrize("case", [(1, 16384, 256, 256), (1, 9000, 512, 300), (2, 8000, 200, 304), (4, 8000, 1000, 1000),
+                                  (3, 2000, 1000, 500), (22, 9189, 166, 500), (22, 9189, 500, 1000), (1, 4000, 2048, 3900),
+                                  (6, 16384, 128, 640), (1, 700, 64, 64)], ids=str)
+@pytest.mark.parametrize("op_b", ["N", "T"])
+def test_gradient_choices(case, op_b):
+    groups, M, N, K = case
+    check_backward(uneven(M, groups), N, K, torch.bfloat16, "none", op_b)
+    check_backward(uneven(M, groups), N, K, torch.float16, "silu", op_b, wdt=torch.float32, lead=1, tail=2)
