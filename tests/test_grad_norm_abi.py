@@ -97,3 +97,16 @@ def test_binding_refuses():
 ])
 def test_dense(shape, stride, dense):
     assert binding._dense(torch.empty(64).as_strided(shape, stride)) is dense
+
+
+def test_lists_of_other_things():
+    import torch
+
+    t = torch.zeros(3)
+    for bad in ([t], [None], [t, None], [3.0], ["x"]):
+        with pytest.raises(TypeError):
+            binding.grad_norm(bad)
+        with pytest.raises(TypeError):
+            binding.clip_grads(bad, t, 1.0)
+        with pytest.raises(TypeError):
+            binding.clip_grad_norm(bad, 1.0)
