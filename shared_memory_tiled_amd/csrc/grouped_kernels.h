@@ -35,6 +35,17 @@ inline int64_t grouped_row_tiles(int64_t rows, int64_t groups, int64_t tile) {
 #if defined(__HIPCC__)
 namespace {
 
+// Share i of a group's rows among `splits` blocks: whole steps of 32 rows, the
+// last ones cut off or empty.  In 64 bits: the rows reach 2^31 - 1.
+struct RowShare {
+    int first, rows;
+};
+__host__ __device__ __forceinline__ RowShare row_share(int rows, int splits, int i) {
+    const int64_t share = ((int64_t)rows + 32 * splits - 1) / (32 * splits) * 32, skip = i * share;
+    const int first = skip < rows ? (int)skip : rows;
+    return {first, share < rows - first ? (int)share : rows - first};
+}
+
 struct GroupRows {
     int group, begin, rows;            // of the group; rows < 0: none for this block
     int tm, tn;                        // the tile within the group

@@ -544,10 +544,10 @@ void grouped_grad_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int
     using Core = GroupedSharedCore<FMT, false, false, 128, NB, STAGES, BLOCKS, DIRECT>;
     __shared__ __attribute__((aligned(16))) unsigned char lds[Core::LDS_BYTES];
     GroupRows r = locate_grad_tile(a, (int)blockIdx.x, tiles_m, tiles_n, group_m);
-    const int splits = (int)gridDim.y, share = (r.rows + 32 * splits - 1) / (32 * splits) * 32;
-    const int skip = min((int)blockIdx.y * share, r.rows);
-    r.begin += skip;
-    r.rows = min(r.rows - skip, share);
+    const int splits = (int)gridDim.y;
+    const RowShare share = row_share(r.rows, splits, (int)blockIdx.y);
+    r.begin += share.first;
+    r.rows = share.rows;
     enter_grad_group(a, r, &p, &e);
     e.C = static_cast<char*>(e.C) + 4 * (blockIdx.y * plane);
     const int m0 = Core::BM * r.tm, n0 = Core::BN * r.tn;
