@@ -27,10 +27,10 @@ __host__ __device__ constexpr int ceil_div(int a, int b) { return (int)(((int64_
 // has its own L2.  This maps block b to a logical tile index so that each XCD
 // walks one contiguous run of the nblocks tiles.
 constexpr int kXcds = 8;
-__device__ __forceinline__ int xcd_contiguous(int b, int nblocks) {
+__host__ __device__ __forceinline__ int xcd_contiguous(int b, int nblocks) {
     const int per = nblocks / kXcds, extra = nblocks % kXcds;
     const int x = b % kXcds, local = b / kXcds;
-    return x * per + min(x, extra) + local;
+    return x * per + (x < extra ? x : extra) + local;
 }
 
 // Four consecutive floats of row `r` starting at column `c` of a row-major

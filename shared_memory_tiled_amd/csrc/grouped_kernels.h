@@ -52,9 +52,10 @@ struct GroupRows {
     int quarter;                       // of the tile; -1: all of it
 };
 
-__device__ __forceinline__ void group_range(const GroupedArgs& a, int g, int* begin, int* end) {
-    *begin = min(max(a.offsets[g], 0), a.rows);
-    *end = min(max(a.offsets[g + 1], *begin), a.rows);
+__host__ __device__ __forceinline__ void group_range(const GroupedArgs& a, int g, int* begin, int* end) {
+    const int from = a.offsets[g], to = a.offsets[g + 1];
+    *begin = from < 0 ? 0 : from < a.rows ? from : a.rows;
+    *end = to < *begin ? *begin : to < a.rows ? to : a.rows;
 }
 
 // Inclusive sum over the wave's lanes: within rows of 16 lanes, then across.
@@ -68,25 +69,51 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
     return v;
 }
 
+// 64 groups in a wave, a lane each: their rows, and the tiles of TILE rows up to
+// and with each.
+template <int TILE>
+struct GroupLanes {
+    int begin, end, incl;
+    __device__ __forceinline__ void load(const GroupedArgs& a, int g0) {
+        const int g = g0 + (threadIdx.x & 63);
+        begin = end = 0;
+        if (g < a.groups) group_range(a, g, &begin, &end);
+        incl = wave_inclusive_sum((end - begin + TILE - 1) / TILE);
+    }
+    __device__ __forceinline__ int sum() const { return __builtin_amdgcn_readlane(incl, 63); }
+    // The first lane whose sum is above `tiles`, which is below sum().
+    __device__ __forceinline__ int past(int tiles) const { return __builtin_ctzll(__builtin_amdgcn_ballot_w64(incl > tiles)); }
+    __device__ __forceinline__ int begin_of(int l) const { return __builtin_amdgcn_readlane(begin, l); }
+    __device__ __forceinline__ int end_of(int l) const { return __builtin_amdgcn_readlane(end, l); }
+    __device__ __forceinline__ int incl_of(int l) const { return __builtin_amdgcn_readlane(incl, l); }
+};
+
 // Block b's tile among the groups' tiles of TILE rows x tiles_n columns, in the
 // order of the groups, within one as grouped_tile orders them, each XCD walking
-// a contiguous run.  Every wave computes it for itself: 64 groups at a time, a
-// lane each.  round > 0: the tiles past a whole number of rounds of `round`, if they
-// are a quarter of one or less, go to four blocks each, which follow the others.
-template <int TILE>
-__device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int b, int tiles_n, int group_m,
-                                                       int round = 0) {
-    const int lane = threadIdx.x & 63;
-    int begin = 0, end = 0, incl = 0, total = 0;
-    const bool one = a.groups <= 64;
+// a contiguous run.  Every wave computes it for itself.  round > 0: the tiles past a
+// whole number of rounds of `round`, if they are a quarter of one or less, go to
+// four blocks each, which follow the others.
+//
+// Offsets that decrease let groups share rows, so that there may be more tiles
+// than an int counts.  64 groups' sum is below 2^30 (the entry points' bound on
+// row tiles, 2^23, for each); the total stops at kMostTiles, beyond any grid.  With
+// that no number here overflows, and whatever the offsets hold, the tile lies in
+// its group and the group in the matrix.
+constexpr int kMostTiles = 1 << 28;
+template <int TILE, typename Lanes = GroupLanes<TILE>>
+__host__ __device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int b, int tiles_n, int group_m,
+                                                                int round = 0) {
+    Lanes lanes;
+    int total = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
-        begin = end = 0;
-        if (g0 + lane < a.groups) group_range(a, g0 + lane, &begin, &end);
-        incl = wave_inclusive_sum((end - begin + TILE - 1) / TILE);
-        total += __builtin_amdgcn_readlane(incl, 63);
+        lanes.load(a, g0);
+        total += lanes.sum();
+        if (total > kMostTiles) total = kMostTiles;
     }
     GroupRows r{0, 0, -1, 0, 0, -1};
-    int blocks = total * tiles_n, rest = 0;
+    const int64_t tiles = (int64_t)total * tiles_n;
+    int blocks = tiles < kMostTiles ? (int)tiles : kMostTiles;
+    int rest = 0;
     if (round > 0) {
         rest = blocks % round;
         if (rest > round / 4) rest = 0;
@@ -104,33 +131,24 @@ __device__ __forceinline__ GroupRows locate_group_tile(const GroupedArgs& a, int
     const int row = logical / tiles_n;                      // row tile if the tiles went row by row
     int before = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
-        if (!one) {
-            begin = end = 0;
-            if (g0 + lane < a.groups) group_range(a, g0 + lane, &begin, &end);
-            incl = wave_inclusive_sum((end - begin + TILE - 1) / TILE);
-        }
-        const int sum = __builtin_amdgcn_readlane(incl, 63);
-        if (row < before + sum) {
-            const uint64_t past = __builtin_amdgcn_ballot_w64(before + incl > row);
-            if (past == 0) return r;
-            const int l = __builtin_ctzll(past);
+        if (a.groups > 64) lanes.load(a, g0);
+        if (row < before + lanes.sum()) {
+            const int l = lanes.past(row - before);
             r.group = g0 + l;
-            r.begin = __builtin_amdgcn_readlane(begin, l);
-            const int rows = __builtin_amdgcn_readlane(end, l) - r.begin;
-            const int tiles_m = (rows + TILE - 1) / TILE;
-            const int first = before + __builtin_amdgcn_readlane(incl, l) - tiles_m;
+            r.begin = lanes.begin_of(l);
+            r.rows = lanes.end_of(l) - r.begin;
+            const int tiles_m = (r.rows + TILE - 1) / TILE;
+            const int first = before + lanes.incl_of(l) - tiles_m;
             const int local = logical - first * tiles_n;
-            const int gsize = min(group_m, tiles_m) * tiles_n;
+            const int gsize = (group_m < tiles_m ? group_m : tiles_m) * tiles_n;
             const int q = local / gsize, first_m = q * group_m;
-            const int gm = min(tiles_m - first_m, group_m);
+            const int gm = tiles_m - first_m < group_m ? tiles_m - first_m : group_m;
             const int in_q = local - q * gsize;
             r.tm = first_m + in_q % gm;
             r.tn = in_q / gm;
-            // offsets that decrease can make more tiles than an int counts
-            if ((unsigned)r.tm < (unsigned)tiles_m && (unsigned)r.tn < (unsigned)tiles_n) r.rows = rows;
             return r;
         }
-        before += sum;
+        before += lanes.sum();
     }
     return r;
 }
