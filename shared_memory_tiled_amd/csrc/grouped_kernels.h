@@ -36,14 +36,15 @@ inline int64_t grouped_row_tiles(int64_t rows, int64_t groups, int64_t tile) {
 namespace {
 
 // Share i of a group's rows among `splits` blocks: whole steps of 32 rows, the
-// last ones cut off or empty.  In 64 bits: the rows reach 2^31 - 1.
+// last ones cut off or empty.  Unsigned: rows reach 2^31 - 1, and no number here
+// passes rows + 32 splits (a division in 64 bits costs 2 to 3 % of a small gradient).
 struct RowShare {
     int first, rows;
 };
 __host__ __device__ __forceinline__ RowShare row_share(int rows, int splits, int i) {
-    const int64_t share = ((int64_t)rows + 32 * splits - 1) / (32 * splits) * 32, skip = i * share;
-    const int first = skip < rows ? (int)skip : rows;
-    return {first, share < rows - first ? (int)share : rows - first};
+    const unsigned all = rows, step = 32u * splits, share = (all + step - 1) / step * 32;
+    const unsigned skip = i * share, first = skip < all ? skip : all;
+    return {(int)first, (int)(share < all - first ? share : all - first)};
 }
 
 struct GroupRows {
