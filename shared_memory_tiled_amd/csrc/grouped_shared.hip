@@ -144,10 +144,12 @@ struct GroupedSharedCore {
             for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // The tile at (m0, n0) of the product; K > 0 if DIRECT.
+    // The tile at (m0, n0) of the product; K > 0 if DIRECT.  turn: the phase to begin
+    // with, modulo their number (the others follow, then those before it), only for
+    // a direct product without k-contiguous factors.
     __device__ static __forceinline__ void run(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
-                                               floatx4 (&acc)[FM][FN]) {
-        if constexpr (DIRECT) run_direct(p, m0, n0, lds, acc);
+                                               floatx4 (&acc)[FM][FN], int turn = 0) {
+        if constexpr (DIRECT) run_direct(p, m0, n0, lds, acc, turn);
         else run_staged(p, m0, n0, lds, acc);
     }
 
@@ -168,7 +170,7 @@ struct GroupedSharedCore {
     }
 
     __device__ static __forceinline__ void run_direct(const Gemm16Args& p, int m0, int n0, unsigned char* lds,
-                                                      floatx4 (&acc)[FM][FN]) {
+                                                      floatx4 (&acc)[FM][FN], int turn) {
         const int lane = threadIdx.x & 63;
         const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         // This wave's copies: CA of A's, CB of those of one 128-wide half of B's
@@ -214,8 +216,11 @@ struct GroupedSharedCore {
         const Fragments fragments(lds, lane, w);
         clear(acc);
         const int phases = ceil_div(p.K, BK);
-        const int turn = KCA ? 0 : (int)((m0 / BM + n0 / BN) % phases);
-        auto turned = [&](int ph) __attribute__((always_inline)) { return KCA ? ph : ph + turn < phases ? ph + turn : ph + turn - phases; };
+        constexpr bool TURNS = !KCA && !KCB && NB == 2;
+        if constexpr (TURNS) turn %= phases;
+        auto turned = [&](int ph) __attribute__((always_inline)) {
+            return !TURNS ? ph : ph + turn < phases ? ph + turn : ph + turn - phases;
+        };
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s)
             if (s < phases) copies(turned(s), s);
@@ -537,6 +542,13 @@ void grouped_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tile
 }
 
 // The same for the gradient: the group's rows in gridDim.y shares.
+// Where 128 x 256 tiles make more than four rounds, neighbouring tiles begin at
+// different rows, so that blocks which start together do not ask for the same
+// lines at once (8192 x 4096 x 4096 over 16 groups 337 us against 378, over 8 270
+// against 285, 16384 x 4096 x 4096 over 16 542 against 583, over 8 480 against 487 to
+// 495; 4096 x 4096 x 4096 over 8 149 against 148).  Fewer rounds lose what they share in
+// the L2s (4096 x 4096 x 4096 in one 110 us against 104, over 4 128 against 124).  The
+// sums' order then depends on the tile's place, the same in every call.
 template <int FMT, int NB, int STAGES, int BLOCKS, bool DIRECT>
 __global__ __launch_bounds__(256, BLOCKS)
 void grouped_grad_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int tiles_m, int tiles_n, int group_m,
@@ -553,7 +565,7 @@ void grouped_grad_shared_kernel(GroupedArgs a, Gemm16Args p, EpilogueArgs e, int
     const int m0 = Core::BM * r.tm, n0 = Core::BN * r.tn;
     if (r.rows == 0) return zero_tile<Core::BM, Core::BN>(e, m0, n0);
     floatx4 acc[Core::FM][Core::FN];
-    Core::run(p, m0, n0, lds, acc);
+    Core::run(p, m0, n0, lds, acc, NB == 2 && gridDim.x > 4 * kRound ? r.tm + r.tn : 0);
     Core::finish_gradient(acc, e, m0, n0, splits > 1, lds);
 }
 
