@@ -96,7 +96,7 @@ extern "C" int64_t gemm_mixed_grouped_workspace_size(int op_b, int format, int64
         return -1;
     if (groups == 0 || M == 0 || N == 0) return 0;
     const GroupedArgs g{(int)groups, offsets, (int)M, stride_b, ld_bias};
-    return grouped_workspace(g, product(M, N, K, A, lda, B, ldb), epilogue_args(format, M, N, nullptr, N, epilogue), op_b);
+    return grouped_workspace(g, product(M, N, K, A, lda, B, ldb), op_b);
 }
 
 extern "C" int gemm_mixed_grouped(int op_b, int format, int64_t groups, int64_t M, int64_t N, int64_t K,
@@ -112,7 +112,7 @@ extern "C" int gemm_mixed_grouped(int op_b, int format, int64_t groups, int64_t 
     const GroupedArgs g{(int)groups, offsets, (int)M, stride_b, ld_bias};
     const Gemm16Args p = product(M, N, K, A, lda, B, ldb);
     const EpilogueArgs e = epilogue_args(format, M, N, C, ldc, epilogue);
-    st = check_workspace(grouped_workspace(g, p, e, op_b), workspace, workspace_bytes);
+    st = check_workspace(grouped_workspace(g, p, op_b), workspace, workspace_bytes);
     if (st != GEMM_F32_OK) return st;
     if ((st = check_device()) != GEMM_F32_OK) return st;
     return finish(launch_grouped(g, p, e, reinterpret_cast<hipStream_t>(stream), format, op_b, workspace));
@@ -126,7 +126,7 @@ extern "C" int64_t gemm_mixed_grouped_grad_workspace_size(int format, int64_t gr
         return -1;
     if (groups == 0 || M == 0 || N == 0) return 0;
     const GroupedArgs g{(int)groups, offsets, (int)rows, M * N, 0};
-    return grouped_grad_workspace(g, product(M, N, 0, A, lda, B, ldb), plain_epilogue(M, N, c_type, nullptr, N));
+    return grouped_grad_workspace(g, product(M, N, 0, A, lda, B, ldb));
 }
 
 extern "C" int gemm_mixed_grouped_grad(int format, int64_t groups, int64_t rows, int64_t M, int64_t N,
@@ -141,7 +141,7 @@ extern "C" int gemm_mixed_grouped_grad(int format, int64_t groups, int64_t rows,
     const GroupedArgs g{(int)groups, offsets, (int)rows, stride_c, 0};
     const Gemm16Args p = product(M, N, 0, A, lda, B, ldb);
     const EpilogueArgs e = plain_epilogue(M, N, c_type, C, ldc);
-    st = check_workspace(grouped_grad_workspace(g, p, e), workspace, workspace_bytes);
+    st = check_workspace(grouped_grad_workspace(g, p), workspace, workspace_bytes);
     if (st != GEMM_F32_OK) return st;
     if ((st = check_device()) != GEMM_F32_OK) return st;
     return finish(launch_grouped_grad(g, p, e, reinterpret_cast<hipStream_t>(stream), format, workspace));

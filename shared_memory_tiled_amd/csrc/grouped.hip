@@ -196,7 +196,7 @@ void grouped_grad_pass_kernel(EpilogueArgs e, int64_t stride_c, int64_t rows, co
 
 }  // namespace
 
-int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs&, int op_b) {
+int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, int op_b) {
     return make_plan(a, p, op_b).bytes;
 }
 
@@ -218,7 +218,7 @@ hipError_t launch_grouped(const GroupedArgs& a, const Gemm16Args& p, const Epilo
     return hipGetLastError();
 }
 
-int64_t grouped_grad_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs&) {
+int64_t grouped_grad_workspace(const GroupedArgs& a, const Gemm16Args& p) {
     return make_grad_plan(a, p).bytes;
 }
 

@@ -205,12 +205,12 @@ hipError_t launch_grouped_grad_shared(const GroupedArgs& a, const Gemm16Args& p,
                                       int format, bool direct, int bn, int splits, int64_t plane);
 
 // p: A, B, N, K and their leading dimensions (M is not used); e: M is not used.
-int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, int op_b);
+int64_t grouped_workspace(const GroupedArgs& a, const Gemm16Args& p, int op_b);
 hipError_t launch_grouped(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s, int format,
                           int op_b, void* workspace);
 // The weights' gradient: p.M x p.N per group from A (rows x M) and B (rows x N), both
 // as stored; e: C, its type and leading dimension.
-int64_t grouped_grad_workspace(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e);
+int64_t grouped_grad_workspace(const GroupedArgs& a, const Gemm16Args& p);
 hipError_t launch_grouped_grad(const GroupedArgs& a, const Gemm16Args& p, const EpilogueArgs& e, hipStream_t s,
                                int format, void* workspace);
 // dZ = dY act'(Z) over the groups' rows, and the groups' column sums (e.bias_grad: groups x N).
