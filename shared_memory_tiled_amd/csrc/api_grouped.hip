@@ -121,8 +121,10 @@ extern "C" int gemm_mixed_grouped(int op_b, int format, int64_t groups, int64_t 
 extern "C" int64_t gemm_mixed_grouped_grad_workspace_size(int format, int64_t groups, int64_t rows, int64_t M,
                                                           int64_t N, const uint16_t* A, int64_t lda, const uint16_t* B,
                                                           int64_t ldb, const int32_t* offsets, int c_type) {
-    if (check_grouped_grad(format, groups, rows, M, N, A, lda, B, ldb, offsets, c_type, at_least_one(N),
-                           at_least_one(M) * at_least_one(N)) != GEMM_F32_OK)
+    // larger sizes are refused before the stride is looked at
+    const int64_t stride_c = M > INT_MAX || N > INT_MAX ? 0 : at_least_one(M) * at_least_one(N);
+    if (check_grouped_grad(format, groups, rows, M, N, A, lda, B, ldb, offsets, c_type, at_least_one(N), stride_c) !=
+        GEMM_F32_OK)
         return -1;
     if (groups == 0 || M == 0 || N == 0) return 0;
     const GroupedArgs g{(int)groups, offsets, (int)rows, M * N, 0};

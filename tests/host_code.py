@@ -8,13 +8,14 @@ import subprocess
 from shared_memory_tiled_amd import build
 
 
-def compile_host(tmp_path, source):
-    """The C functions of ``source`` (HIP, host side only) as a ctypes library."""
+def compile_host(tmp_path, source, overflow="-fwrapv"):
+    """The C functions of ``source`` (HIP, host side only) as a ctypes library;
+    ``overflow``: what a signed one does."""
     src, lib = os.path.join(tmp_path, "host.hip"), os.path.join(tmp_path, "host.so")
     with open(src, "w") as f:
         f.write(source)
-    # wrapping arithmetic: an overflow shows as the wrong place that it gives
-    cmd = [build.HIPCC, "--cuda-host-only", "-O1", "-std=c++17", "-fwrapv", "-fPIC", "-shared", "-w", "-I", build.INCLUDE,
+    # by default it wraps, and shows as the wrong place that it gives
+    cmd = [build.HIPCC, "--cuda-host-only", "-O1", "-std=c++17", overflow, "-fPIC", "-shared", "-w", "-I", build.INCLUDE,
            "-I", build.CSRC, src, "-o", lib]
     subprocess.run(cmd, check=True)
     return ctypes.CDLL(lib)
