@@ -678,7 +678,9 @@ int layer_norm_backward(int type, int64_t rows, int64_t cols, const void *dy, in
  *             counts twice in grad_norm and is refused in place
  *   norm      device pointer to one binary32 value: written by grad_norm and
  *             grad_clip_norm, read by grad_clip (so that the norms of shards
- *             can be joined in between)
+ *             can be joined in between); in both calls of clipping no part of
+ *             an output, in grad_clip_norm of a gradient neither
+ *             (GEMM_F32_ERR_OVERLAP)
  *   max_norm  >= 0, finite;  eps > 0, finite
  *   workspace of grad_norm_workspace_size() bytes, as for gemm_mixed_epilogue
  * Squares are added in binary64 in a fixed order, so that no binary32 value is

@@ -1174,7 +1174,7 @@ def clip_grads(grads, norm, max_norm, eps=1e-6, out=None, stream=None):
     """Multiplies the tensors by min(1, max_norm / (norm + eps)), with ``norm`` on
     the GPU (from ``grad_norm``, or joined from several shards'), in place or
     into the tensors of ``out``; returns those written.  No tensor to be written
-    may overlap another."""
+    may overlap another or ``norm``."""
     g = _TensorList(grads)
     if g.count == 0:
         return [] if out is None else out

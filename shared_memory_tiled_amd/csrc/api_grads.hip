@@ -36,19 +36,21 @@ int check_tensors(int64_t count, const void* const* data, const int64_t* sizes, 
 }
 
 // Blocks write outputs while others still read: an output may be its own
-// input, and overlap nothing else.
+// input, and overlap nothing else.  The norm is one more input, or, where it is
+// written (by a block of the same launch), one more output.
 struct Range {
     uintptr_t begin, end;
     bool output;
 };
-int check_overlaps(const GradList& l) {
-    Range few[512];
+int check_overlaps(const GradList& l, const float* norm, bool written) {
+    Range few[513];
     Range* r = few;
     if (l.count > 256) {
-        r = static_cast<Range*>(malloc(2 * (size_t)l.count * sizeof(Range)));
+        r = static_cast<Range*>(malloc((2 * (size_t)l.count + 1) * sizeof(Range)));
         if (r == nullptr) return GEMM_F32_ERR_TOO_LARGE;
     }
     int64_t n = 0;
+    r[n++] = Range{(uintptr_t)norm, (uintptr_t)norm + sizeof(float), written};
     for (int64_t i = 0; i < l.count; ++i) {
         if (l.size[i] == 0) continue;
         const uintptr_t in = (uintptr_t)l.in[i], out = (uintptr_t)l.out[i];
@@ -68,7 +70,7 @@ int check_overlaps(const GradList& l) {
     return st;
 }
 
-int check_clip(const GradList& l, float max_norm, float eps, const float* norm) {
+int check_clip(const GradList& l, float max_norm, float eps, const float* norm, bool written) {
     int st = check_tensors(l.count, l.in, l.size, l.type);
     if (st != GEMM_F32_OK) return st;
     if (!(max_norm >= 0.0f) || !isfinite(max_norm) || !(eps > 0.0f) || !isfinite(eps)) return GEMM_F32_ERR_INVALID_SCALAR;
@@ -78,7 +80,7 @@ int check_clip(const GradList& l, float max_norm, float eps, const float* norm) 
         if (l.size[i] > 0 && l.out[i] == nullptr) return GEMM_F32_ERR_NULL_PTR;
         if (misaligned_type(l.out[i], l.type[i])) return GEMM_F32_ERR_MISALIGNED;
     }
-    return check_overlaps(l);
+    return check_overlaps(l, norm, written);
 }
 
 }  // namespace
@@ -111,7 +113,7 @@ extern "C" int grad_norm(int64_t count, const void* const* grads, const int64_t*
 extern "C" int grad_clip(int64_t count, const void* const* grads, void* const* out, const int64_t* sizes,
                          const int* types, const float* norm, float max_norm, float eps, void* stream) {
     const GradList l{count, grads, out, sizes, types};
-    int st = check_clip(l, max_norm, eps, norm);
+    int st = check_clip(l, max_norm, eps, norm, false);
     if (st != GEMM_F32_OK) return st;
     if ((st = check_device()) != GEMM_F32_OK) return st;
     return finish(launch_grad_clip(l, nullptr, 0, const_cast<float*>(norm), max_norm, eps,
@@ -122,7 +124,7 @@ extern "C" int grad_clip_norm(int64_t count, const void* const* grads, void* con
                               const int* types, float max_norm, float eps, float* norm, void* workspace,
                               int64_t workspace_bytes, void* stream) {
     const GradList l{count, grads, out, sizes, types};
-    int st = check_clip(l, max_norm, eps, norm);
+    int st = check_clip(l, max_norm, eps, norm, true);
     if (st != GEMM_F32_OK) return st;
     const int64_t partials = grad_partials(count, sizes);
     st = check_workspace(8 * partials, workspace, workspace_bytes);
