@@ -696,7 +696,7 @@ int grad_norm(int64_t count, const void *const *grads, const int64_t *sizes, con
               void *workspace, int64_t workspace_bytes, void *stream);
 int grad_clip(int64_t count, const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
               const float *norm, float max_norm, float eps, void *stream);
-/* Both, in a launch less. */
+/* Both; of up to 128 tensors in a launch less. */
 int grad_clip_norm(int64_t count, const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
                    float max_norm, float eps, float *norm, void *workspace, int64_t workspace_bytes, void *stream);
 
