@@ -552,8 +552,13 @@ int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, int64_t N, in
  * Any number of rows is taken; the weight is expanded once for every 64 of
  * them, so that past a few hundred a 16-bit weight is the better choice.  Sums
  * are binary32, of x (16 + q) with 16 + zero times the sum of x taken off: their
- * error is that of a sum whose terms are up to four times as large.  For the
- * same reason an infinity in A gives NaN.  The workspace, of
+ * error is that of binary32 sums of the terms scale |x| (16 + q + 16 + |zero|),
+ * not of scale |x (q - zero)|, which are 12 (values spread evenly, zero 8) to 24
+ * times smaller in all (normal weights) and may be 0.  A 16-bit product of
+ * the same whole numbers is up to 6 times closer in binary32, which a 16-bit
+ * result does not show.  For the same reason finite bfloat16 x give infinities
+ * or NaN where such a sum over up to 128 k passes binary32's range (not below |x|
+ * of 2^116 with zeros of -15 .. 15), and an infinity in A gives NaN.  The workspace, of
  * gemm_w4_epilogue_workspace_size() bytes, and the rest as for
  * gemm_mixed_epilogue; M at most 65535 * 64, N at most 2^25. */
 int64_t gemm_w4_epilogue_workspace_size(int64_t M, int64_t N, int64_t K);   /* bytes; -1 if invalid */

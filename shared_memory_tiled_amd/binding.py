@@ -708,8 +708,9 @@ def linear_w4(X, Q, scales, zeros=None, group_size=128, bias=None, activation="n
     X is M x K; Q is uint8, N x ceil(K / 2), q[n, k] in the low half of a byte
     for an even k and in the high half for the next one; ``scales`` and ``zeros``
     have X's dtype, N x ceil(K / group_size); without ``zeros`` they are 8.
-    ``group_size`` is 32, 64 or a multiple of 128.  The rest as for
-    ``linear``."""
+    ``group_size`` is 32, 64 or a multiple of 128.  Sums are of x (16 + q), which
+    costs 2 to 3 bits of a float32 result; infinities in X, and bfloat16 values past
+    2^116, may give NaN.  The rest as for ``linear``."""
     device = _device_of(X, Q, scales, zeros, bias, residual, out)
     if _elsewhere(stream, device):
         with _placed(stream, device):

@@ -11,8 +11,13 @@
 //   sum x (q - z) = sum x (16 + q) - (16 + z) sum x,
 // where sum x comes from one more matrix product, with ones, per 32 k: it lands
 // in the registers where the rows' sums are.  The scale multiplies the group's
-// binary32 sum: no weight is rounded.  (16 + q is at most four times |q - 8| on
-// average, so the sums' rounding is 2 bits above an unshifted sum's: 2^-22.)
+// binary32 sum: no weight is rounded.  The sums are rounded relative to |x| (16 + q)
+// and |x| (16 + z), together 12 times |x (q - 8)| for q spread evenly and 24 for
+// normal weights with the largest of 128 at 7: measured against binary64 (16 x
+// 512 x 4096, 128 k to a scale, f32 out, root mean square of the result) 1.1e-7 and
+// 2.0e-7 in bf16, 2.4e-7 and 4.6e-7 in f16, where products of the same whole
+// numbers in 16 bits leave 6e-8 and 8e-8.  A 16-bit result's own rounding is 450
+// times as much and more.  Range: below |x| = 2^116 no sum of 128 passes 2^128.
 //
 // A step is 128 k.  Lane (c = l % 16, g = l / 16) loads 16 bytes, 32 values,
 // of column c from k 32 g on; a 4 x 4 transpose of dwords across the four lane
