@@ -691,8 +691,9 @@ int layer_norm_backward(int type, int64_t rows, int64_t cols, const void *dy, in
  * Squares are added in binary64 in a fixed order, so that no binary32 value is
  * too large or too small to count; the norm is rounded to binary32, the factor
  * is computed from it and rounded to binary32, and every value times the factor
- * is rounded once more to its type.  In place with a factor of 1 nothing is
- * written.  A norm that is infinite gives a factor of 0 (0, and NaN in place of
+ * to binary32 and then to its type.  In place with a factor of 1 nothing is
+ * written.  A norm that is infinite (an infinity among the values, or finite ones
+ * whose norm passes binary32) gives a factor of 0 (0, and NaN in place of
  * infinities), a NaN gives NaN: look at the norm before the update.  Without
  * tensors the norm is +0.  Statuses, streams and graphs as above; a captured
  * graph holds the lists as they were. */

@@ -59,8 +59,8 @@ extern "C" int gemm_mixed_epilogue(int op_a, int op_b, int format, int64_t M, in
 
 namespace {
 
-// Blocks of 16 columns and up to 1024 threads, rows by 64 in the second
-// coordinate.
+// Blocks of 16 columns and up to 512 threads, so that a grid keeps below 2^32
+// work-items with room to spare; rows by 64 in the second coordinate.
 constexpr int64_t kMaxW4Cols = 1 << 25, kMaxW4Rows = 65535 * 64;
 
 int check_w4(int format, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint8_t* Q,

@@ -5,8 +5,9 @@
 // their epilogue (12 to 20 us) pass with the matrix units idle, which is the
 // most of a tile's time where K is short -- a weight's gradient over an expert's
 // few hundred rows above all -- and groups of unequal rows leave their last
-// round badly filled.  Here a block takes a half, a third or a quarter of a CU's
-// LDS and registers, so that one block computes while another starts or stores.
+// round badly filled.  Here two or three blocks share a CU's LDS and registers (of
+// the 64 x 128 tiles through registers four), so that one computes while another
+// starts or stores.
 //
 // K goes in phases of 32 through a ring of LDS stages: while one is computed the
 // copies of the next are in flight, about 96 KB on a CU whatever the tile, which

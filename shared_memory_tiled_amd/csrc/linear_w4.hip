@@ -39,8 +39,10 @@
 // Measured in a graph, 128 k to a scale: 1 x 4096 x 4096 bf16 6.9 us (7.3 with the
 // weight in memory; a launch, one load's latency and a block's sum), 1 x 8192 x
 // 8192 11.6 (15.3, 2.3 TB/s), 16 x 8192 x 8192 16.5, 64 x 4096 x 4096 13.4, 256 x
-// 4096 x 4096 29: past a few rows the expansion bounds it, two operations for every
-// pair of values and 64 rows.
+// 4096 x 4096 26 to 29.  The expansion does not bound it (without it 16 x 8192 x 8192
+// f16 with 64 k to a scale 17.5 for 17.7, 256 x 4096 x 4096 27 for 26): up to 16 rows
+// each wave reads 4 KB of x per step for 2 KB of weight (without x 12.0) and, one to
+// a SIMD, waits for its steps' loads; more rows take a barrier a step.
 #include "epilogue.h"
 #include "linear_w4.h"
 #include "mfma16_common.h"
@@ -130,12 +132,13 @@ struct GroupValues {
 };
 
 // What a wave reads of its J tiles of 16 columns from memory for a step: the
-// weight's bytes.  SLICES: slices of 32 k per scale within a step (1, 2, or 4 for
-// groups of 128 and more), so 4 / SLICES scales.
+// weight's bytes.
 template <int J>
 struct Weights {
     u32x4 q[J];
 };
+// SLICES: slices of 32 k per scale within a step (1, 2, or 4 for groups of 128 and
+// more), so 4 / SLICES scales.
 template <int J, int SLICES>
 struct Columns {
     const uint8_t* q[J];
