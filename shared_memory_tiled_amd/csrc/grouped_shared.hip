@@ -21,12 +21,12 @@
 // (KsplitTile128): one for A's 128 rows or half of one for 64, one or two side
 // by side for B's columns.
 //
-// Measured: 16384 x 4096 x 4096 bf16 over 8 groups 542 to 559 us (1.0 PFLOP/s, the
+// Measured: 16384 x 4096 x 4096 bf16 over 8 groups 542 to 563 us (1.0 PFLOP/s, the
 // matrix units 54 % busy at the clock that their power allows; its tiles are 4 to
 // 4.4 rounds), 4096 x 1024 x 2048 over 64 65 (the weights' read, 4.7 TB/s), 16 x 2048
 // x 4096 over 16 28.5 and the pass over four shares of K 4 (6 TB/s); gradients
-// (alone): 16384 x 4096 x 4096 over 8 480 to 500, 8192 x 2048 x 4096 over 16 147,
-// 4096 x 1024 x 2048 over 64 63.
+// (alone): 16384 x 4096 x 4096 over 8 470 to 480, 8192 x 2048 x 4096 over 16 147 to
+// 150, 4096 x 1024 x 2048 over 64 59.
 #include "epilogue.h"
 #include "grouped_kernels.h"
 #include "mfma16_ksplit128_core.h"
